@@ -97,7 +97,7 @@ dg_status_t dg_rope_apply(const dg_rope_t* r, dg_dtype_t dtype, const dg_heads_t
  *     + head*head_stride + d                                  (elements).
  * Supported: head_dim 64, 128 or 256; page_size 16, 32, 64, 128 or 256;
  * bf16 or fp16; pointers 16-byte aligned, strides multiples of 8 elements.
- * Keys and values may be one tensor (K = V).  Pools are borrowed.
+ * The two pools do not overlap.  They are borrowed.
  * ------------------------------------------------------------------------ */
 typedef struct {
   void* p;

@@ -2,8 +2,12 @@
 layer: router + top-k, token->expert grouping, grouped tcgen05 GEMMs with
 fused GEGLU and weighted combine, dense branch, norm sandwich and residual.
 
+Beside it the attention half: rotary positions, a paged key/value cache with
+its page operations, and attention of a chunk of new tokens over that cache.
+
 The compute runs in ``lib/libdgmoe.so`` (built by :func:`build`) behind the C
-ABI of ``include/dg_moe.h``; this package is its Python binding.
+ABI of ``include/dg_moe.h`` and ``include/dg_attn.h``; this package is its
+Python binding.
 """
 
 from .build import build, LIB  # noqa: F401
@@ -16,4 +20,7 @@ def __getattr__(name):
     if name in ("MoEBlock", "ScMlp", "params_to_device"):
         from . import block
         return getattr(block, name)
+    if name in ("Rope", "KvBatch", "KvCache", "KvFork", "KvPager", "PagedAttention"):
+        from . import attention
+        return getattr(attention, name)
     raise AttributeError(name)

@@ -1,0 +1,1162 @@
+// Attention of new tokens over a paged key/value cache on sm_103a.
+//
+// A work item is one key/value head and a tile of query rows of one sequence:
+// the G = n_q_heads / n_kv_heads query heads that share the key/value head
+// are packed with their tokens (row = token * G + head of the group), so that
+// a single token still fills G rows of the 128-row MMA and every key is read
+// once for all of them.  Per 128-key tile j of the item
+//   S = Q K_j^T                    tcgen05.mma, operands in shared memory
+//   m' = max(m, rowmax(S)),  P = 2^(S scale log2 e - m')
+//   O += P V_j,  l += rowsum(P)    tcgen05.mma, P from tensor memory
+// with O, l and the statistics in fp32 (running softmax: one pass over the
+// keys).  P enters the product rounded to the element type, as the operand of
+// a 16-bit MMA must; l sums it before the rounding.
+//
+// The reference m of a row is only moved when the true maximum has grown past
+// it by more than 2^8 (P then stays below 2^8, harmless in fp32 sums and in
+// bf16 or fp16): O, which lives in tensor memory, is rescaled a few times a
+// row instead of once a tile.
+//
+// The items of a call are cut into units of one key tile, and the units dealt
+// evenly to one CTA an SM: a CTA takes a contiguous range, so long and short
+// sequences, many and few tokens balance alike.  An item that crosses a range
+// boundary leaves fp32 partial results in the workspace, joined in a fixed
+// order by k_attn_join.
+//
+// Warps 0-3 and 4-7: softmax; 8: TMA producer; 9: MMA issuer and TMEM owner.
+// NQ = 2 (many rows, head size up to 128): two 128-row tiles an item, one a
+// warpgroup, which take turns on the tensor core.  NQ = 1 (few rows, or head
+// size 256, whose accumulator takes half of the TMEM): one tile, its key
+// tiles double-buffered, its columns halved between the warpgroups.
+#include <math.h>
+#include <stdio.h>
+
+#include <new>
+
+#include <cuda_fp16.h>
+
+#include "../../include/dg_attn.h"
+#include "dg_attn_host.h"
+#include "dg_common.cuh"
+#include "dg_tmem.cuh"
+
+using namespace dg;
+using namespace dg::host;
+
+namespace {
+
+constexpr int kMaxCtas = 160;
+constexpr int kThreads = 320;
+constexpr int kRows = 128;  // rows of a query tile
+constexpr int kKeys = 128;  // keys of a key tile
+
+// Sites of the device status word.
+enum : unsigned int {
+  kSiteAttnLoad = 32, kSiteAttnMma = 33, kSiteAttnSoftmax = 34, kSiteAttnDrain = 35,
+  kSiteAttnPage = 36, kSiteAttnLen = 37,
+};
+
+// An item that several CTAs worked on, written by the CTA that begins it.
+struct JoinRec {
+  int parts;  // 0: none
+  int head, tok0, ntok;
+};
+
+struct AttnParams {
+  CUtensorMap qm, km, vm;
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* cu;
+  int64_t table_stride;
+  int n_seqs, cap, n_tokens, n_pages, page_shift;
+  int kv_heads, group, step;  // step: tokens of a 128-row tile
+  int q_box;                  // tokens of a query box
+  int left, right;
+  float scale2;  // scale log2 e
+  uint16_t* out;
+  int64_t o_tok, o_head;
+  float* lse;
+  float* part;   // [2 ctas][NQ * 128][D]
+  float2* ml;    // [2 ctas][NQ * 128] (m, l)
+  JoinRec* rec;  // [ctas]
+  DevStatus* status;
+};
+
+template <int D, int NQ>
+struct Cfg {
+  // ring stage: 128 keys x D up to 128; at 256 a half of a key tile (128 keys
+  // x 128) or of a value tile (64 keys x 256)
+  static constexpr int kParts = D == 256 ? 2 : 1;
+  static constexpr int kStageBytes = kKeys * D * 2 / kParts;
+  static constexpr int kStages = 160 * 1024 / kStageBytes;
+  static constexpr int kChunks = D / 64;  // 128-byte columns of a row
+  static constexpr int kQTile = kRows * D * 2;
+  static constexpr int kQBufs = (NQ == 1 && D <= 128) ? 2 : 1;
+  static constexpr size_t kSmem =
+      1024 + (size_t)kStages * kStageBytes + (size_t)kQBufs * NQ * kQTile;
+  // tensor memory columns
+  static constexpr uint32_t kO = 256;
+};
+
+struct Seq {
+  int n0, n, kv;
+};
+
+__device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
+  const int a = __ldg(p.cu + b), e = __ldg(p.cu + b + 1), kv = __ldg(p.lens + b);
+  Seq s;
+  s.n0 = min(max(a, 0), p.n_tokens);
+  s.n = max(min(e, p.n_tokens) - s.n0, 0);
+  s.kv = min(max(kv, 0), p.cap);
+  return s;
+}
+
+// Keys [x, y) that the tokens [first, first + n) of a sequence see together.
+__device__ __forceinline__ int2 key_range(const AttnParams& p, const Seq& s, int first, int n) {
+  const int pos = s.kv - s.n + first;
+  const int lo = p.left < 0 ? 0 : max(0, pos - p.left);
+  const int hi = p.right < 0 ? s.kv : min(s.kv, pos + n + p.right);
+  return make_int2(lo, max(hi, 0));
+}
+
+// Key tiles [x, x + y) of item tile t.
+template <int NQ>
+__device__ __forceinline__ int2 tile_range(const AttnParams& p, const Seq& s, int t) {
+  const int first = t * NQ * p.step;
+  const int2 k = key_range(p, s, first, min(NQ * p.step, s.n - first));
+  if (k.x >= k.y) return make_int2(0, 0);
+  const int a = k.x / kKeys;
+  return make_int2(a, (k.y + kKeys - 1) / kKeys - a);
+}
+
+// The part of an item that a CTA works on.
+struct Seg {
+  int head, tok0, ntok;  // key/value head; first row of q / out; tokens
+  int pos;               // position of the first token
+  int b, kv, klo, khi;   // sequence, its length, keys that the item sees
+  int kt0, n;            // key tiles
+  bool first, last;      // holds the item's first / last tile
+  long long end;         // unit after the item's last one
+};
+
+// Walk over the segments of a range of units; the same in every role.
+template <int NQ>
+struct Walk {
+  int h, b, t, skip;
+  long long u, end;
+  Seq s;
+  __device__ __forceinline__ bool next(const AttnParams& p, Seg& g) {
+    if (u >= end) return false;
+    const int first = t * NQ * p.step;
+    const int2 tr = tile_range<NQ>(p, s, t);
+    const int cost = max(tr.y, 1);
+    const int take = (int)min((long long)(cost - skip), end - u);
+    g.head = h;
+    g.b = b;
+    g.tok0 = s.n0 + first;
+    g.ntok = min(NQ * p.step, s.n - first);
+    g.pos = s.kv - s.n + first;
+    const int2 k = key_range(p, s, first, g.ntok);
+    g.kv = s.kv;
+    g.klo = k.x;
+    g.khi = k.y;
+    g.kt0 = tr.x + skip;
+    g.n = tr.y ? take : 0;
+    g.first = skip == 0;
+    g.last = skip + take == cost;
+    g.end = u - skip + cost;
+    u += take;
+    skip = 0;
+    if (u < end) {
+      ++t;
+      if (t * NQ * p.step >= s.n) {
+        t = 0;
+        do {
+          if (++b == p.n_seqs) {
+            b = 0;
+            ++h;
+          }
+          s = load_seq(p, b);
+        } while (s.n == 0);
+      }
+    }
+    return true;
+  }
+};
+
+struct Start {
+  int h, b, t, skip;
+  long long u, end, total;
+  int ctas;
+};
+
+__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, uint32_t dst,
+                                            int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(const CUtensorMap* map, uint64_t* bar, uint32_t dst,
+                                            int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], 16-bit inputs, fp32 accumulate.
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Operand whose rows are 64-element columns of N (128 bytes a row, one row a
+// k): the leading offset steps from one 64-element column to the next, the
+// stride offset from 8 k to the next 8.
+__device__ __forceinline__ uint64_t sw128_nmajor_desc(uint32_t smem_addr, uint32_t chunk_bytes) {
+  return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | ((uint64_t)(chunk_bytes >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+template <bool FP16>
+__device__ __forceinline__ constexpr uint32_t idesc_16(int M, int N, bool b_nmajor) {
+  const uint32_t t = FP16 ? 0u : 1u;
+  return (1u << 4) | (t << 7) | (t << 10) | ((b_nmajor ? 1u : 0u) << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t r;
+  if (FP16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Barrier of the two warps that share 32 rows (NQ = 1), with an OR of `stop`.
+__device__ __forceinline__ bool pair_barrier(int id, bool stop) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "barrier.cta.red.or.pred p, %2, 64, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)stop), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  while (true) {
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
+  }
+}
+
+// Ring position, inside its segment of n tiles, of the first stage of key
+// tile j and of value tile j (order K0, K1, V0, K2, V1, ..., V(n-1)).
+template <int PARTS>
+__device__ __forceinline__ int k_stage(int j) {
+  return j == 0 ? 0 : PARTS * (2 * j - 1);
+}
+template <int PARTS>
+__device__ __forceinline__ int v_stage(int j, int n) {
+  return j + 1 < n ? PARTS * (2 * j + 2) : PARTS * (2 * n - 1);
+}
+
+// Where this CTA's range of units begins.  Sequence costs go through `cost`
+// (shared memory, n_seqs entries).  All threads; ends with a barrier.
+template <int NQ>
+__device__ __forceinline__ void find_start(const AttnParams& p, long long* cost, Start* out) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < 256) {
+    int lps = 32;  // lanes a sequence
+    while (lps > 1 && lps * p.n_seqs > 256) lps >>= 1;
+    const int per = 256 / lps, sub = tid % lps;
+    for (int s0 = 0; s0 < p.n_seqs; s0 += per) {
+      const int b = s0 + tid / lps;
+      long long c = 0;
+      if (b < p.n_seqs) {
+        const Seq s = load_seq(p, b);
+        for (int t = sub; t * NQ * p.step < s.n; t += lps) c += max(tile_range<NQ>(p, s, t).y, 1);
+        if (blockIdx.x == 0 && sub == 0) {
+          const int a = __ldg(p.cu + b), e = __ldg(p.cu + b + 1), kv = __ldg(p.lens + b);
+          if (a < 0 || e < a || e > p.n_tokens || kv < 0 || kv > p.cap)
+            report(p.status, kDevBounds, kSiteAttnLen, (unsigned)b, (unsigned)kv);
+        }
+      }
+      for (int o = lps >> 1; o; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+      if (b < p.n_seqs && sub == 0) cost[b] = c;
+    }
+  }
+  __syncthreads();
+  if (tid < 32) {
+    const int ch = (p.n_seqs + 31) / 32;
+    const int b0 = min(lane * ch, p.n_seqs), b1 = min(b0 + ch, p.n_seqs);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) sum += cost[b];
+    long long incl = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const long long one = __shfl_sync(0xffffffffu, incl, 31);
+    const long long total = one * p.kv_heads;
+    const int ctas = (int)min((long long)gridDim.x, total);
+    const int c = blockIdx.x;
+    long long u0 = 0, u1 = 0;
+    if (c < ctas) {
+      u0 = (long long)c * total / ctas;
+      u1 = (long long)(c + 1) * total / ctas;
+    }
+    int h = 0, b = 0, t = 0, skip = 0;
+    if (u0 < u1) {
+      h = (int)(u0 / one);
+      long long r = u0 - h * one;
+      const bool mine = r >= incl - sum && r < incl;
+      const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+      b = b0;
+      if (mine) {
+        r -= incl - sum;
+        while (r >= cost[b]) r -= cost[b++];
+      }
+      b = __shfl_sync(0xffffffffu, b, src);
+      r = __shfl_sync(0xffffffffu, r, src);
+      const Seq s = load_seq(p, b);
+      for (int base = 0;; base += 32) {
+        const int tt = base + lane;
+        int cc = 0;
+        if (tt * NQ * p.step < s.n) cc = max(tile_range<NQ>(p, s, tt).y, 1);
+        long long in = cc;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, in, o);
+          if (lane >= o) in += v;
+        }
+        const long long all = __shfl_sync(0xffffffffu, in, 31);
+        if (r < all) {
+          const unsigned hit = __ballot_sync(0xffffffffu, r < in);
+          const int l = __ffs(hit) - 1;
+          t = base + l;
+          skip = (int)(r - __shfl_sync(0xffffffffu, in - cc, l));
+          break;
+        }
+        r -= all;
+        if (base * NQ * p.step >= s.n) {  // cannot happen: r lies in this sequence
+          u1 = u0;
+          break;
+        }
+      }
+    }
+    if (lane == 0) *out = Start{h, b, t, skip, u0, u1, total, ctas};
+  }
+  fence_proxy_async_smem();  // `cost` lies where copies will land
+  __syncthreads();
+}
+
+template <int D, int NQ, bool FP16>
+__global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constant__ AttnParams p) {
+  using C = Cfg<D, NQ>;
+  constexpr int NS = C::kStages, PARTS = C::kParts;
+  constexpr int NC = NQ == 2 ? 128 : 64;        // score columns a softmax thread
+  constexpr int OC = NQ == 2 ? D : D / 2;       // output columns a softmax thread
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t qbase = ring + NS * C::kStageBytes;
+  __shared__ uint64_t full[NS], empty[NS];
+  __shared__ uint64_t q_full[C::kQBufs], q_empty[C::kQBufs];
+  __shared__ uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2], drain;
+  __shared__ uint32_t tmem_holder;
+  __shared__ int abort_word;
+  __shared__ Start start;
+  __shared__ float xch[2][NQ == 1 ? 256 : 1];
+  volatile int* abort_flag = &abort_word;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_trigger();
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < C::kQBufs; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], NQ == 2 ? 4 : 8);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&o_empty[i], NQ == 2 ? 4 : 8);
+    }
+    mbar_init(&drain, 1);
+    abort_word = 0;
+    fence_mbar_init();
+  }
+  if (tid == 8 * 32) {
+    tma_prefetch_map(&p.qm);
+    tma_prefetch_map(&p.km);
+    tma_prefetch_map(&p.vm);
+  }
+  if (warp == 9) {
+    tmem_alloc(&tmem_holder, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  tc_fence_before();
+  find_start<NQ>(p, reinterpret_cast<long long*>(smem), &start);
+  tc_fence_after();
+  const uint32_t tmem = tmem_holder;
+  Walk<NQ> w;
+  w.h = start.h;
+  w.b = start.b;
+  w.t = start.t;
+  w.skip = start.skip;
+  w.u = start.u;
+  w.end = start.end;
+  if (w.u < w.end) w.s = load_seq(p, w.b);
+  Seg g;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ producer
+    const int ps = 1 << p.page_shift;
+    const int kbox = min(ps, kKeys), kpieces = kKeys / kbox;
+    constexpr int VKEYS = kKeys / PARTS;             // keys of a value stage
+    constexpr int KCH = D == 256 ? 2 : C::kChunks;   // columns of a key stage
+    const int vbox = min(ps, VKEYS), vpieces = VKEYS / vbox;
+    int pos = 0, qn = 0;
+    bool ok = true;
+    uint32_t armed = 0, armed_par = 0, q_armed = 0, q_par = 0;
+    auto acquire = [&]() -> int {
+      const int st = pos % NS;
+      if (!mbar_wait(&empty[st], ((uint32_t)(pos / NS) & 1u) ^ 1u, abort_flag)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      armed |= 1u << st;
+      armed_par = (armed_par & ~(1u << st)) | (((uint32_t)(pos / NS) & 1u) << st);
+      ++pos;
+      return st;
+    };
+    while (ok && w.next(p, g)) {
+      if (g.n == 0) continue;
+      // page ids of 32 consecutive pieces of kbox keys, one a lane
+      int pid_base = -1, pid = 0;
+      auto fetch = [&](int piece) {
+        const int base = piece & ~31;
+        if (base == pid_base) return;
+        pid_base = base;
+        const int key = (base + lane) * kbox;
+        pid = p.n_pages;  // out of range: the copy reads zeros
+        if (key < g.khi) {
+          const int pg = (int)((unsigned)key >> p.page_shift);
+          // a page that ends before the first key any query sees may be gone
+          if (((pg + 1) << p.page_shift) > g.klo) {
+            const int id = __ldg(p.table + (int64_t)g.b * p.table_stride + pg);
+            if ((unsigned)id < (unsigned)p.n_pages)
+              pid = id;
+            else
+              report(p.status, kDevBounds, kSiteAttnPage, (unsigned)g.b, (unsigned)id);
+          }
+        }
+      };
+      fetch(g.kt0 * kpieces);
+      {
+        const int qb = qn % C::kQBufs;
+        if (!mbar_wait(&q_empty[qb], ((uint32_t)(qn / C::kQBufs) & 1u) ^ 1u, abort_flag)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full[qb], NQ * C::kChunks * 128 * p.group * p.q_box);
+          for (int i = 0; i < NQ; ++i)
+            for (int c = 0; c < C::kChunks; ++c)
+              tma_load_3d(&p.qm, &q_full[qb],
+                          qbase + (qb * NQ + i) * C::kQTile + c * (kRows * 128), 64 * c,
+                          g.head * p.group, g.tok0 + i * p.step);
+        }
+        q_armed |= 1u << qb;
+        q_par = (q_par & ~(1u << qb)) | (((uint32_t)(qn / C::kQBufs) & 1u) << qb);
+        ++qn;
+      }
+      for (int j = 0; j <= g.n && ok; ++j) {
+        if (j < g.n) {  // keys of tile j
+          const int kt = g.kt0 + j;
+          fetch(kt * kpieces);
+          const int live = min(kpieces, (g.khi - kt * kKeys + kbox - 1) / kbox);
+#pragma unroll
+          for (int h = 0; h < PARTS; ++h) {
+            const int st = acquire();
+            if (!ok) break;
+            const int i = lane % kpieces, c = lane / kpieces;
+            const int id = __shfl_sync(0xffffffffu, pid, (kt * kpieces + i) & 31);
+            if (lane == 0) mbar_arrive_expect_tx(&full[st], live * kbox * 128 * KCH);
+            __syncwarp();
+            if (i < live && c < KCH)
+              tma_load_4d(&p.km, &full[st],
+                          ring + st * C::kStageBytes + c * (kKeys * 128) + i * kbox * 128,
+                          (h * KCH + c) * 64, g.head, (kt * kKeys + i * kbox) & (ps - 1), id);
+          }
+        }
+        if (j > 0 && ok) {  // values of tile j - 1
+          const int kt = g.kt0 + j - 1;
+          fetch(kt * kpieces);
+#pragma unroll
+          for (int h = 0; h < PARTS; ++h) {
+            const int st = acquire();
+            if (!ok) break;
+            const int key0 = kt * kKeys + h * VKEYS;
+            const int live = max(0, min(vpieces, (g.khi - key0 + vbox - 1) / vbox));
+            if (lane == 0) mbar_arrive_expect_tx(&full[st], live * vbox * 128 * C::kChunks);
+            __syncwarp();
+            const int i = lane % vpieces, c = lane / vpieces, key = key0 + i * vbox;
+            const int id = __shfl_sync(0xffffffffu, pid, (key / kbox) & 31);
+            if (i < live && c < C::kChunks)
+              tma_load_4d(&p.vm, &full[st],
+                          ring + st * C::kStageBytes + c * (VKEYS * 128) + i * vbox * 128, 64 * c,
+                          g.head, key & (ps - 1), id);
+          }
+        }
+      }
+    }
+    if (!ok) {
+      if (lane == 0) report(p.status, kDevTimeout, kSiteAttnLoad, (unsigned)pos, 0u);
+      *abort_flag = 1;
+    }
+    // no copy may still be landing in shared memory when the CTA exits
+    if (lane == 0) {
+      for (int i = 0; i < NS; ++i)
+        if ((armed >> i) & 1u)
+          if (!wait_drain(&full[i], (armed_par >> i) & 1u))
+            report(p.status, kDevTimeout, kSiteAttnDrain, (unsigned)i, 0u);
+      for (int i = 0; i < C::kQBufs; ++i)
+        if ((q_armed >> i) & 1u)
+          if (!wait_drain(&q_full[i], (q_par >> i) & 1u))
+            report(p.status, kDevTimeout, kSiteAttnDrain, 64u + i, 0u);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      int pos = 0, qn = 0, at = 0, segs = 0;  // ring position, query tiles, key tiles, segments
+      bool ok = true, issued = false;
+      auto need = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && !mbar_wait(bar, parity, abort_flag)) {
+          report(p.status, kDevTimeout, kSiteAttnMma, (unsigned)at, smem_u32(bar));
+          *abort_flag = 1;
+          ok = false;
+        }
+        return ok;
+      };
+      while (ok && w.next(p, g)) {
+        if (g.n == 0) continue;
+        const int qb = qn % C::kQBufs;
+        if (!need(&q_full[qb], (uint32_t)(qn / C::kQBufs) & 1u)) break;
+        ++qn;
+        // 16-key steps of tile j that some row sees
+        auto steps = [&](int j) {
+          return (min(kKeys, g.khi - (g.kt0 + j) * kKeys) + 15) >> 4;
+        };
+        auto scores = [&](int i, int j) {  // S_i(j) = Q_i K_j^T
+          const int rp = pos + k_stage<PARTS>(j);
+          const uint32_t d = tmem + (NQ == 2 ? i : ((at + j) & 1)) * 128u;
+          const uint32_t idesc = idesc_16<FP16>(128, 16 * steps(j), false);
+#pragma unroll
+          for (int h = 0; h < PARTS; ++h) {
+            const int st = (rp + h) % NS;
+            if (i == 0 && !need(&full[st], (uint32_t)((rp + h) / NS) & 1u)) return;
+            tc_fence_after();
+            constexpr int CH = C::kChunks / PARTS;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+              const uint32_t a = qbase + (qb * NQ + i) * C::kQTile + (h * CH + c) * (kRows * 128);
+              const uint32_t b = ring + st * C::kStageBytes + c * (kKeys * 128);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_bf16(d, sw128_kmajor_desc(a + 32 * k), sw128_kmajor_desc(b + 32 * k), idesc,
+                          (h | c | k) ? 1u : 0u);
+            }
+            if (i == NQ - 1) umma_commit(&empty[st]);
+          }
+          issued = true;
+          umma_commit(&s_full[NQ == 2 ? i : ((at + j) & 1)]);
+          if (i == NQ - 1 && j == g.n - 1) umma_commit(&q_empty[qb]);
+        };
+        auto values = [&](int i, int j) {  // O_i += P_i(j) V_j
+          const int buf = NQ == 2 ? i : ((at + j) & 1);
+          const uint32_t use = NQ == 2 ? (uint32_t)(at + j) : (uint32_t)(at + j) >> 1;
+          if (!need(&p_full[buf], use & 1u)) return;
+          if (j == 0 && !need(&o_empty[i], ((uint32_t)segs & 1u) ^ 1u)) return;
+          const int rp = pos + v_stage<PARTS>(j, g.n);
+          const uint32_t d = tmem + C::kO + i * D;
+          const uint32_t a = tmem + buf * 128u;
+          const uint32_t idesc = idesc_16<FP16>(128, D, true);
+          const int ks = steps(j);
+          constexpr int SK = 8 / PARTS;  // k steps a stage
+#pragma unroll
+          for (int h = 0; h < PARTS; ++h) {
+            const int st = (rp + h) % NS;
+            if (i == 0 && !need(&full[st], (uint32_t)((rp + h) / NS) & 1u)) return;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < SK; ++k)
+              if (h * SK + k < ks)
+                umma_ts(d, a + 8 * (h * SK + k),
+                        sw128_nmajor_desc(ring + st * C::kStageBytes + k * 2048, SK * 2048), idesc,
+                        (j | h | k) ? 1u : 0u);
+            if (i == NQ - 1) umma_commit(&empty[st]);
+          }
+          umma_commit(&pv_done[i]);
+        };
+        if (NQ == 2) {
+          scores(0, 0);
+          if (ok) scores(1, 0);
+          for (int j = 0; j < g.n && ok; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (ok) values(i, j);
+              if (ok && j + 1 < g.n) scores(i, j + 1);
+            }
+        } else {
+          scores(0, 0);
+          if (ok && g.n > 1) scores(0, 1);
+          for (int j = 0; j < g.n && ok; ++j) {
+            values(0, j);
+            if (ok && j + 2 < g.n) scores(0, j + 2);
+          }
+        }
+        pos += 2 * PARTS * g.n;
+        at += g.n;
+        ++segs;
+      }
+      // every MMA issued here must have completed before TMEM is released
+      if (issued) {
+        umma_commit(&drain);
+        if (!wait_drain(&drain, 0u)) report(p.status, kDevTimeout, kSiteAttnDrain, 99u, 0u);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int wg = warp >> 2, quarter = warp & 3;
+    const int i = NQ == 2 ? wg : 0;        // tile of the item
+    const int c0 = NQ == 2 ? 0 : wg * NC;  // first score column
+    const int o0 = NQ == 2 ? 0 : wg * OC;  // first output column
+    const int row = quarter * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+    const int tok = row / p.group, gh = row - tok * p.group;
+    int pos = 0, at = 0;  // ring position, key tiles
+    int xn = 0;           // exchanges (NQ = 1)
+    bool ok = true;
+    JoinRec rec{0, 0, 0, 0};
+    while (ok && w.next(p, g)) {
+      const bool row_live = tok < p.step && tok + i * p.step < g.ntok;
+      const bool live = __any_sync(0xffffffffu, row_live);
+      int lo = 0, hi = 0;
+      if (row_live) {
+        const int qp = g.pos + i * p.step + tok;
+        lo = p.left < 0 ? 0 : max(0, qp - p.left);
+        hi = p.right < 0 ? g.kv : min(g.kv, qp + p.right + 1);
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < g.n; ++j) {
+        const int buf = NQ == 2 ? i : ((at + j) & 1);
+        const uint32_t use = NQ == 2 ? (uint32_t)(at + j) : (uint32_t)(at + j) >> 1;
+        const int key0 = (g.kt0 + j) * kKeys;
+        if (!mbar_wait(&s_full[buf], use & 1u, abort_flag)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok && (NQ == 2 || !live)) break;  // a live pair leaves at its barrier
+        tc_fence_after();
+        if (live) {
+          const uint32_t ts = tl + buf * 128u;
+          float s[NC];
+          if constexpr (NC == 128) {
+            tmem_load64(ts, *reinterpret_cast<float(*)[64]>(s));
+            tmem_load64(ts + 64, *reinterpret_cast<float(*)[64]>(s + 64));
+          } else {
+            tmem_load64(ts + c0, s);
+          }
+          const int rl = lo - key0 - c0, rh = hi - key0 - c0;
+          if (!__all_sync(0xffffffffu, rl <= 0 && rh >= NC)) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              if (c < rl || c >= rh) s[c] = -INFINITY;
+          }
+          float mx4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int c = 4; c < NC; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], s[c]);
+          float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          if (NQ == 1) {
+            float* x = xch[xn & 1];
+            x[wg * 128 + row] = mx;
+            // also orders the partner's loads of S before this warp's P
+            tc_fence_before();
+            if (pair_barrier(1 + quarter, !ok)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            mx = fmaxf(mx, x[(wg ^ 1) * 128 + row]);
+            ++xn;
+          }
+          const float mt = mx * p.scale2;
+          float fac = 1.f;
+          if (mt > m) {
+            if (m == -INFINITY) {
+              m = mt;
+            } else if (mt > m + 8.f) {
+              fac = exp2_fast(m - mt);
+              m = mt;
+              l *= fac;
+            }
+          }
+          if (j > 0 && __any_sync(0xffffffffu, fac != 1.f)) {
+            // O holds the tiles before this one once their product is done
+            bool here = mbar_wait(&pv_done[i], (uint32_t)(at + j - 1) & 1u, abort_flag);
+            here = __all_sync(0xffffffffu, here);
+            if (!here) {
+              ok = false;
+              if (NQ == 2) break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < OC; c += 32) {
+              float o[32];
+              uint32_t r[32];
+              tmem_load32(tl + C::kO + i * D + o0 + c, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(o[e] * fac);
+              tmem_store32(tl + C::kO + i * D + o0 + c, r);
+            }
+          }
+          const float mr = m == -INFINITY ? 0.f : m;
+          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t pk[NC / 2];
+#pragma unroll
+          for (int c = 0; c < NC; c += 2) {
+            const float a = exp2_fast(fmaf(s[c], p.scale2, -mr));
+            const float b = exp2_fast(fmaf(s[c + 1], p.scale2, -mr));
+            l4[c & 2] += a;
+            l4[(c & 2) + 1] += b;
+            pk[c / 2] = pack16<FP16>(a, b);
+          }
+          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          if constexpr (NC == 128) {
+            tmem_store32(ts, *reinterpret_cast<uint32_t(*)[32]>(pk));
+            tmem_store32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
+          } else {
+            tmem_store32(ts + c0 / 2, pk);
+          }
+          tmem_store_wait();
+        }
+        // The last tile of an item may hold keys that no row sees, and rows
+        // that were never written: their V is zeroed up to the 16-key step,
+        // so that 0 * V cannot bring in a NaN.
+        const int vis = g.khi - key0;
+        if (vis < kKeys && (vis & 15) && i == 0) {
+          const int rp = pos + v_stage<PARTS>(j, g.n);
+          constexpr int VK = kKeys / PARTS;
+          const int h = vis / VK;  // the stage that holds the step
+          const int st = (rp + h) % NS;
+          if (!mbar_wait(&full[st], (uint32_t)((rp + h) / NS) & 1u, abort_flag)) ok = false;
+          const int r0 = vis - h * VK, r1 = (r0 + 15) & ~15;
+          constexpr int NT = NQ == 2 ? 128 : 256;
+          for (int x = (tid & (NT - 1)); x < (r1 - r0) * C::kChunks * 8; x += NT) {
+            const int u = x & 7, r = r0 + (x >> 3) / C::kChunks, c = (x >> 3) % C::kChunks;
+            *reinterpret_cast<uint4*>(smem + st * C::kStageBytes + c * (VK * 128) + r * 128 +
+                                      u * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[buf]);
+      }
+      // ------------------------------------------------- end of the segment
+      if (g.n) {
+        if (ok && !mbar_wait(&pv_done[i], (uint32_t)(at + g.n - 1) & 1u, abort_flag)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (NQ == 2 && !ok) break;
+        tc_fence_after();
+      }
+      if (live) {
+        if (NQ == 1 && g.n) {
+          float* x = xch[xn & 1];
+          x[wg * 128 + row] = l;
+          if (pair_barrier(1 + quarter, !ok)) {
+            ok = false;
+            break;
+          }
+          l += x[(wg ^ 1) * 128 + row];
+          ++xn;
+        }
+        const bool whole = g.first && g.last;
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        const int trow = g.tok0 + i * p.step + tok;
+        const int head = g.head * p.group + gh;
+        const int slot = 2 * blockIdx.x + (g.first ? 1 : 0);
+        const size_t prow = (size_t)slot * (NQ * kRows) + i * kRows + row;
+#pragma unroll
+        for (int c = 0; c < OC; c += 32) {
+          float o[32];
+          if (g.n) {
+            __syncwarp();
+            tmem_load32(tl + C::kO + i * D + o0 + c, o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
+          if (!row_live) continue;
+          if (whole) {
+            uint16_t* dst = p.out + trow * p.o_tok + head * p.o_head + o0 + c;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint4 v;
+              // nothing seen: O may hold what was there before
+              const bool z = l == 0.f;
+              v.x = z ? 0u : pack16<FP16>(o[e] * inv, o[e + 1] * inv);
+              v.y = z ? 0u : pack16<FP16>(o[e + 2] * inv, o[e + 3] * inv);
+              v.z = z ? 0u : pack16<FP16>(o[e + 4] * inv, o[e + 5] * inv);
+              v.w = z ? 0u : pack16<FP16>(o[e + 6] * inv, o[e + 7] * inv);
+              *reinterpret_cast<uint4*>(dst + e) = v;
+            }
+          } else {
+            float* dst = p.part + prow * D + o0 + c;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+        if (row_live && (NQ == 2 || wg == 0)) {
+          if (!whole)
+            p.ml[prow] = make_float2(m, l);
+          else if (p.lse)
+            p.lse[(size_t)trow * (p.kv_heads * p.group) + head] =
+                l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+        }
+      }
+      if (g.first && !g.last) {
+        // unit range of CTA c: [c total / ctas, (c + 1) total / ctas)
+        rec.parts = (int)((g.end * start.ctas - 1) / start.total) - (int)blockIdx.x + 1;
+        rec.head = g.head;
+        rec.tok0 = g.tok0;
+        rec.ntok = g.ntok;
+      }
+      if (g.n) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_empty[i]);
+        pos += 2 * PARTS * g.n;
+        at += g.n;
+      }
+    }
+    if (!ok) {
+      if (lane == 0) report(p.status, kDevTimeout, kSiteAttnSoftmax, (unsigned)at, (unsigned)warp);
+      *abort_flag = 1;
+    }
+    if (tid == 0) p.rec[blockIdx.x] = ok ? rec : JoinRec{0, 0, 0, 0};
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Join the parts of the item that CTA blockIdx.x began: with m the largest
+// reference, o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i, parts in order.
+// A warp takes a row.
+template <int D, int NQ, bool FP16>
+__global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnParams p) {
+  pdl_trigger();
+  pdl_wait();
+  const JoinRec rec = p.rec[blockIdx.x];
+  if (rec.parts == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int E = D / 32;
+  for (int vr = warp + 8 * (int)blockIdx.y; vr < rec.ntok * p.group; vr += 8 * (int)gridDim.y) {
+    const int tok = vr / p.group, gh = vr - tok * p.group;
+    const int i = tok / p.step;
+    const int row = i * kRows + (tok - i * p.step) * p.group + gh;
+    auto prow = [&](int k) {
+      const int slot = 2 * ((int)blockIdx.x + k) + (k == 0 ? 1 : 0);
+      return (size_t)slot * (NQ * kRows) + row;
+    };
+    float m = -INFINITY;
+    for (int k = lane; k < rec.parts; k += 32) m = fmaxf(m, p.ml[prow(k)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < rec.parts; ++k) {
+      const float2 ml = p.ml[prow(k)];
+      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+      const float* src = p.part + prow(k) * D + lane * E;
+      float v[E];
+      if constexpr (E == 2) {
+        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 4)
+          *reinterpret_cast<float4*>(v + e) = *reinterpret_cast<const float4*>(src + e);
+      }
+      if (ml.x != -INFINITY) {  // a part that saw nothing holds nothing
+        l += f * ml.y;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += f * v[e];
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t r[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      r[e / 2] = l == 0.f ? 0u : pack16<FP16>(acc[e] * inv, acc[e + 1] * inv);
+    const int trow = rec.tok0 + tok, head = rec.head * p.group + gh;
+    uint16_t* dst = p.out + trow * p.o_tok + head * p.o_head + lane * E;
+    if constexpr (E == 2)
+      *reinterpret_cast<uint32_t*>(dst) = r[0];
+    else if constexpr (E == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(r[0], r[1]);
+    else
+      *reinterpret_cast<uint4*>(dst) = make_uint4(r[0], r[1], r[2], r[3]);
+    if (p.lse && lane == 0)
+      p.lse[(size_t)trow * (p.kv_heads * p.group) + head] =
+          l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+struct Layout {
+  size_t status, rec, ml, part, total;
+};
+Layout layout_of(int head_dim) {
+  Layout L;
+  const size_t rows = head_dim == 256 ? kRows : 2 * kRows;
+  size_t at = 0;
+  L.status = at;
+  at += 256;
+  L.rec = at;
+  at = round_up(at + sizeof(JoinRec) * kMaxCtas, 256);
+  L.ml = at;
+  at = round_up(at + 2 * kMaxCtas * rows * sizeof(float2), 256);
+  L.part = at;
+  at += 2 * kMaxCtas * rows * head_dim * sizeof(float);
+  L.total = at;
+  return L;
+}
+
+template <int D, int NQ, bool FP16>
+cudaError_t run(const AttnParams& p, int ctas, cudaStream_t s) {
+  cudaError_t e = launch_pdl(k_paged_attn<D, NQ, FP16>, dim3(ctas), dim3(kThreads),
+                             Cfg<D, NQ>::kSmem, s, p);
+  if (e == cudaSuccess)
+    e = launch_pdl(k_attn_join<D, NQ, FP16>, dim3(ctas), dim3(256), 0, s, p);
+  return e;
+}
+
+template <int D, int NQ, bool FP16>
+cudaError_t allow() {
+  return cudaFuncSetAttribute(k_paged_attn<D, NQ, FP16>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)Cfg<D, NQ>::kSmem);
+}
+template <bool FP16>
+cudaError_t allow_dim(int d) {
+  if (d == 256) return allow<256, 1, FP16>();
+  cudaError_t e = d == 128 ? allow<128, 1, FP16>() : allow<64, 1, FP16>();
+  if (e == cudaSuccess) e = d == 128 ? allow<128, 2, FP16>() : allow<64, 2, FP16>();
+  return e;
+}
+template <bool FP16>
+cudaError_t run_dim(int d, int nq, const AttnParams& p, int ctas, cudaStream_t s) {
+  if (d == 256) return run<256, 1, FP16>(p, ctas, s);
+  if (d == 128) return nq == 2 ? run<128, 2, FP16>(p, ctas, s) : run<128, 1, FP16>(p, ctas, s);
+  return nq == 2 ? run<64, 2, FP16>(p, ctas, s) : run<64, 1, FP16>(p, ctas, s);
+}
+
+dg_status_t check_config(const dg_attn_config_t* c, const dg_kv* kv) {
+  if (!c || !kv) return DG_ERR_INVALID_ARG;
+  if (c->n_q_heads <= 0 || c->flags != 0 || !(c->scale > 0.f) || !isfinite(c->scale))
+    return DG_ERR_INVALID_ARG;
+  if (c->n_q_heads % kv->cfg.n_kv_heads) return DG_ERR_INVALID_ARG;
+  if (c->n_q_heads / kv->cfg.n_kv_heads > kRows) return DG_ERR_UNSUPPORTED;
+  return DG_OK;
+}
+
+// Pages of one layer as (64-column block, head, token of the page, page).
+bool encode_pages(CUtensorMap* map, const dg_kv_config_t& c, const dg_kv_pool_t& pool, int layer,
+                  uint32_t box_tokens) {
+  const uint16_t* base = static_cast<const uint16_t*>(pool.p) + layer * pool.layer_stride;
+  const uint64_t dims[4] = {(uint64_t)c.head_dim, (uint64_t)c.n_kv_heads, (uint64_t)c.page_size,
+                            (uint64_t)c.n_pages};
+  const uint64_t strides[3] = {(uint64_t)pool.head_stride * 2, (uint64_t)pool.token_stride * 2,
+                               (uint64_t)pool.page_stride * 2};
+  const uint32_t box[4] = {64, 1, box_tokens, 1};
+  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, base, dims, strides, box);
+}
+
+}  // namespace
+
+struct dg_attn {
+  dg_attn_config_t cfg;
+  const dg_kv* kv;
+  uint8_t* ws;
+  Layout L;
+  int ctas;
+};
+
+namespace dg {
+namespace host {
+dg_status_t read_status(void* word, dg_stream_t stream, unsigned int* where, unsigned int* info) {
+  if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return DG_ERR_CUDA;
+  DevStatus st;
+  if (cudaMemcpy(&st, word, sizeof(st), cudaMemcpyDeviceToHost) != cudaSuccess) return DG_ERR_CUDA;
+  if (cudaMemset(word, 0, sizeof(st)) != cudaSuccess) return DG_ERR_CUDA;
+  if (where) *where = st.where;
+  if (info) *info = st.info0;
+  if (st.code == kDevTimeout) return DG_ERR_TIMEOUT;
+  if (st.code == kDevBounds) return DG_ERR_DEVICE_CHECK;
+  return DG_OK;
+}
+}  // namespace host
+}  // namespace dg
+
+extern "C" {
+
+dg_status_t dg_attn_workspace_size(const dg_attn_config_t* cfg, const dg_kv_t* kv, size_t* bytes) {
+  if (!bytes) return DG_ERR_INVALID_ARG;
+  const dg_status_t s = check_config(cfg, kv);
+  if (s != DG_OK) return s;
+  *bytes = layout_of(kv->cfg.head_dim).total;
+  return DG_OK;
+}
+
+dg_status_t dg_attn_create(const dg_attn_config_t* cfg, const dg_kv_t* kv, void* workspace,
+                           size_t workspace_bytes, dg_attn_t** out) {
+  if (!out) return DG_ERR_INVALID_ARG;
+  *out = nullptr;
+  const dg_status_t s = check_config(cfg, kv);
+  if (s != DG_OK) return s;
+  const Layout L = layout_of(kv->cfg.head_dim);
+  if (!workspace || workspace_bytes < L.total || !aligned(workspace, 1024)) return DG_ERR_WORKSPACE;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return DG_ERR_CUDA;
+  const cudaError_t e = kv->cfg.dtype == DG_T_FP16 ? allow_dim<true>(kv->cfg.head_dim)
+                                                   : allow_dim<false>(kv->cfg.head_dim);
+  if (e != cudaSuccess) return DG_ERR_CUDA;
+  if (cudaMemset(static_cast<uint8_t*>(workspace) + L.status, 0, sizeof(DevStatus)) != cudaSuccess)
+    return DG_ERR_CUDA;
+  dg_attn* a = new (std::nothrow) dg_attn();
+  if (!a) return DG_ERR_CUDA;
+  a->cfg = *cfg;
+  a->kv = kv;
+  a->ws = static_cast<uint8_t*>(workspace);
+  a->L = L;
+  a->ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  *out = a;
+  return DG_OK;
+}
+
+dg_status_t dg_attn_destroy(dg_attn_t* a) {
+  delete a;
+  return DG_OK;
+}
+
+dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const dg_heads_t* out,
+                            float* lse, const dg_kv_batch_t* batch, int n_tokens,
+                            dg_stream_t stream) {
+  if (!a) return DG_ERR_INVALID_ARG;
+  const dg_kv_config_t& c = a->kv->cfg;
+  if (layer < 0 || layer >= c.n_layers || n_tokens < 0) return DG_ERR_INVALID_ARG;
+  dg_status_t st = check_batch(batch, c);
+  if (st != DG_OK) return st;
+  if (n_tokens > kMaxKvTokens) return DG_ERR_UNSUPPORTED;
+  if (n_tokens == 0 || batch->n_seqs == 0) return DG_OK;
+  if ((st = check_heads(q)) != DG_OK || (st = check_heads(out)) != DG_OK) return st;
+  if (lse && !aligned(lse, 4)) return DG_ERR_ALIGNMENT;
+  if (q->p == out->p) return DG_ERR_INVALID_ARG;
+  const int group = a->cfg.n_q_heads / c.n_kv_heads;
+  AttnParams p;
+  p.step = kRows / group;
+  p.q_box = p.step < n_tokens ? p.step : n_tokens;
+  {
+    // a size-1 dimension's stride is never used, but must be a valid one
+    const uint64_t hs = a->cfg.n_q_heads > 1 ? q->head_stride : c.head_dim;
+    const uint64_t ts = n_tokens > 1 ? q->token_stride : c.head_dim;
+    if (hs == 0 || ts == 0) return DG_ERR_UNSUPPORTED;
+    const uint64_t dims[3] = {(uint64_t)c.head_dim, (uint64_t)a->cfg.n_q_heads,
+                              (uint64_t)n_tokens};
+    const uint64_t strides[2] = {hs * 2, ts * 2};
+    const uint32_t box[3] = {64, (uint32_t)group, (uint32_t)p.q_box};
+    if (!encode_tiled(&p.qm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, q->p, dims, strides, box))
+      return DG_ERR_CUDA;
+  }
+  const uint32_t kbox = c.page_size < kKeys ? c.page_size : kKeys;
+  const uint32_t vmax = c.head_dim == 256 ? 64 : 128;
+  const uint32_t vbox = kbox < vmax ? kbox : vmax;
+  if (!encode_pages(&p.km, c, c.k, layer, kbox) || !encode_pages(&p.vm, c, c.v, layer, vbox))
+    return DG_ERR_CUDA;
+  p.table = batch->page_table;
+  p.table_stride = batch->table_stride;
+  p.lens = batch->lens;
+  p.cu = batch->cu;
+  p.n_seqs = batch->n_seqs;
+  p.cap = batch->max_pages * c.page_size;
+  p.n_tokens = n_tokens;
+  p.n_pages = c.n_pages;
+  p.page_shift = log2_of(c.page_size);
+  p.kv_heads = c.n_kv_heads;
+  p.group = group;
+  // a limit past every distance is none
+  p.left = a->cfg.left >= p.cap + n_tokens ? -1 : a->cfg.left;
+  p.right = a->cfg.right >= p.cap + n_tokens ? -1 : a->cfg.right;
+  p.scale2 = a->cfg.scale * 1.4426950408889634f;
+  p.out = static_cast<uint16_t*>(out->p);
+  p.o_tok = out->token_stride;
+  p.o_head = out->head_stride;
+  p.lse = lse;
+  p.part = reinterpret_cast<float*>(a->ws + a->L.part);
+  p.ml = reinterpret_cast<float2*>(a->ws + a->L.ml);
+  p.rec = reinterpret_cast<JoinRec*>(a->ws + a->L.rec);
+  p.status = reinterpret_cast<DevStatus*>(a->ws + a->L.status);
+  // two tiles an item when the average sequence has more rows than one tile
+  const int nq =
+      c.head_dim < 256 && (int64_t)n_tokens * group > (int64_t)kRows * batch->n_seqs ? 2 : 1;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = c.dtype == DG_T_FP16 ? run_dim<true>(c.head_dim, nq, p, a->ctas, s)
+                                             : run_dim<false>(c.head_dim, nq, p, a->ctas, s);
+  return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+}
+
+dg_status_t dg_attn_last_device_status(dg_attn_t* a, dg_stream_t stream, unsigned int* where,
+                                       unsigned int* info) {
+  if (!a) return DG_ERR_INVALID_ARG;
+  return read_status(a->ws + a->L.status, stream, where, info);
+}
+
+}  // extern "C"

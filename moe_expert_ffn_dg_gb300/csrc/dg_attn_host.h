@@ -24,7 +24,8 @@ namespace dg {
 namespace host {
 
 constexpr int kMaxSeqs = 16384;
-constexpr int kMaxKvTokens = 1 << 30;
+// tokens of a sequence and of a call: sums of three stay inside 32 bits
+constexpr int kMaxKvTokens = 1 << 28;
 
 inline bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s < ((int64_t)1 << 37); }
 
