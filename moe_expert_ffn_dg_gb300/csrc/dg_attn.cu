@@ -93,7 +93,7 @@ struct Cfg {
   static constexpr int kQTile = kRows * D * 2;
   static constexpr int kQBufs = (NQ == 1 && D <= 128) ? 2 : 1;
   static constexpr size_t kSmem =
-      1024 + (size_t)kStages * kStageBytes + (size_t)kQBufs * NQ * kQTile;
+      (size_t)kStages * kStageBytes + (size_t)kQBufs * NQ * kQTile;
   // tensor memory columns
   static constexpr uint32_t kO = 256;
 };
@@ -379,14 +379,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   constexpr int NS = C::kStages, PARTS = C::kParts;
   constexpr int NC = NQ == 2 ? 128 : 64;        // score columns a softmax thread
   constexpr int OC = NQ == 2 ? D : D / 2;       // output columns a softmax thread
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem =
-      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t ring = smem_u32(smem);
   const uint32_t qbase = ring + NS * C::kStageBytes;
   __shared__ uint64_t full[NS], empty[NS];
   __shared__ uint64_t q_full[C::kQBufs], q_empty[C::kQBufs];
-  __shared__ uint64_t s_full[2], p_full[2], pv_done[2], o_empty[2], drain;
+  __shared__ uint64_t s_full[2], p_full[2], pv_done[2], o_full[2], o_empty[2], drain;
   __shared__ uint32_t tmem_holder;
   __shared__ int abort_word;
   __shared__ Start start;
@@ -395,6 +393,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
+  if (ring & 1023u) {  // the swizzle needs it; the declaration asks for it
+    if (tid == 0) report(p.status, kDevBounds, kSiteAttnLoad, ring, 0u);
+    return;
+  }
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 1);
@@ -408,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], NQ == 2 ? 4 : 8);
       mbar_init(&pv_done[i], 1);
+      mbar_init(&o_full[i], 1);
       mbar_init(&o_empty[i], NQ == 2 ? 4 : 8);
     }
     mbar_init(&drain, 1);
@@ -624,6 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             if (i == NQ - 1) umma_commit(&empty[st]);
           }
           umma_commit(&pv_done[i]);
+          if (j == g.n - 1) umma_commit(&o_full[i]);
         };
         if (NQ == 2) {
           scores(0, 0);
@@ -661,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     const int row = quarter * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     const int tok = row / p.group, gh = row - tok * p.group;
-    int pos = 0, at = 0;  // ring position, key tiles
+    int pos = 0, at = 0, segs = 0;  // ring position, key tiles, segments
     int xn = 0;           // exchanges (NQ = 1)
     bool ok = true;
     JoinRec rec{0, 0, 0, 0};
@@ -727,7 +731,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             }
           }
           if (j > 0 && __any_sync(0xffffffffu, fac != 1.f)) {
-            // O holds the tiles before this one once their product is done
+            // O holds the tiles before this one once their product is done.
+            // The products before that one are: S of this tile was issued
+            // after them, so the barrier is at most one phase behind.
             bool here = mbar_wait(&pv_done[i], (uint32_t)(at + j - 1) & 1u, abort_flag);
             here = __all_sync(0xffffffffu, here);
             if (!here) {
@@ -790,7 +796,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       }
       // ------------------------------------------------- end of the segment
       if (g.n) {
-        if (ok && !mbar_wait(&pv_done[i], (uint32_t)(at + g.n - 1) & 1u, abort_flag)) ok = false;
+        if (ok && !mbar_wait(&o_full[i], (uint32_t)segs & 1u, abort_flag)) ok = false;
+        ++segs;
         ok = __all_sync(0xffffffffu, ok);
         if (NQ == 2 && !ok) break;
         tc_fence_after();
