@@ -157,8 +157,8 @@ dg_status_t dg_kv_copy(dg_kv_t* kv, const int32_t* copies, int n, dg_stream_t st
 
 /* Compact: token i of sequence s becomes the token keep[cu[s] + i] that it had
  * (any order, repeats allowed), all layers, keys and values.  src and dst are
- * page tables as in dg_kv_batch_t (both [n_seqs, ...]); the pages written must
- * not be among those read.  n_keep: length of keep; cu: int32 [n_seqs + 1].
+ * page tables of n_seqs rows as in dg_kv_batch_t; the pages written must not
+ * be among those read.  n_keep: length of keep; cu: int32 [n_seqs + 1].
  * Tokens keep the rotary positions with which they were written. */
 dg_status_t dg_kv_gather(dg_kv_t* kv, const int32_t* src_table, int64_t src_stride, int src_pages,
                          const int32_t* dst_table, int64_t dst_stride, int dst_pages,

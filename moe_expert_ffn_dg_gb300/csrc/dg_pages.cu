@@ -354,7 +354,10 @@ __global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kForkThreads
       int id = -1;
       if (i < stay) {
         id = __ldg(f.table_in + (int64_t)g.parent * f.row + i);
-        if ((unsigned)id >= (unsigned)f.n_pages) id = -1;
+        if ((unsigned)id >= (unsigned)f.n_pages) {
+          report(p.status, kDevBounds, kSiteForkPage, (unsigned)g.parent, (unsigned)id);
+          id = -1;
+        }
       }
       if (i < stay || i >= want) f.table_out[(int64_t)j * f.row + i] = id;
     }
