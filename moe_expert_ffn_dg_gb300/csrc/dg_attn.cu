@@ -23,6 +23,12 @@
 // boundary leaves fp32 partial results in the workspace, joined in a fixed
 // order by k_attn_join.
 //
+// Query tiles of one sequence read the same keys.  `team` CTAs take as many
+// neighbouring tiles through the same key tiles at the same time, so that the
+// keys come from memory once, and the CL CTAs of a cluster (a team is made of
+// whole clusters) share each copy: every CTA loads its part of a stage and
+// multicasts it to all, and a stage is free once all have read it.
+//
 // Warps 0-3 and 4-7: softmax; 8: TMA producer; 9: MMA issuer and TMEM owner.
 // NQ = 2 (many rows, head size up to 128): two 128-row tiles an item, one a
 // warpgroup, which take turns on the tensor core.  NQ = 1 (few rows, or head
@@ -46,7 +52,10 @@ using namespace dg::host;
 namespace {
 
 constexpr int kMaxCtas = 160;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;  // 12 warps: registers are dealt by warpgroup
+// Registers a thread: 384 x 168 at launch; the producer and MMA warpgroup
+// gives up what the two softmax warpgroups take (2 x 224 + 56 = 3 x 168).
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 constexpr int kRows = 128;  // rows of a query tile
 constexpr int kKeys = 128;  // keys of a key tile
 
@@ -71,6 +80,7 @@ struct AttnParams {
   int n_seqs, cap, n_tokens, n_pages, page_shift;
   int kv_heads, group, step;  // step: tokens of a 128-row tile
   int q_box;                  // tokens of a query box
+  int team;                   // CTAs that take neighbouring tiles of a sequence
   int left, right;
   float scale2;  // scale log2 e
   uint16_t* out;
@@ -119,11 +129,17 @@ __device__ __forceinline__ int2 key_range(const AttnParams& p, const Seq& s, int
   return make_int2(lo, max(hi, 0));
 }
 
-// Key tiles [x, x + y) of item tile t.
+// Tokens of a team's item.
+template <int NQ>
+__device__ __forceinline__ int item_tokens(const AttnParams& p) {
+  return p.team * NQ * p.step;
+}
+
+// Key tiles [x, x + y) of item t of a team.
 template <int NQ>
 __device__ __forceinline__ int2 tile_range(const AttnParams& p, const Seq& s, int t) {
-  const int first = t * NQ * p.step;
-  const int2 k = key_range(p, s, first, min(NQ * p.step, s.n - first));
+  const int first = t * item_tokens<NQ>(p);
+  const int2 k = key_range(p, s, first, min(item_tokens<NQ>(p), s.n - first));
   if (k.x >= k.y) return make_int2(0, 0);
   const int a = k.x / kKeys;
   return make_int2(a, (k.y + kKeys - 1) / kKeys - a);
@@ -131,7 +147,7 @@ __device__ __forceinline__ int2 tile_range(const AttnParams& p, const Seq& s, in
 
 // The part of an item that a CTA works on.
 struct Seg {
-  int head, tok0, ntok;  // key/value head; first row of q / out; tokens
+  int head, tok0, ntok;  // key/value head; first row of q / out, tokens of this CTA (may be none)
   int pos;               // position of the first token
   int b, kv, klo, khi;   // sequence, its length, keys that the item sees
   int kt0, n;            // key tiles
@@ -147,16 +163,17 @@ struct Walk {
   Seq s;
   __device__ __forceinline__ bool next(const AttnParams& p, Seg& g) {
     if (u >= end) return false;
-    const int first = t * NQ * p.step;
+    const int item = item_tokens<NQ>(p);
     const int2 tr = tile_range<NQ>(p, s, t);
+    const int mine = t * item + (int)(blockIdx.x % p.team) * NQ * p.step;
     const int cost = max(tr.y, 1);
     const int take = (int)min((long long)(cost - skip), end - u);
     g.head = h;
     g.b = b;
-    g.tok0 = s.n0 + first;
-    g.ntok = min(NQ * p.step, s.n - first);
-    g.pos = s.kv - s.n + first;
-    const int2 k = key_range(p, s, first, g.ntok);
+    g.tok0 = s.n0 + mine;
+    g.ntok = max(0, min(NQ * p.step, s.n - mine));
+    g.pos = s.kv - s.n + mine;
+    const int2 k = key_range(p, s, t * item, min(item, s.n - t * item));
     g.kv = s.kv;
     g.klo = k.x;
     g.khi = k.y;
@@ -169,7 +186,7 @@ struct Walk {
     skip = 0;
     if (u < end) {
       ++t;
-      if (t * NQ * p.step >= s.n) {
+      if (t * item >= s.n) {
         t = 0;
         do {
           if (++b == p.n_seqs) {
@@ -187,7 +204,7 @@ struct Walk {
 struct Start {
   int h, b, t, skip;
   long long u, end, total;
-  int ctas;
+  int teams;
 };
 
 __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, uint32_t dst,
@@ -198,13 +215,79 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* ba
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
+// CL > 1: into the same place of every CTA of the cluster, counted on each
+// one's barrier.
+template <int CL>
 __device__ __forceinline__ void tma_load_4d(const CUtensorMap* map, uint64_t* bar, uint32_t dst,
                                             int c0, int c1, int c2, int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
+  if constexpr (CL > 1)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".multicast::cluster [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2),
+        "r"(c3), "h"((uint16_t)((1 << CL) - 1))
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2),
+        "r"(c3)
+        : "memory");
+}
+
+// umma_commit on the barrier of every CTA of the cluster.
+template <int CL>
+__device__ __forceinline__ void commit_cluster(uint64_t* bar) {
+  if constexpr (CL > 1)
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)((1 << CL) - 1))
+        : "memory");
+  else
+    umma_commit(bar);
+}
+
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void set_max_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_max_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__host__ __device__ constexpr int key_box_max(int d) { return d == 64 ? 64 : 128; }
+__host__ __device__ constexpr int value_box_max(int d) { return d == 128 ? 128 : 64; }
+
+// Two fp32 lanes of one instruction.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unf2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // D[tmem] (+)= A[tmem] * B[smem], 16-bit inputs, fp32 accumulate.
@@ -298,7 +381,7 @@ __device__ __forceinline__ void find_start(const AttnParams& p, long long* cost,
       long long c = 0;
       if (b < p.n_seqs) {
         const Seq s = load_seq(p, b);
-        for (int t = sub; t * NQ * p.step < s.n; t += lps) c += max(tile_range<NQ>(p, s, t).y, 1);
+        for (int t = sub; t * item_tokens<NQ>(p) < s.n; t += lps) c += max(tile_range<NQ>(p, s, t).y, 1);
         if (blockIdx.x == 0 && sub == 0) {
           const int a = __ldg(p.cu + b), e = __ldg(p.cu + b + 1), kv = __ldg(p.lens + b);
           if (a < 0 || e < a || e > p.n_tokens || kv < 0 || kv > p.cap)
@@ -322,12 +405,12 @@ __device__ __forceinline__ void find_start(const AttnParams& p, long long* cost,
     }
     const long long one = __shfl_sync(0xffffffffu, incl, 31);
     const long long total = one * p.kv_heads;
-    const int ctas = (int)min((long long)gridDim.x, total);
-    const int c = blockIdx.x;
+    const int teams = (int)min((long long)(gridDim.x / p.team), total);
+    const int c = blockIdx.x / p.team;
     long long u0 = 0, u1 = 0;
-    if (c < ctas) {
-      u0 = (long long)c * total / ctas;
-      u1 = (long long)(c + 1) * total / ctas;
+    if (c < teams) {
+      u0 = (long long)c * total / teams;
+      u1 = (long long)(c + 1) * total / teams;
     }
     int h = 0, b = 0, t = 0, skip = 0;
     if (u0 < u1) {
@@ -346,7 +429,7 @@ __device__ __forceinline__ void find_start(const AttnParams& p, long long* cost,
       for (int base = 0;; base += 32) {
         const int tt = base + lane;
         int cc = 0;
-        if (tt * NQ * p.step < s.n) cc = max(tile_range<NQ>(p, s, tt).y, 1);
+        if (tt * item_tokens<NQ>(p) < s.n) cc = max(tile_range<NQ>(p, s, tt).y, 1);
         long long in = cc;
         for (int o = 1; o < 32; o <<= 1) {
           const long long v = __shfl_up_sync(0xffffffffu, in, o);
@@ -361,19 +444,19 @@ __device__ __forceinline__ void find_start(const AttnParams& p, long long* cost,
           break;
         }
         r -= all;
-        if (base * NQ * p.step >= s.n) {  // cannot happen: r lies in this sequence
+        if (base * item_tokens<NQ>(p) >= s.n) {  // cannot happen: r lies in this sequence
           u1 = u0;
           break;
         }
       }
     }
-    if (lane == 0) *out = Start{h, b, t, skip, u0, u1, total, ctas};
+    if (lane == 0) *out = Start{h, b, t, skip, u0, u1, total, teams};
   }
   fence_proxy_async_smem();  // `cost` lies where copies will land
   __syncthreads();
 }
 
-template <int D, int NQ, bool FP16>
+template <int D, int NQ, int CL, bool FP16>
 __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constant__ AttnParams p) {
   using C = Cfg<D, NQ>;
   constexpr int NS = C::kStages, PARTS = C::kParts;
@@ -400,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], CL);
     }
     for (int i = 0; i < C::kQBufs; ++i) {
       mbar_init(&q_full[i], 1);
@@ -426,10 +509,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     tmem_alloc(&tmem_holder, 512);
     tmem_relinquish();
   }
+  if (CL > 1) cluster_arrive();  // barriers must be there before a neighbour's copy or arrival
   pdl_wait();
   tc_fence_before();
   find_start<NQ>(p, reinterpret_cast<long long*>(smem), &start);
   tc_fence_after();
+  if (CL > 1) cluster_wait();
   const uint32_t tmem = tmem_holder;
   Walk<NQ> w;
   w.h = start.h;
@@ -441,13 +526,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   if (w.u < w.end) w.s = load_seq(p, w.b);
   Seg g;
 
+  if (warp >= 8) {
+    set_max_regs_down<kRegsOther>();
   if (warp == 8) {
     // ------------------------------------------------------------ producer
     const int ps = 1 << p.page_shift;
-    const int kbox = min(ps, kKeys), kpieces = kKeys / kbox;
+    // tokens of a key box (two boxes a stage at least, one a CTA of the cluster)
+    const int kbox = min(ps, key_box_max(D)), kpieces = kKeys / kbox;
+    const uint32_t rank = CL > 1 ? blockIdx.x % CL : 0;
     constexpr int VKEYS = kKeys / PARTS;             // keys of a value stage
     constexpr int KCH = D == 256 ? 2 : C::kChunks;   // columns of a key stage
-    const int vbox = min(ps, VKEYS), vpieces = VKEYS / vbox;
+    const int vbox = min(ps, value_box_max(D)), vpieces = VKEYS / vbox;
     int pos = 0, qn = 0;
     bool ok = true;
     uint32_t armed = 0, armed_par = 0, q_armed = 0, q_par = 0;
@@ -513,8 +602,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             const int id = __shfl_sync(0xffffffffu, pid, (kt * kpieces + i) & 31);
             if (lane == 0) mbar_arrive_expect_tx(&full[st], live * kbox * 128 * KCH);
             __syncwarp();
-            if (i < live && c < KCH)
-              tma_load_4d(&p.km, &full[st],
+            if (i < live && c < KCH && lane % CL == rank)
+              tma_load_4d<CL>(&p.km, &full[st],
                           ring + st * C::kStageBytes + c * (kKeys * 128) + i * kbox * 128,
                           (h * KCH + c) * 64, g.head, (kt * kKeys + i * kbox) & (ps - 1), id);
           }
@@ -532,8 +621,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             __syncwarp();
             const int i = lane % vpieces, c = lane / vpieces, key = key0 + i * vbox;
             const int id = __shfl_sync(0xffffffffu, pid, (key / kbox) & 31);
-            if (i < live && c < C::kChunks)
-              tma_load_4d(&p.vm, &full[st],
+            if (i < live && c < C::kChunks && lane % CL == rank)
+              tma_load_4d<CL>(&p.vm, &full[st],
                           ring + st * C::kStageBytes + c * (VKEYS * 128) + i * vbox * 128, 64 * c,
                           g.head, key & (ps - 1), id);
           }
@@ -596,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
                 umma_bf16(d, sw128_kmajor_desc(a + 32 * k), sw128_kmajor_desc(b + 32 * k), idesc,
                           (h | c | k) ? 1u : 0u);
             }
-            if (i == NQ - 1) umma_commit(&empty[st]);
+            if (i == NQ - 1) commit_cluster<CL>(&empty[st]);
           }
           issued = true;
           umma_commit(&s_full[NQ == 2 ? i : ((at + j) & 1)]);
@@ -624,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
                 umma_ts(d, a + 8 * (h * SK + k),
                         sw128_nmajor_desc(ring + st * C::kStageBytes + k * 2048, SK * 2048), idesc,
                         (j | h | k) ? 1u : 0u);
-            if (i == NQ - 1) umma_commit(&empty[st]);
+            if (i == NQ - 1) commit_cluster<CL>(&empty[st]);
           }
           umma_commit(&pv_done[i]);
           if (j == g.n - 1) umma_commit(&o_full[i]);
@@ -656,7 +745,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         if (!wait_drain(&drain, 0u)) report(p.status, kDevTimeout, kSiteAttnDrain, 99u, 0u);
       }
     }
+  }
   } else {
+    set_max_regs_up<kRegsSoftmax>();
     // ------------------------------------------------------------ softmax
     const int wg = warp >> 2, quarter = warp & 3;
     const int i = NQ == 2 ? wg : 0;        // tile of the item
@@ -690,12 +781,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         if (live) {
           const uint32_t ts = tl + buf * 128u;
           float s[NC];
-          if constexpr (NC == 128) {
-            tmem_load64(ts, *reinterpret_cast<float(*)[64]>(s));
-            tmem_load64(ts + 64, *reinterpret_cast<float(*)[64]>(s + 64));
-          } else {
-            tmem_load64(ts + c0, s);
-          }
+          if constexpr (NC == 128) tmem_load128(ts, s);
+          else tmem_load64(ts + c0, s);
           const int rl = lo - key0 - c0, rh = hi - key0 - c0;
           if (!__all_sync(0xffffffffu, rl <= 0 && rh >= NC)) {
 #pragma unroll
@@ -704,7 +791,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
           }
           float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int c = 4; c < NC; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], s[c]);
+          for (int c = 4; c + 7 < NC; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(fmaxf(mx4[e], s[c + e]), s[c + 4 + e]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(mx4[e], s[NC - 4 + e]);
           float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
           if (NQ == 1) {
             float* x = xch[xn & 1];
@@ -741,33 +832,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
               if (NQ == 2) break;
             }
             tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < OC; c += 16) {
+              float o[16];
+              uint32_t r[16];
+              tmem_ld16(tl + C::kO + i * D + o0 + c, o);
 #pragma unroll
-            for (int c = 0; c < OC; c += 32) {
-              float o[32];
-              uint32_t r[32];
-              tmem_load32(tl + C::kO + i * D + o0 + c, o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(o[e] * fac);
-              tmem_store32(tl + C::kO + i * D + o0 + c, r);
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(o[e] * fac);
+              tmem_store16(tl + C::kO + i * D + o0 + c, r);
             }
           }
           const float mr = m == -INFINITY ? 0.f : m;
-          float l4[4] = {0.f, 0.f, 0.f, 0.f};
-          uint32_t pk[NC / 2];
+          const uint64_t sc2 = f2(p.scale2, p.scale2), mr2 = f2(-mr, -mr);
+          uint64_t l2[2] = {0, 0};
 #pragma unroll
-          for (int c = 0; c < NC; c += 2) {
-            const float a = exp2_fast(fmaf(s[c], p.scale2, -mr));
-            const float b = exp2_fast(fmaf(s[c + 1], p.scale2, -mr));
-            l4[c & 2] += a;
-            l4[(c & 2) + 1] += b;
-            pk[c / 2] = pack16<FP16>(a, b);
+          for (int b = 0; b < NC; b += 32) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const float2 x = unf2(fma2(f2(s[b + c], s[b + c + 1]), sc2, mr2));
+              const float e0 = exp2_fast(x.x), e1 = exp2_fast(x.y);
+              l2[(c >> 1) & 1] = add2(l2[(c >> 1) & 1], f2(e0, e1));
+              pk[c / 2] = pack16<FP16>(e0, e1);
+            }
+            tmem_store16(ts + c0 / 2 + b / 2, pk);
           }
-          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-          if constexpr (NC == 128) {
-            tmem_store32(ts, *reinterpret_cast<uint32_t(*)[32]>(pk));
-            tmem_store32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
-          } else {
-            tmem_store32(ts + c0 / 2, pk);
+          {
+            const float2 x = unf2(add2(l2[0], l2[1]));
+            l += x.x + x.y;
           }
           tmem_store_wait();
         }
@@ -859,8 +951,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         }
       }
       if (g.first && !g.last) {
-        // unit range of CTA c: [c total / ctas, (c + 1) total / ctas)
-        rec.parts = (int)((g.end * start.ctas - 1) / start.total) - (int)blockIdx.x + 1;
+        // unit range of team c: [c total / teams, (c + 1) total / teams)
+        rec.parts =
+            (int)((g.end * start.teams - 1) / start.total) - (int)(blockIdx.x / p.team) + 1;
         rec.head = g.head;
         rec.tok0 = g.tok0;
         rec.ntok = g.ntok;
@@ -887,6 +980,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (CL > 1) {  // a neighbour's copies and arrivals may still come here
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+  }
 }
 
 // Join the parts of the item that CTA blockIdx.x began: with m the largest
@@ -905,7 +1003,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnP
     const int i = tok / p.step;
     const int row = i * kRows + (tok - i * p.step) * p.group + gh;
     auto prow = [&](int k) {
-      const int slot = 2 * ((int)blockIdx.x + k) + (k == 0 ? 1 : 0);
+      const int slot = 2 * ((int)blockIdx.x + k * p.team) + (k == 0 ? 1 : 0);
       return (size_t)slot * (NQ * kRows) + row;
     };
     float m = -INFINITY;
@@ -974,33 +1072,54 @@ Layout layout_of(int head_dim) {
   return L;
 }
 
-template <int D, int NQ, bool FP16>
-cudaError_t run(const AttnParams& p, int ctas, cudaStream_t s) {
-  cudaError_t e = launch_pdl(k_paged_attn<D, NQ, FP16>, dim3(ctas), dim3(kThreads),
-                             Cfg<D, NQ>::kSmem, s, p);
-  if (e == cudaSuccess)
-    e = launch_pdl(k_attn_join<D, NQ, FP16>, dim3(ctas), dim3(256), 0, s, p);
-  return e;
-}
+// The variants of a head size: few rows (one tile, no cluster) and many rows
+// (as wide an item as fits, clusters of two).
+template <int D, bool FP16>
+struct Variant {
+  static constexpr int kManyNq = D == 256 ? 1 : 2;
+  static constexpr auto few = k_paged_attn<D, 1, 1, FP16>;
+  static constexpr auto many = k_paged_attn<D, kManyNq, 2, FP16>;
+  static cudaError_t run(bool m, const AttnParams& p, int ctas, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = m ? Cfg<D, kManyNq>::kSmem : Cfg<D, 1>::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = m ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, m ? many : few, p);
+    if (e != cudaSuccess) return e;
+    if (m && kManyNq == 2)
+      return launch_pdl(k_attn_join<D, kManyNq, FP16>, dim3(ctas), dim3(256), 0, s, p);
+    return launch_pdl(k_attn_join<D, 1, FP16>, dim3(ctas), dim3(256), 0, s, p);
+  }
+  static cudaError_t prepare() {
+    cudaError_t e = cudaFuncSetAttribute(few, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Cfg<D, 1>::kSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(many, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)Cfg<D, kManyNq>::kSmem);
+    return e;
+  }
+};
 
-template <int D, int NQ, bool FP16>
-cudaError_t allow() {
-  return cudaFuncSetAttribute(k_paged_attn<D, NQ, FP16>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)Cfg<D, NQ>::kSmem);
+template <bool FP16>
+cudaError_t prepare_dim(int d) {
+  return d == 256   ? Variant<256, FP16>::prepare()
+         : d == 128 ? Variant<128, FP16>::prepare()
+                    : Variant<64, FP16>::prepare();
 }
 template <bool FP16>
-cudaError_t allow_dim(int d) {
-  if (d == 256) return allow<256, 1, FP16>();
-  cudaError_t e = d == 128 ? allow<128, 1, FP16>() : allow<64, 1, FP16>();
-  if (e == cudaSuccess) e = d == 128 ? allow<128, 2, FP16>() : allow<64, 2, FP16>();
-  return e;
-}
-template <bool FP16>
-cudaError_t run_dim(int d, int nq, const AttnParams& p, int ctas, cudaStream_t s) {
-  if (d == 256) return run<256, 1, FP16>(p, ctas, s);
-  if (d == 128) return nq == 2 ? run<128, 2, FP16>(p, ctas, s) : run<128, 1, FP16>(p, ctas, s);
-  return nq == 2 ? run<64, 2, FP16>(p, ctas, s) : run<64, 1, FP16>(p, ctas, s);
+cudaError_t run_dim(int d, bool many, const AttnParams& p, int ctas, cudaStream_t s) {
+  return d == 256   ? Variant<256, FP16>::run(many, p, ctas, s)
+         : d == 128 ? Variant<128, FP16>::run(many, p, ctas, s)
+                    : Variant<64, FP16>::run(many, p, ctas, s);
 }
 
 dg_status_t check_config(const dg_attn_config_t* c, const dg_kv* kv) {
@@ -1073,8 +1192,8 @@ dg_status_t dg_attn_create(const dg_attn_config_t* cfg, const dg_kv_t* kv, void*
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return DG_ERR_CUDA;
-  const cudaError_t e = kv->cfg.dtype == DG_T_FP16 ? allow_dim<true>(kv->cfg.head_dim)
-                                                   : allow_dim<false>(kv->cfg.head_dim);
+  const cudaError_t e = kv->cfg.dtype == DG_T_FP16 ? prepare_dim<true>(kv->cfg.head_dim)
+                                                   : prepare_dim<false>(kv->cfg.head_dim);
   if (e != cudaSuccess) return DG_ERR_CUDA;
   if (cudaMemset(static_cast<uint8_t*>(workspace) + L.status, 0, sizeof(DevStatus)) != cudaSuccess)
     return DG_ERR_CUDA;
@@ -1123,9 +1242,8 @@ dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const 
     if (!encode_tiled(&p.qm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, q->p, dims, strides, box))
       return DG_ERR_CUDA;
   }
-  const uint32_t kbox = c.page_size < kKeys ? c.page_size : kKeys;
-  const uint32_t vmax = c.head_dim == 256 ? 64 : 128;
-  const uint32_t vbox = kbox < vmax ? kbox : vmax;
+  const int ps = c.page_size, kmax = key_box_max(c.head_dim), vmax = value_box_max(c.head_dim);
+  const uint32_t kbox = ps < kmax ? ps : kmax, vbox = ps < vmax ? ps : vmax;
   if (!encode_pages(&p.km, c, c.k, layer, kbox) || !encode_pages(&p.vm, c, c.v, layer, vbox))
     return DG_ERR_CUDA;
   p.table = batch->page_table;
@@ -1151,12 +1269,16 @@ dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const 
   p.ml = reinterpret_cast<float2*>(a->ws + a->L.ml);
   p.rec = reinterpret_cast<JoinRec*>(a->ws + a->L.rec);
   p.status = reinterpret_cast<DevStatus*>(a->ws + a->L.status);
-  // two tiles an item when the average sequence has more rows than one tile
-  const int nq =
-      c.head_dim < 256 && (int64_t)n_tokens * group > (int64_t)kRows * batch->n_seqs ? 2 : 1;
+  // By the average rows of a sequence: few (one tile) or many.  Many: teams of
+  // two clusters when there are that many tiles.
+  const int64_t rows = (int64_t)n_tokens * group / batch->n_seqs;
+  const bool many = rows > kRows;
+  const int wide = c.head_dim == 256 ? kRows : 2 * kRows;
+  p.team = !many ? 1 : (rows > 2 * wide ? 4 : 2);
+  const int ctas = a->ctas / p.team * p.team;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = c.dtype == DG_T_FP16 ? run_dim<true>(c.head_dim, nq, p, a->ctas, s)
-                                             : run_dim<false>(c.head_dim, nq, p, a->ctas, s);
+  const cudaError_t e = c.dtype == DG_T_FP16 ? run_dim<true>(c.head_dim, many, p, ctas, s)
+                                             : run_dim<false>(c.head_dim, many, p, ctas, s);
   return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 
