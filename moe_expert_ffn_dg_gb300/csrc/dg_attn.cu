@@ -290,23 +290,48 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// D[tmem] (+)= A[tmem] * B[smem], 16-bit inputs, fp32 accumulate.
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                        uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r != 0;
 }
 
-// Operand whose rows are 64-element columns of N (128 bytes a row, one row a
-// k): the leading offset steps from one 64-element column to the next, the
-// stride offset from 8 k to the next 8.
-__device__ __forceinline__ uint64_t sw128_nmajor_desc(uint32_t smem_addr, uint32_t chunk_bytes) {
-  return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | ((uint64_t)(chunk_bytes >> 4) << 16) |
-         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Shared-memory matrix descriptors with the 128-byte swizzle (8-row x 128-byte
+// atoms, 1024 bytes from one to the next).  The high word is the same for all:
+// stride offset 1024, version 1, swizzle mode 2.  The low word holds the start
+// address and the leading offset, which only N-major operands use (rows of
+// 64 N elements, one row a k: the step from one 64-element column to the next).
+// Shared-memory addresses carry the CTA's rank of a cluster above 18 bits.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr, uint32_t leading) {
+  return ((smem_addr & 0x3FFFFu) >> 4) | ((leading >> 4) << 16);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit inputs, fp32 accumulate.
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                        uint32_t idesc, int accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+      : "memory");
+}
+// The same with A in tensor memory.
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                        uint32_t idesc, int accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+      : "memory");
 }
 
 template <bool FP16>
@@ -646,14 +671,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    // The whole warp runs the loop, so that operands stay in uniform registers,
+    // and one elected lane issues.
+    {
+      const bool leader = elect_one();
       int pos = 0, qn = 0, at = 0, segs = 0;  // ring position, query tiles, key tiles, segments
       bool ok = true, issued = false;
       auto need = [&](uint64_t* bar, uint32_t parity) {
-        if (ok && !mbar_wait(bar, parity, abort_flag)) {
-          report(p.status, kDevTimeout, kSiteAttnMma, (unsigned)at, smem_u32(bar));
-          *abort_flag = 1;
-          ok = false;
+        if (ok) {
+          const bool here = mbar_wait(bar, parity, abort_flag);
+          ok = __all_sync(0xffffffffu, here);
+          if (!ok) {
+            if (lane == 0) report(p.status, kDevTimeout, kSiteAttnMma, (unsigned)at, smem_u32(bar));
+            *abort_flag = 1;
+          }
         }
         return ok;
       };
@@ -668,7 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         };
         auto scores = [&](int i, int j) {  // S_i(j) = Q_i K_j^T
           const int rp = pos + k_stage<PARTS>(j);
-          const uint32_t d = tmem + (NQ == 2 ? i : ((at + j) & 1)) * 128u;
+          const int buf = NQ == 2 ? i : ((at + j) & 1);
+          const uint32_t d = tmem + buf * 128u;
           const uint32_t idesc = idesc_16<FP16>(128, 16 * steps(j), false);
 #pragma unroll
           for (int h = 0; h < PARTS; ++h) {
@@ -676,20 +708,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             if (i == 0 && !need(&full[st], (uint32_t)((rp + h) / NS) & 1u)) return;
             tc_fence_after();
             constexpr int CH = C::kChunks / PARTS;
+            const uint32_t a =
+                desc_lo(qbase + (qb * NQ + i) * C::kQTile + h * CH * (kRows * 128), 16);
+            const uint32_t b = desc_lo(ring + st * C::kStageBytes, 16);
+            if (leader) {
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-              const uint32_t a = qbase + (qb * NQ + i) * C::kQTile + (h * CH + c) * (kRows * 128);
-              const uint32_t b = ring + st * C::kStageBytes + c * (kKeys * 128);
+              for (int c = 0; c < CH; ++c)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_bf16(d, sw128_kmajor_desc(a + 32 * k), sw128_kmajor_desc(b + 32 * k), idesc,
-                          (h | c | k) ? 1u : 0u);
+                for (int k = 0; k < 4; ++k)
+                  umma_ss(d, a + (c * (kRows * 128) + 32 * k) / 16,
+                          b + (c * (kKeys * 128) + 32 * k) / 16, idesc, h | c | k);
+              if (i == NQ - 1) commit_cluster<CL>(&empty[st]);
+              if (h == PARTS - 1) {
+                umma_commit(&s_full[buf]);
+                if (i == NQ - 1 && j == g.n - 1) umma_commit(&q_empty[qb]);
+              }
             }
-            if (i == NQ - 1) commit_cluster<CL>(&empty[st]);
+            __syncwarp();
           }
           issued = true;
-          umma_commit(&s_full[NQ == 2 ? i : ((at + j) & 1)]);
-          if (i == NQ - 1 && j == g.n - 1) umma_commit(&q_empty[qb]);
         };
         auto values = [&](int i, int j) {  // O_i += P_i(j) V_j
           const int buf = NQ == 2 ? i : ((at + j) & 1);
@@ -707,16 +744,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             const int st = (rp + h) % NS;
             if (i == 0 && !need(&full[st], (uint32_t)((rp + h) / NS) & 1u)) return;
             tc_fence_after();
+            // one 64-column chunk of V to the next: SK steps of 16 rows
+            const uint32_t b = desc_lo(ring + st * C::kStageBytes, SK * 2048);
+            if (leader) {
+              if (j == 0 && h == 0) umma_ts(d, a, b, idesc, 0);
+              else if (h * SK < ks) umma_ts(d, a + 8 * h * SK, b, idesc, 1);
+              if (ks >= (h + 1) * SK) {
 #pragma unroll
-            for (int k = 0; k < SK; ++k)
-              if (h * SK + k < ks)
-                umma_ts(d, a + 8 * (h * SK + k),
-                        sw128_nmajor_desc(ring + st * C::kStageBytes + k * 2048, SK * 2048), idesc,
-                        (j | h | k) ? 1u : 0u);
-            if (i == NQ - 1) commit_cluster<CL>(&empty[st]);
+                for (int k = 1; k < SK; ++k)
+                  umma_ts(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc, 1);
+              } else {
+                for (int k = 1; h * SK + k < ks; ++k)
+                  umma_ts(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc, 1);
+              }
+              if (i == NQ - 1) commit_cluster<CL>(&empty[st]);
+              if (h == PARTS - 1) {
+                umma_commit(&pv_done[i]);
+                if (j == g.n - 1) umma_commit(&o_full[i]);
+              }
+            }
+            __syncwarp();
           }
-          umma_commit(&pv_done[i]);
-          if (j == g.n - 1) umma_commit(&o_full[i]);
         };
         if (NQ == 2) {
           scores(0, 0);
@@ -740,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         ++segs;
       }
       // every MMA issued here must have completed before TMEM is released
-      if (issued) {
+      if (issued && leader) {
         umma_commit(&drain);
         if (!wait_drain(&drain, 0u)) report(p.status, kDevTimeout, kSiteAttnDrain, 99u, 0u);
       }
