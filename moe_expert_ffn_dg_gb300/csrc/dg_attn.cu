@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   const uint32_t qbase = ring + NS * C::kStageBytes;
   __shared__ uint64_t full[NS], empty[NS];
   __shared__ uint64_t q_full[C::kQBufs], q_empty[C::kQBufs];
-  __shared__ uint64_t s_full[2], p_full[2], pv_done[2], o_full[2], o_empty[2], drain;
+  __shared__ uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], o_full[2], o_empty[2], drain;
   __shared__ uint32_t tmem_holder;
   __shared__ int abort_word;
   __shared__ Start start;
@@ -516,6 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
+      mbar_init(&p_half[i], 4);
       mbar_init(&p_full[i], NQ == 2 ? 4 : 8);
       mbar_init(&pv_done[i], 1);
       mbar_init(&o_full[i], 1);
@@ -731,7 +732,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         auto values = [&](int i, int j) {  // O_i += P_i(j) V_j
           const int buf = NQ == 2 ? i : ((at + j) & 1);
           const uint32_t use = NQ == 2 ? (uint32_t)(at + j) : (uint32_t)(at + j) >> 1;
-          if (!need(&p_full[buf], use & 1u)) return;
+          // NQ = 2: the first 64 keys' weights come ahead of the others'
+          if (!need(NQ == 2 ? &p_half[buf] : &p_full[buf], use & 1u)) return;
           if (j == 0 && !need(&o_empty[i], ((uint32_t)segs & 1u) ^ 1u)) return;
           const int rp = pos + v_stage<PARTS>(j, g.n);
           const uint32_t d = tmem + C::kO + i * D;
@@ -749,14 +751,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             if (leader) {
               if (j == 0 && h == 0) umma_ts(d, a, b, idesc, 0);
               else if (h * SK < ks) umma_ts(d, a + 8 * h * SK, b, idesc, 1);
-              if (ks >= (h + 1) * SK) {
+            }
+            constexpr int S0 = NQ == 2 ? SK / 2 : SK;  // steps before the second wait
+            auto more = [&](int k0, int k1) {
+              if (ks >= h * SK + k1) {
 #pragma unroll
                 for (int k = 1; k < SK; ++k)
-                  umma_ts(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc, 1);
+                  if (k >= k0 && k < k1)
+                    umma_ts(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc, 1);
               } else {
-                for (int k = 1; h * SK + k < ks; ++k)
+                for (int k = k0; h * SK + k < ks; ++k)
                   umma_ts(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc, 1);
               }
+            };
+            if (leader) more(1, S0);
+            if (NQ == 2) {
+              __syncwarp();
+              if (!need(&p_full[buf], use & 1u)) return;
+              tc_fence_after();
+            }
+            if (leader) {
+              if (S0 < SK) more(S0, SK);
               if (i == NQ - 1) commit_cluster<CL>(&empty[st]);
               if (h == PARTS - 1) {
                 umma_commit(&pv_done[i]);
@@ -826,6 +841,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         ok = __all_sync(0xffffffffu, ok);
         if (!ok && (NQ == 2 || !live)) break;  // a live pair leaves at its barrier
         tc_fence_after();
+        // The last tile of an item may hold keys that no row sees, and rows
+        // that were never written: their V is zeroed up to the 16-key step,
+        // so that 0 * V cannot bring in a NaN.
+        const int vis = g.khi - key0;
+        if (vis < kKeys && (vis & 15) && i == 0) {
+          const int rp = pos + v_stage<PARTS>(j, g.n);
+          constexpr int VK = kKeys / PARTS;
+          const int h = vis / VK;  // the stage that holds the step
+          const int st = (rp + h) % NS;
+          if (!mbar_wait(&full[st], (uint32_t)((rp + h) / NS) & 1u, abort_flag)) ok = false;
+          const int r0 = vis - h * VK, r1 = (r0 + 15) & ~15;
+          constexpr int NT = NQ == 2 ? 128 : 256;
+          for (int x = (tid & (NT - 1)); x < (r1 - r0) * C::kChunks * 8; x += NT) {
+            const int u = x & 7, r = r0 + (x >> 3) / C::kChunks, c = (x >> 3) % C::kChunks;
+            *reinterpret_cast<uint4*>(smem + st * C::kStageBytes + c * (VK * 128) + r * 128 +
+                                      u * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
         if (live) {
           const uint32_t ts = tl + buf * 128u;
           float s[NC];
@@ -904,31 +938,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
               pk[c / 2] = pack16<FP16>(e0, e1);
             }
             tmem_store16(ts + c0 / 2 + b / 2, pk);
+            if (NQ == 2 && b == 32) {
+              tmem_store_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&p_half[buf]);
+            }
           }
           {
             const float2 x = unf2(add2(l2[0], l2[1]));
             l += x.x + x.y;
           }
           tmem_store_wait();
-        }
-        // The last tile of an item may hold keys that no row sees, and rows
-        // that were never written: their V is zeroed up to the 16-key step,
-        // so that 0 * V cannot bring in a NaN.
-        const int vis = g.khi - key0;
-        if (vis < kKeys && (vis & 15) && i == 0) {
-          const int rp = pos + v_stage<PARTS>(j, g.n);
-          constexpr int VK = kKeys / PARTS;
-          const int h = vis / VK;  // the stage that holds the step
-          const int st = (rp + h) % NS;
-          if (!mbar_wait(&full[st], (uint32_t)((rp + h) / NS) & 1u, abort_flag)) ok = false;
-          const int r0 = vis - h * VK, r1 = (r0 + 15) & ~15;
-          constexpr int NT = NQ == 2 ? 128 : 256;
-          for (int x = (tid & (NT - 1)); x < (r1 - r0) * C::kChunks * 8; x += NT) {
-            const int u = x & 7, r = r0 + (x >> 3) / C::kChunks, c = (x >> 3) % C::kChunks;
-            *reinterpret_cast<uint4*>(smem + st * C::kStageBytes + c * (VK * 128) + r * 128 +
-                                      u * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
+        } else if (NQ == 2) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_half[buf]);
         }
         tc_fence_before();
         __syncwarp();
@@ -1144,8 +1168,8 @@ struct Variant {
     const cudaError_t e = cudaLaunchKernelEx(&cfg, m ? many : few, p);
     if (e != cudaSuccess) return e;
     if (m && kManyNq == 2)
-      return launch_pdl(k_attn_join<D, kManyNq, FP16>, dim3(ctas), dim3(256), 0, s, p);
-    return launch_pdl(k_attn_join<D, 1, FP16>, dim3(ctas), dim3(256), 0, s, p);
+      return launch_pdl(k_attn_join<D, kManyNq, FP16>, dim3(ctas, 8), dim3(256), 0, s, p);
+    return launch_pdl(k_attn_join<D, 1, FP16>, dim3(ctas, m ? 8 : 1), dim3(256), 0, s, p);
   }
   static cudaError_t prepare() {
     cudaError_t e = cudaFuncSetAttribute(few, cudaFuncAttributeMaxDynamicSharedMemorySize,
