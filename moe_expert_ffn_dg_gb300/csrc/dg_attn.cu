@@ -29,7 +29,8 @@
 // whole clusters) share each copy: every CTA loads its part of a stage and
 // multicasts it to all, and a stage is free once all have read it.
 //
-// Warps 0-3 and 4-7: softmax; 8: TMA producer; 9: MMA issuer and TMEM owner.
+// Warps 0-3 and 4-7: softmax; 8 and 10: TMA producers of keys and values; 9: MMA
+// issuer and TMEM owner.
 // NQ = 2 (many rows, head size up to 128): two 128-row tiles an item, one a
 // warpgroup, which take turns on the tensor core.  NQ = 1 (few rows, or head
 // size 256, whose accumulator takes half of the TMEM): one tile, its key
@@ -55,7 +56,7 @@ constexpr int kMaxCtas = 160;
 constexpr int kThreads = 384;  // 12 warps: registers are dealt by warpgroup
 // Registers a thread: 384 x 168 at launch; the producer and MMA warpgroup
 // gives up what the two softmax warpgroups take (2 x 224 + 56 = 3 x 168).
-constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 constexpr int kRows = 128;  // rows of a query tile
 constexpr int kKeys = 128;  // keys of a key tile
 
@@ -265,8 +266,9 @@ __device__ __forceinline__ void set_max_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-__host__ __device__ constexpr int key_box_max(int d) { return d == 64 ? 64 : 128; }
-__host__ __device__ constexpr int value_box_max(int d) { return d == 128 ? 128 : 64; }
+// log2 of the most tokens of a box.
+__host__ __device__ constexpr int key_shift_max(int d) { return d == 64 ? 6 : 7; }
+__host__ __device__ constexpr int value_shift_max(int d) { return d == 128 ? 7 : 6; }
 
 // Two fp32 lanes of one instruction.
 __device__ __forceinline__ uint64_t f2(float a, float b) {
@@ -554,256 +556,269 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
 
   if (warp >= 8) {
     set_max_regs_down<kRegsOther>();
-  if (warp == 8) {
-    // ------------------------------------------------------------ producer
+  if (warp == 8 || warp == 10) {
+    // ------------------------------------------------------------ producers
+    // Warp 8 fills the key stages (and the query tiles), warp 10 the value
+    // stages.  Uniform loops, one elected lane issues; of the cluster's CTAs
+    // each takes its share of the 64-column chunks (of the pieces at 64).
+    const bool leader = elect_one(), keys = warp == 8;
     const int ps = 1 << p.page_shift;
-    // tokens of a key box (two boxes a stage at least, one a CTA of the cluster)
-    const int kbox = min(ps, key_box_max(D)), kpieces = kKeys / kbox;
-    const uint32_t rank = CL > 1 ? blockIdx.x % CL : 0;
-    constexpr int VKEYS = kKeys / PARTS;             // keys of a value stage
-    constexpr int KCH = D == 256 ? 2 : C::kChunks;   // columns of a key stage
-    const int vbox = min(ps, value_box_max(D)), vpieces = VKEYS / vbox;
+    const int piece_shift = min(p.page_shift, keys ? key_shift_max(D) : value_shift_max(D));
+    const int piece = 1 << piece_shift;                    // tokens of a box
+    const int rank = CL > 1 ? blockIdx.x % CL : 0;
+    const int tokens = keys ? kKeys : kKeys / PARTS;       // of a stage
+    const int chunks = keys ? C::kChunks / PARTS : C::kChunks;
+    const CUtensorMap* map = keys ? &p.km : &p.vm;
     int pos = 0, qn = 0;
     bool ok = true;
-    uint32_t armed = 0, armed_par = 0, q_armed = 0, q_par = 0;
-    auto acquire = [&]() -> int {
-      const int st = pos % NS;
-      if (!mbar_wait(&empty[st], ((uint32_t)(pos / NS) & 1u) ^ 1u, abort_flag)) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
-      armed |= 1u << st;
-      armed_par = (armed_par & ~(1u << st)) | (((uint32_t)(pos / NS) & 1u) << st);
-      ++pos;
-      return st;
+    auto acquire = [&](uint64_t* bar, uint32_t parity) {
+      const bool here = mbar_wait(bar, parity, abort_flag);
+      ok = __all_sync(0xffffffffu, here);
+      return ok;
     };
     while (ok && w.next(p, g)) {
       if (g.n == 0) continue;
-      // page ids of 32 consecutive pieces of kbox keys, one a lane
-      int pid_base = -1, pid = 0;
-      auto fetch = [&](int piece) {
-        const int base = piece & ~31;
-        if (base == pid_base) return;
-        pid_base = base;
-        const int key = (base + lane) * kbox;
-        pid = p.n_pages;  // out of range: the copy reads zeros
-        if (key < g.khi) {
-          const int pg = (int)((unsigned)key >> p.page_shift);
-          // a page that ends before the first key any query sees may be gone
-          if (((pg + 1) << p.page_shift) > g.klo) {
-            const int id = __ldg(p.table + (int64_t)g.b * p.table_stride + pg);
-            if ((unsigned)id < (unsigned)p.n_pages)
-              pid = id;
-            else
-              report(p.status, kDevBounds, kSiteAttnPage, (unsigned)g.b, (unsigned)id);
+      // Page ids of 32 consecutive boxes, one a lane, and of the next 32.  An
+      // id out of range (or of a box that no query sees, whose page may be
+      // gone) becomes n_pages: the copy then reads zeros.
+      auto ids_at = [&](int base) {
+        int id = p.n_pages;
+        const int key = (base + lane) << piece_shift, pg = key >> p.page_shift;
+        if (key < g.khi && ((pg + 1) << p.page_shift) > g.klo) {
+          id = __ldg(p.table + (int64_t)g.b * p.table_stride + pg);
+          if ((unsigned)id >= (unsigned)p.n_pages) {
+            report(p.status, kDevBounds, kSiteAttnPage, (unsigned)g.b, (unsigned)id);
+            id = p.n_pages;
           }
         }
+        return id;
       };
-      fetch(g.kt0 * kpieces);
-      {
+      int base = ((g.kt0 * kKeys) >> piece_shift) & ~31;
+      int ids = ids_at(base), ids_next = ids_at(base + 32);
+      if (keys) {
         const int qb = qn % C::kQBufs;
-        if (!mbar_wait(&q_empty[qb], ((uint32_t)(qn / C::kQBufs) & 1u) ^ 1u, abort_flag)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&q_full[qb], NQ * C::kChunks * 128 * p.group * p.q_box);
-          for (int i = 0; i < NQ; ++i)
-            for (int c = 0; c < C::kChunks; ++c)
-              tma_load_3d(&p.qm, &q_full[qb],
-                          qbase + (qb * NQ + i) * C::kQTile + c * (kRows * 128), 64 * c,
-                          g.head * p.group, g.tok0 + i * p.step);
-        }
-        q_armed |= 1u << qb;
-        q_par = (q_par & ~(1u << qb)) | (((uint32_t)(qn / C::kQBufs) & 1u) << qb);
+        if (!acquire(&q_empty[qb], ((uint32_t)(qn / C::kQBufs) & 1u) ^ 1u)) break;
         ++qn;
+        if (leader) {
+          mbar_arrive_expect_tx(&q_full[qb], NQ * C::kChunks * 128 * p.group * p.q_box);
+#pragma unroll 1
+          for (int x = 0; x < NQ * C::kChunks; ++x)
+            tma_load_3d(&p.qm, &q_full[qb],
+                        qbase + qb * NQ * C::kQTile + x * (kRows * 128),
+                        64 * (x % C::kChunks), g.head * p.group, g.tok0 + x / C::kChunks * p.step);
+        }
+        __syncwarp();
       }
-      for (int j = 0; j <= g.n && ok; ++j) {
-        if (j < g.n) {  // keys of tile j
-          const int kt = g.kt0 + j;
-          fetch(kt * kpieces);
-          const int live = min(kpieces, (g.khi - kt * kKeys + kbox - 1) / kbox);
-#pragma unroll
-          for (int h = 0; h < PARTS; ++h) {
-            const int st = acquire();
-            if (!ok) break;
-            const int i = lane % kpieces, c = lane / kpieces;
-            const int id = __shfl_sync(0xffffffffu, pid, (kt * kpieces + i) & 31);
-            if (lane == 0) mbar_arrive_expect_tx(&full[st], live * kbox * 128 * KCH);
+#pragma unroll 1
+      for (int j = 0; j < g.n && ok; ++j) {
+        const int rp = pos + (keys ? k_stage<PARTS>(j) : v_stage<PARTS>(j, g.n));
+        const int key_t = (g.kt0 + j) * kKeys;
+#pragma unroll 1
+        for (int h = 0; h < PARTS; ++h) {
+          const int st = (rp + h) % NS;
+          if (!acquire(&empty[st], ((uint32_t)((rp + h) / NS) & 1u) ^ 1u)) break;
+          const int key0 = keys ? key_t : key_t + h * tokens;
+          const int live = max(0, min(tokens, (g.khi - key0 + piece - 1) & -piece));
+          if (leader) mbar_arrive_expect_tx(&full[st], live * 128 * chunks);
+#pragma unroll 1
+          for (int r = 0; r < live; r += piece) {
+            const int x = (key0 + r) >> piece_shift;
+            if (x - base >= 32) {
+              base += 32;
+              ids = ids_next;
+              ids_next = ids_at(base + 32);
+            }
+            const int id = __shfl_sync(0xffffffffu, ids, x & 31);
+            // the cluster's CTAs share the chunks, or the boxes of one chunk
+            const int c0 = chunks >= CL ? rank : 0;
+            if (leader && (chunks >= CL || x % CL == rank))
+#pragma unroll 1
+              for (int c = c0; c < chunks; c += CL)
+                tma_load_4d<CL>(map, &full[st],
+                                ring + st * C::kStageBytes + (c * tokens + r) * 128,
+                                ((keys ? h * chunks : 0) + c) * 64, g.head, (key0 + r) & (ps - 1),
+                                id);
             __syncwarp();
-            if (i < live && c < KCH && lane % CL == rank)
-              tma_load_4d<CL>(&p.km, &full[st],
-                          ring + st * C::kStageBytes + c * (kKeys * 128) + i * kbox * 128,
-                          (h * KCH + c) * 64, g.head, (kt * kKeys + i * kbox) & (ps - 1), id);
           }
         }
-        if (j > 0 && ok) {  // values of tile j - 1
-          const int kt = g.kt0 + j - 1;
-          fetch(kt * kpieces);
-#pragma unroll
-          for (int h = 0; h < PARTS; ++h) {
-            const int st = acquire();
-            if (!ok) break;
-            const int key0 = kt * kKeys + h * VKEYS;
-            const int live = max(0, min(vpieces, (g.khi - key0 + vbox - 1) / vbox));
-            if (lane == 0) mbar_arrive_expect_tx(&full[st], live * vbox * 128 * C::kChunks);
-            __syncwarp();
-            const int i = lane % vpieces, c = lane / vpieces, key = key0 + i * vbox;
-            const int id = __shfl_sync(0xffffffffu, pid, (key / kbox) & 31);
-            if (i < live && c < C::kChunks && lane % CL == rank)
-              tma_load_4d<CL>(&p.vm, &full[st],
-                          ring + st * C::kStageBytes + c * (VKEYS * 128) + i * vbox * 128, 64 * c,
-                          g.head, key & (ps - 1), id);
-          }
-        }
       }
+      pos += 2 * PARTS * g.n;
     }
     if (!ok) {
-      if (lane == 0) report(p.status, kDevTimeout, kSiteAttnLoad, (unsigned)pos, 0u);
+      if (lane == 0) report(p.status, kDevTimeout, kSiteAttnLoad, (unsigned)pos, (unsigned)warp);
       *abort_flag = 1;
     }
-    // no copy may still be landing in shared memory when the CTA exits
-    if (lane == 0) {
-      for (int i = 0; i < NS; ++i)
-        if ((armed >> i) & 1u)
-          if (!wait_drain(&full[i], (armed_par >> i) & 1u))
-            report(p.status, kDevTimeout, kSiteAttnDrain, (unsigned)i, 0u);
-      for (int i = 0; i < C::kQBufs; ++i)
-        if ((q_armed >> i) & 1u)
-          if (!wait_drain(&q_full[i], (q_par >> i) & 1u))
-            report(p.status, kDevTimeout, kSiteAttnDrain, 64u + i, 0u);
+    // No copy may still be landing in shared memory when the CTA exits: the
+    // last use of every stage and query tile.  After a timeout some of these
+    // never began; the first wait that runs out ends the list.
+    if (keys && leader) {
+      bool done = true;
+      for (int i = max(0, pos - NS); i < pos && done; ++i)
+        done = wait_drain(&full[i % NS], (uint32_t)(i / NS) & 1u);
+      for (int i = max(0, qn - C::kQBufs); i < qn && done; ++i)
+        done = wait_drain(&q_full[i % C::kQBufs], (uint32_t)(i / C::kQBufs) & 1u);
+      if (!done && ok) report(p.status, kDevTimeout, kSiteAttnDrain, 0u, 0u);
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
-    // The whole warp runs the loop, so that operands stay in uniform registers,
-    // and one elected lane issues.
-    {
-      const bool leader = elect_one();
-      int pos = 0, qn = 0, at = 0, segs = 0;  // ring position, query tiles, key tiles, segments
-      bool ok = true, issued = false;
-      auto need = [&](uint64_t* bar, uint32_t parity) {
-        if (ok) {
-          const bool here = mbar_wait(bar, parity, abort_flag);
-          ok = __all_sync(0xffffffffu, here);
-          if (!ok) {
-            if (lane == 0) report(p.status, kDevTimeout, kSiteAttnMma, (unsigned)at, smem_u32(bar));
-            *abort_flag = 1;
+    // One elected lane.  Its instructions between a wait and the MMAs that the
+    // wait releases are on the critical path of the whole CTA (with a division
+    // for the ring position and warp votes around the waits 4096 tokens behind
+    // 12288 took 690 us), so ring positions are running counters.
+    if (elect_one()) {
+      struct Cursor {
+        int st;
+        uint32_t ph;
+        __device__ __forceinline__ void add(int n) {
+          st += n;
+          if (st >= NS) {
+            st -= NS;
+            ph ^= 1u;
           }
         }
+      };
+      Cursor base{0, 0u};
+      int qb = 0, at = 0;  // query buffer, key tiles
+      uint32_t qph = 0, segs = 0;
+      bool ok = true, issued = false;
+      auto need = [&](uint64_t* bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity)) return true;
+        ok = mbar_wait(bar, parity, abort_flag);
         return ok;
       };
       while (ok && w.next(p, g)) {
         if (g.n == 0) continue;
-        const int qb = qn % C::kQBufs;
-        if (!need(&q_full[qb], (uint32_t)(qn / C::kQBufs) & 1u)) break;
-        ++qn;
-        // 16-key steps of tile j that some row sees
-        auto steps = [&](int j) {
-          return (min(kKeys, g.khi - (g.kt0 + j) * kKeys) + 15) >> 4;
-        };
-        auto scores = [&](int i, int j) {  // S_i(j) = Q_i K_j^T
-          const int rp = pos + k_stage<PARTS>(j);
+        Cursor kc = base, vc = base;
+        vc.add(g.n == 1 ? PARTS : 2 * PARTS);
+        if (!need(&q_full[qb], qph)) break;
+        const uint32_t q_lo = desc_lo(qbase + qb * NQ * C::kQTile, 16);
+        const uint32_t ring_k = desc_lo(ring, 16);
+        constexpr int SK = 8 / PARTS;  // 16-key steps of a value stage
+        const uint32_t ring_v = desc_lo(ring, SK * 2048);
+        int rem = g.khi - g.kt0 * kKeys;  // keys from the tile at hand on that some row sees
+        // S_i(j) = Q_i K_j^T for the tile under kc; `keys` of it are seen
+        auto scores = [&](int i, int j, int keys) {
           const int buf = NQ == 2 ? i : ((at + j) & 1);
           const uint32_t d = tmem + buf * 128u;
-          const uint32_t idesc = idesc_16<FP16>(128, 16 * steps(j), false);
+          const uint32_t idesc =
+              idesc_16<FP16>(128, 0, false) | ((uint32_t)min(16, (keys + 15) >> 4 << 1) << 17);
+          Cursor c = kc;
 #pragma unroll
           for (int h = 0; h < PARTS; ++h) {
-            const int st = (rp + h) % NS;
-            if (i == 0 && !need(&full[st], (uint32_t)((rp + h) / NS) & 1u)) return;
+            if (i == 0 && !need(&full[c.st], c.ph)) return;
             tc_fence_after();
             constexpr int CH = C::kChunks / PARTS;
-            const uint32_t a =
-                desc_lo(qbase + (qb * NQ + i) * C::kQTile + h * CH * (kRows * 128), 16);
-            const uint32_t b = desc_lo(ring + st * C::kStageBytes, 16);
-            if (leader) {
+            const uint32_t a = q_lo + (i * C::kQTile + h * CH * (kRows * 128)) / 16;
+            const uint32_t b = ring_k + c.st * (C::kStageBytes / 16);
 #pragma unroll
-              for (int c = 0; c < CH; ++c)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  umma_ss(d, a + (c * (kRows * 128) + 32 * k) / 16,
-                          b + (c * (kKeys * 128) + 32 * k) / 16, idesc, h | c | k);
-              if (i == NQ - 1) commit_cluster<CL>(&empty[st]);
-              if (h == PARTS - 1) {
-                umma_commit(&s_full[buf]);
-                if (i == NQ - 1 && j == g.n - 1) umma_commit(&q_empty[qb]);
-              }
-            }
-            __syncwarp();
+            for (int x = 0; x < CH * 4; ++x)
+              umma_ss(d, a + ((x >> 2) * (kRows * 128) + 32 * (x & 3)) / 16,
+                      b + ((x >> 2) * (kKeys * 128) + 32 * (x & 3)) / 16, idesc, h | x);
+            if (i == NQ - 1) commit_cluster<CL>(&empty[c.st]);
+            c.add(1);
           }
+          umma_commit(&s_full[buf]);
           issued = true;
+          if (i == NQ - 1) {
+            if (j == g.n - 1) umma_commit(&q_empty[qb]);
+            kc.add(j == 0 ? PARTS : 2 * PARTS);
+          }
         };
-        auto values = [&](int i, int j) {  // O_i += P_i(j) V_j
+        // O_i += P_i(j) V_j for the tile under vc
+        auto values = [&](int i, int j) {
           const int buf = NQ == 2 ? i : ((at + j) & 1);
           const uint32_t use = NQ == 2 ? (uint32_t)(at + j) : (uint32_t)(at + j) >> 1;
-          // NQ = 2: the first 64 keys' weights come ahead of the others'
-          if (!need(NQ == 2 ? &p_half[buf] : &p_full[buf], use & 1u)) return;
-          if (j == 0 && !need(&o_empty[i], ((uint32_t)segs & 1u) ^ 1u)) return;
-          const int rp = pos + v_stage<PARTS>(j, g.n);
           const uint32_t d = tmem + C::kO + i * D;
           const uint32_t a = tmem + buf * 128u;
-          const uint32_t idesc = idesc_16<FP16>(128, D, true);
-          const int ks = steps(j);
-          constexpr int SK = 8 / PARTS;  // k steps a stage
+          constexpr uint32_t idesc = idesc_16<FP16>(128, D, true);
+          Cursor c = vc;
+          // NQ = 2: the first 64 keys' weights come ahead of the others'
+          if (!need(NQ == 2 ? &p_half[buf] : &p_full[buf], use & 1u)) return;
+          if (j == 0 && !need(&o_empty[i], (segs & 1u) ^ 1u)) return;
+          if (i == 0 && !need(&full[c.st], c.ph)) return;
+          tc_fence_after();
+          if (rem >= kKeys) {
 #pragma unroll
-          for (int h = 0; h < PARTS; ++h) {
-            const int st = (rp + h) % NS;
-            if (i == 0 && !need(&full[st], (uint32_t)((rp + h) / NS) & 1u)) return;
-            tc_fence_after();
-            // one 64-column chunk of V to the next: SK steps of 16 rows
-            const uint32_t b = desc_lo(ring + st * C::kStageBytes, SK * 2048);
-            if (leader) {
-              if (j == 0 && h == 0) umma_ts(d, a, b, idesc, 0);
-              else if (h * SK < ks) umma_ts(d, a + 8 * h * SK, b, idesc, 1);
-            }
-            constexpr int S0 = NQ == 2 ? SK / 2 : SK;  // steps before the second wait
-            auto more = [&](int k0, int k1) {
-              if (ks >= h * SK + k1) {
-#pragma unroll
-                for (int k = 1; k < SK; ++k)
-                  if (k >= k0 && k < k1)
-                    umma_ts(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc, 1);
-              } else {
-                for (int k = k0; h * SK + k < ks; ++k)
-                  umma_ts(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc, 1);
+            for (int h = 0; h < PARTS; ++h) {
+              if (h > 0 && i == 0) {
+                if (!need(&full[c.st], c.ph)) return;
+                tc_fence_after();
               }
-            };
-            if (leader) more(1, S0);
+              const uint32_t b = ring_v + c.st * (C::kStageBytes / 16);
+#pragma unroll
+              for (int k = 0; k < SK; ++k) {
+                if (NQ == 2 && h * SK + k == 4) {
+                  if (!need(&p_full[buf], use & 1u)) return;
+                  tc_fence_after();
+                }
+                umma_ts(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc,
+                        h + k == 0 ? j != 0 : 1);
+              }
+              if (i == NQ - 1) commit_cluster<CL>(&empty[c.st]);
+              c.add(1);
+            }
+          } else {  // the item's last keys: only their 16-key steps
             if (NQ == 2) {
-              __syncwarp();
               if (!need(&p_full[buf], use & 1u)) return;
               tc_fence_after();
             }
-            if (leader) {
-              if (S0 < SK) more(S0, SK);
-              if (i == NQ - 1) commit_cluster<CL>(&empty[st]);
-              if (h == PARTS - 1) {
-                umma_commit(&pv_done[i]);
-                if (j == g.n - 1) umma_commit(&o_full[i]);
+            const int ks = (rem + 15) >> 4;
+#pragma unroll 1
+            for (int h = 0; h < PARTS; ++h) {
+              if (h > 0 && i == 0) {
+                if (!need(&full[c.st], c.ph)) return;
+                tc_fence_after();
               }
+              const uint32_t b = ring_v + c.st * (C::kStageBytes / 16);
+#pragma unroll 1
+              for (int k = 0; k < SK && h * SK + k < ks; ++k)
+                umma_ts(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc, j | h | k);
+              if (i == NQ - 1) commit_cluster<CL>(&empty[c.st]);
+              c.add(1);
             }
-            __syncwarp();
+          }
+          umma_commit(&pv_done[i]);
+          if (j == g.n - 1) umma_commit(&o_full[i]);
+          if (i == NQ - 1) {
+            if (j == g.n - 1) {
+              base = vc;
+              base.add(PARTS);
+            }
+            vc.add(j + 1 < g.n - 1 ? 2 * PARTS : PARTS);
+            rem -= kKeys;
           }
         };
         if (NQ == 2) {
-          scores(0, 0);
-          if (ok) scores(1, 0);
-          for (int j = 0; j < g.n && ok; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (ok) values(i, j);
-              if (ok && j + 1 < g.n) scores(i, j + 1);
-            }
+          scores(0, 0, rem);
+          if (ok) scores(1, 0, rem);
+          for (int j = 0; j < g.n && ok; ++j) {
+            const int next = rem - kKeys;
+            values(0, j);
+            if (ok && j + 1 < g.n) scores(0, j + 1, next);
+            if (ok) values(1, j);
+            if (ok && j + 1 < g.n) scores(1, j + 1, next);
+          }
         } else {
-          scores(0, 0);
-          if (ok && g.n > 1) scores(0, 1);
+          scores(0, 0, rem);
+          if (ok && g.n > 1) scores(0, 1, rem - kKeys);
           for (int j = 0; j < g.n && ok; ++j) {
             values(0, j);
-            if (ok && j + 2 < g.n) scores(0, j + 2);
+            if (ok && j + 2 < g.n) scores(0, j + 2, rem - kKeys);
           }
         }
-        pos += 2 * PARTS * g.n;
         at += g.n;
         ++segs;
+        if (++qb == C::kQBufs) {
+          qb = 0;
+          qph ^= 1u;
+        }
+      }
+      if (!ok) {
+        report(p.status, kDevTimeout, kSiteAttnMma, (unsigned)at, segs);
+        *abort_flag = 1;
       }
       // every MMA issued here must have completed before TMEM is released
-      if (issued && leader) {
+      if (issued) {
         umma_commit(&drain);
         if (!wait_drain(&drain, 0u)) report(p.status, kDevTimeout, kSiteAttnDrain, 99u, 0u);
       }
@@ -1314,7 +1329,8 @@ dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const 
     if (!encode_tiled(&p.qm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, q->p, dims, strides, box))
       return DG_ERR_CUDA;
   }
-  const int ps = c.page_size, kmax = key_box_max(c.head_dim), vmax = value_box_max(c.head_dim);
+  const int ps = c.page_size, kmax = 1 << key_shift_max(c.head_dim),
+            vmax = 1 << value_shift_max(c.head_dim);
   const uint32_t kbox = ps < kmax ? ps : kmax, vbox = ps < vmax ? ps : vmax;
   if (!encode_pages(&p.km, c, c.k, layer, kbox) || !encode_pages(&p.vm, c, c.v, layer, vbox))
     return DG_ERR_CUDA;
