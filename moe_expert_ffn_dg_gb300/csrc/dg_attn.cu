@@ -908,35 +908,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             ++xn;
           }
           const float mt = mx * p.scale2;
-          float fac = 1.f;
-          if (mt > m) {
-            if (m == -INFINITY) {
-              m = mt;
-            } else if (mt > m + 8.f) {
-              fac = exp2_fast(m - mt);
-              m = mt;
-              l *= fac;
-            }
-          }
-          if (j > 0 && __any_sync(0xffffffffu, fac != 1.f)) {
-            // O holds the tiles before this one once their product is done.
-            // The products before that one are: S of this tile was issued
-            // after them, so the barrier is at most one phase behind.
-            bool here = mbar_wait(&pv_done[i], (uint32_t)(at + j - 1) & 1u, abort_flag);
-            here = __all_sync(0xffffffffu, here);
-            if (!here) {
-              ok = false;
-              if (NQ == 2) break;
-            }
-            tc_fence_after();
+          // also true of the first key that a row sees (m is -inf before it)
+          const bool grown = mt > m + 8.f;
+          if (__any_sync(0xffffffffu, grown)) {
+            const float fac = grown && m != -INFINITY ? exp2_fast(m - mt) : 1.f;
+            if (grown) m = mt;
+            l *= fac;
+            if (j > 0 && __any_sync(0xffffffffu, fac != 1.f)) {
+              // O holds the tiles before this one once their product is done.
+              // The products before that one are: S of this tile was issued
+              // after them, so the barrier is at most one phase behind.
+              bool here = mbar_wait(&pv_done[i], (uint32_t)(at + j - 1) & 1u, abort_flag);
+              here = __all_sync(0xffffffffu, here);
+              if (!here) {
+                ok = false;
+                if (NQ == 2) break;
+              }
+              tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < OC; c += 16) {
-              float o[16];
-              uint32_t r[16];
-              tmem_ld16(tl + C::kO + i * D + o0 + c, o);
+              for (int c = 0; c < OC; c += 16) {
+                float o[16];
+                uint32_t r[16];
+                tmem_ld16(tl + C::kO + i * D + o0 + c, o);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(o[e] * fac);
-              tmem_store16(tl + C::kO + i * D + o0 + c, r);
+                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(o[e] * fac);
+                tmem_store16(tl + C::kO + i * D + o0 + c, r);
+              }
             }
           }
           const float mr = m == -INFINITY ? 0.f : m;
