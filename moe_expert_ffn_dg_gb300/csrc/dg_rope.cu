@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 32;  // tokens of a block
-constexpr int kUnits = 4;       // units a thread holds in flight
+constexpr int kUnits = 2;       // units a thread holds in flight
 
 enum : unsigned int { kSiteAppendPos = 40, kSiteAppendPage = 41 };
 
@@ -37,17 +37,21 @@ struct Part {
   const void* src;
   void* dst;
   int64_t s_tok, s_head, d_tok, d_head, d_page;
-  int first;   // first unit of a token that belongs to this part
-  int units;   // units of a head
-  int pairs;   // of which this many rotate, the others copy
-  int paged;   // rows of dst are (page, token of the page)
+  int rotated;  // else copied
+  int paged;    // rows of dst are (page, token of the page)
 };
 
 struct RopeParams {
   Part part[3];
-  int n_parts, units;  // units of a token
+  int first[2];  // first head of parts 1 and 2 among the heads of a token
+  int heads;     // of a token, all parts
+  // Units of a head: vector path: two 16-byte vectors; else one pair or
+  // element.  unit_magic, head_magic: ceil(2^32 / x) for quotients of small
+  // numbers.
+  int units;
+  uint32_t unit_magic, head_magic;
   int n_tokens, per_block;
-  int half, interleaved, grad;
+  int dim, half, interleaved, grad;
   float amplitude;
   const int32_t* positions;
   const int32_t* table;  // null: no cache
@@ -124,11 +128,19 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int n, int tok, int l
   return (__ldg(cu + lo) <= tok && tok < __ldg(cu + lo + 1)) ? lo : -1;
 }
 
-// VEC: a unit is 16 bytes of a head (or, rotated in the half layout, the two
-// 16-byte vectors of eight pairs); else one pair or one copied element.
+// Quotient by d with its magic number m: exact while x (m d - 2^32) < 2^32, and
+// m d - 2^32 < d.
+__device__ __forceinline__ int quot(int x, uint32_t magic) {
+  return magic ? (int)__umulhi((uint32_t)x, magic) : x;  // 0: divisor 1
+}
+
+// VEC: a unit is two 16-byte vectors of a head: in the half layout the two
+// halves of eight (four) pairs, else, and where nothing rotates, neighbours.
+// Otherwise a unit is one pair or one copied element.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeParams p) {
-  constexpr int N = VEC ? Vec<T>::N : 1;
+__global__ void __launch_bounds__(kThreads, VEC ? 6 : 4)
+    k_rope(const __grid_constant__ RopeParams p) {
+  constexpr int N = Vec<T>::N;
   extern __shared__ float2 cs[];  // [per_block][half] cosine and sine
   __shared__ int s_pos[kMaxTokens], s_page[kMaxTokens], s_rot[kMaxTokens];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -136,118 +148,125 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeP
   pdl_wait();
   const int t0 = blockIdx.x * p.per_block;
   const int nt = min(p.per_block, p.n_tokens - t0);
-  const int units = nt * p.units;
+  const int total = nt * p.heads * p.units;
 
   struct Unit {
-    int tok, part, head, u;
+    int tok, head, u;  // head among those of the token
   };
   auto locate = [&](int x) {
     Unit a;
-    a.tok = x / p.units;
-    int r = x - a.tok * p.units;
-    a.part = 0;
-    if (p.n_parts > 1 && r >= p.part[1].first) a.part = 1;
-    if (p.n_parts > 2 && r >= p.part[2].first) a.part = 2;
-    const Part& q = p.part[a.part];
-    r -= q.first;
-    a.head = r / q.units;
-    a.u = r - a.head * q.units;
+    const int row = quot(x, p.unit_magic);
+    a.u = x - row * p.units;
+    a.tok = quot(row, p.head_magic);
+    a.head = row - a.tok * p.heads;
     return a;
   };
-  // first element of a unit, and of its second vector / element (rotated
-  // pairs of the half layout; scalar pairs)
-  auto place = [&](const Unit& a, int& e0, int& e1) {
-    const Part& q = p.part[a.part];
-    if (a.u >= q.pairs) {
-      const int skip = (!VEC || !p.interleaved) ? 2 * q.pairs * N : q.pairs * N;
-      e0 = skip + (a.u - q.pairs) * N;
-      e1 = -1;
-    } else if (p.interleaved) {
-      e0 = VEC ? a.u * N : 2 * a.u;
-      e1 = VEC ? -1 : e0 + 1;
-    } else {
-      e0 = a.u * N;
-      e1 = p.half + e0;
+  auto part_of = [&](Unit& a) -> const Part& {
+    const int i = (a.head >= p.first[0]) + (a.head >= p.first[1]);
+    a.head -= i == 0 ? 0 : p.first[i - 1];
+    return p.part[i];
+  };
+  // first elements of a unit's two vectors (scalars; e1 < 0: only one), and
+  // whether they rotate
+  auto place = [&](const Part& q, int u, int& e0, int& e1) {
+    const int half = q.rotated ? p.half : 0;
+    if (VEC) {
+      if (!p.interleaved && u * N < half) {
+        e0 = u * N;
+        e1 = e0 + half;
+        return true;
+      }
+      e0 = 2 * u * N;
+      e1 = e0 + N;
+      return p.interleaved && e0 < 2 * half;
     }
+    if (u < half) {
+      e0 = p.interleaved ? 2 * u : u;
+      e1 = p.interleaved ? e0 + 1 : half + u;
+      return true;
+    }
+    e0 = half + u;
+    e1 = -1;
+    // heads of more units than a copied one has
+    if (e0 >= p.dim) e0 = -1;
+    return false;
   };
 
   uint4 va[kUnits], vb[kUnits];
-  float fa[kUnits], fb[kUnits];
-  auto load = [&](int i, const Unit& a) {
-    const Part& q = p.part[a.part];
+  auto load = [&](int i, Unit a) {
+    const Part& q = part_of(a);
     const T* src = static_cast<const T*>(q.src) + (int64_t)(t0 + a.tok) * q.s_tok +
                    (int64_t)a.head * q.s_head;
     int e0, e1;
-    place(a, e0, e1);
+    place(q, a.u, e0, e1);
     if (VEC) {
-      va[i] = *reinterpret_cast<const uint4*>(src + e0);
-      if (e1 >= 0) vb[i] = *reinterpret_cast<const uint4*>(src + e1);
+      va[i] = __ldcs(reinterpret_cast<const uint4*>(src + e0));
+      vb[i] = __ldcs(reinterpret_cast<const uint4*>(src + e1));
     } else {
-      fa[i] = get(src + e0);
-      if (e1 >= 0) fb[i] = get(src + e1);
+      if (e0 >= 0) va[i].x = __float_as_uint(get(src + e0));
+      if (e1 >= 0) vb[i].x = __float_as_uint(get(src + e1));
     }
   };
-  auto finish = [&](int i, const Unit& a) {
-    const Part& q = p.part[a.part];
-    T* dst;
+  auto finish = [&](int i, Unit a) {
+    const Part& q = part_of(a);
+    T* dst = static_cast<T*>(q.dst) + (int64_t)a.head * q.d_head;
     if (q.paged) {
       const int page = s_page[a.tok];
       if (page < 0) return;
-      dst = static_cast<T*>(q.dst) + (int64_t)page * q.d_page +
-            (int64_t)(s_pos[a.tok] & ((1 << p.page_shift) - 1)) * q.d_tok +
-            (int64_t)a.head * q.d_head;
+      dst += (int64_t)page * q.d_page +
+             (int64_t)(s_pos[a.tok] & ((1 << p.page_shift) - 1)) * q.d_tok;
     } else {
       if (p.table && s_page[a.tok] == -2) return;  // outside every sequence
-      dst = static_cast<T*>(q.dst) + (int64_t)(t0 + a.tok) * q.d_tok + (int64_t)a.head * q.d_head;
+      dst += (int64_t)(t0 + a.tok) * q.d_tok;
     }
     int e0, e1;
-    place(a, e0, e1);
+    const bool rot = place(q, a.u, e0, e1);
+    const float2* c = cs + a.tok * p.half;
     if (VEC) {
-      if (a.u < q.pairs) {
-        const float2* c = cs + a.tok * p.half;
-        float x[Vec<T>::N];
+      if (rot) {
+        float x[N], y[N];
         unpack<T>(va[i], x);
+        unpack<T>(vb[i], y);
         if (p.interleaved) {
+          c += e0 >> 1;
 #pragma unroll
-          for (int k = 0; k < Vec<T>::N; k += 2) {
-            const float2 w = c[(e0 + k) >> 1];
-            const float y0 = fmaf(x[k], w.x, -x[k + 1] * w.y);
+          for (int k = 0; k < N; k += 2) {
+            const float2 w = c[k >> 1], z = c[(N + k) >> 1];
+            const float x0 = fmaf(x[k], w.x, -x[k + 1] * w.y);
+            const float y0 = fmaf(y[k], z.x, -y[k + 1] * z.y);
             x[k + 1] = fmaf(x[k + 1], w.x, x[k] * w.y);
-            x[k] = y0;
+            y[k + 1] = fmaf(y[k + 1], z.x, y[k] * z.y);
+            x[k] = x0;
+            y[k] = y0;
           }
         } else {
-          float y[Vec<T>::N];
-          unpack<T>(vb[i], y);
+          c += e0;
 #pragma unroll
-          for (int k = 0; k < Vec<T>::N; ++k) {
-            const float2 w = c[e0 + k];
-            const float y0 = fmaf(x[k], w.x, -y[k] * w.y);
+          for (int k = 0; k < N; ++k) {
+            const float2 w = c[k];
+            const float x0 = fmaf(x[k], w.x, -y[k] * w.y);
             y[k] = fmaf(y[k], w.x, x[k] * w.y);
-            x[k] = y0;
+            x[k] = x0;
           }
-          *reinterpret_cast<uint4*>(dst + e1) = pack<T>(y);
         }
         va[i] = pack<T>(x);
+        vb[i] = pack<T>(y);
       }
       *reinterpret_cast<uint4*>(dst + e0) = va[i];
-    } else if (e1 < 0) {
-      put(dst + e0, fa[i]);
-    } else {
-      const float2 w = cs[a.tok * p.half + a.u];
-      put(dst + e0, fmaf(fa[i], w.x, -fb[i] * w.y));
-      put(dst + e1, fmaf(fb[i], w.x, fa[i] * w.y));
+      *reinterpret_cast<uint4*>(dst + e1) = vb[i];
+    } else if (rot) {
+      const float2 w = c[a.u];
+      const float x = __uint_as_float(va[i].x), y = __uint_as_float(vb[i].x);
+      put(dst + e0, fmaf(x, w.x, -y * w.y));
+      put(dst + e1, fmaf(y, w.x, x * w.y));
+    } else if (e0 >= 0) {
+      put(dst + e0, __uint_as_float(va[i].x));
     }
   };
 
-  Unit un[kUnits];
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const int x = tid + i * kThreads;
-    if (x < units) {
-      un[i] = locate(x);
-      load(i, un[i]);
-    }
-  }
+  for (int i = 0; i < kUnits; ++i)
+    if (tid + i * kThreads < total) load(i, locate(tid + i * kThreads));
   if (p.table) {
     for (int t = warp; t < nt; t += kThreads / 32) {
       const int s = find_seq(p.cu, p.n_seqs, t0 + t, lane);
@@ -273,13 +292,11 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeP
       }
     }
     __syncthreads();
-  } else if (tid < nt) {
-    s_rot[tid] = __ldg(p.positions + t0 + tid);
   }
-  if (!p.table) __syncthreads();
   for (int x = tid; x < nt * p.half; x += kThreads) {
     const int t = x / p.half, i = x - t * p.half;
-    const uint64_t a = p.turn[i] * (uint64_t)(int64_t)s_rot[t];
+    const int pos = p.table ? s_rot[t] : __ldg(p.positions + t0 + t);
+    const uint64_t a = p.turn[i] * (uint64_t)(int64_t)pos;
     float s, c;
     sincospif((float)(int32_t)(a >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
     cs[x] = make_float2(c * p.amplitude, (p.grad ? -s : s) * p.amplitude);
@@ -287,29 +304,23 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeP
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kUnits; ++i)
-    if (tid + i * kThreads < units) finish(i, un[i]);
-  for (int x0 = tid + kUnits * kThreads; x0 < units; x0 += kUnits * kThreads) {
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int x = x0 + i * kThreads;
-      if (x < units) {
-        un[i] = locate(x);
-        load(i, un[i]);
-      }
-    }
+    if (tid + i * kThreads < total) finish(i, locate(tid + i * kThreads));
+  for (int x0 = tid + kUnits * kThreads; x0 < total; x0 += kUnits * kThreads) {
 #pragma unroll
     for (int i = 0; i < kUnits; ++i)
-      if (x0 + i * kThreads < units) finish(i, un[i]);
+      if (x0 + i * kThreads < total) load(i, locate(x0 + i * kThreads));
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+      if (x0 + i * kThreads < total) finish(i, locate(x0 + i * kThreads));
   }
 }
 
-// Whether every part can be moved in 16-byte vectors.
+// Whether every part can be moved in pairs of 16-byte vectors.
 template <typename T>
-bool vector_ok(const RopeParams& p, int dim, int rot) {
+bool vector_ok(const RopeParams& p, int n_parts, int dim, int rot) {
   const int n = Vec<T>::N;
-  if (dim % n) return false;
-  if (rot && (p.interleaved ? rot % n : (rot / 2) % n)) return false;
-  for (int i = 0; i < p.n_parts; ++i) {
+  if (dim % (2 * n) || rot % (2 * n)) return false;
+  for (int i = 0; i < n_parts; ++i) {
     const Part& q = p.part[i];
     if (!aligned(q.src, 16) || !aligned(q.dst, 16)) return false;
     for (const int64_t s : {q.s_tok, q.s_head, q.d_tok, q.d_head, q.d_page})
@@ -318,26 +329,32 @@ bool vector_ok(const RopeParams& p, int dim, int rot) {
   return true;
 }
 
-// heads[i], rotated[i]: of part i.
+// The quotients by magic numbers are exact for this many.
+bool heads_ok(int heads, int dim) { return heads <= 16384 && (int64_t)heads * dim <= 1 << 22; }
+
+uint32_t magic_of(int d) { return d <= 1 ? 0 : (uint32_t)((((uint64_t)1 << 32) + d - 1) / d); }
+
 template <typename T>
-cudaError_t launch(RopeParams& p, const int* heads, const bool* rotated, int dim, int rot,
+cudaError_t launch(RopeParams& p, int n_parts, const int* heads, int dim, int rot,
                    cudaStream_t s) {
-  const bool vec = vector_ok<T>(p, dim, rot);
-  const int n = vec ? Vec<T>::N : 1;
+  const bool vec = vector_ok<T>(p, n_parts, dim, rot);
+  bool copies = false;
+  for (int i = 0; i < n_parts; ++i) copies = copies || !p.part[i].rotated;
+  p.dim = dim;
   p.half = rot / 2;
-  p.units = 0;
-  for (int i = 0; i < p.n_parts; ++i) {
-    Part& q = p.part[i];
-    const int r = rotated[i] ? rot : 0;
-    // rotated units: vectors of an interleaved head, else (vectors of) pairs
-    q.pairs = vec && p.interleaved ? r / n : r / 2 / n;
-    q.units = q.pairs + (dim - r) / n;
-    q.first = p.units;
-    p.units += heads[i] * q.units;
+  p.units = vec ? dim / (2 * Vec<T>::N) : (copies ? dim : dim - p.half);
+  p.heads = 0;
+  for (int i = 0; i < n_parts; ++i) {
+    if (i) p.first[i - 1] = p.heads;
+    p.heads += heads[i];
   }
-  // About three units a thread, but several blocks an SM (of 152) before a
+  for (int i = n_parts; i < 3; ++i) p.first[i - 1] = p.heads;  // nothing from here on
+  p.unit_magic = magic_of(p.units);
+  p.head_magic = magic_of(p.heads);
+  // About kUnits units a thread, but several blocks an SM (of 152) before a
   // block takes more than one token, and at most 32 KB of cosines.
-  int per = p.units > 0 ? 3 * kThreads / p.units : 1;
+  const int64_t token_units = (int64_t)p.heads * p.units;
+  int per = (int)(kUnits * kThreads / token_units);
   const int spread = p.n_tokens / (152 * 4);
   if (per > spread) per = spread;
   if (per > kMaxTokens) per = kMaxTokens;
@@ -424,21 +441,19 @@ dg_status_t dg_rope_apply(const dg_rope_t* r, dg_dtype_t dtype, const dg_heads_t
     return st;
   if (!positions) return DG_ERR_INVALID_ARG;
   if (!aligned(positions, 4)) return DG_ERR_ALIGNMENT;
-  if ((int64_t)n_heads * r->cfg.head_dim > (1 << 24)) return DG_ERR_UNSUPPORTED;
+  if (!heads_ok(n_heads, r->cfg.head_dim)) return DG_ERR_UNSUPPORTED;
   RopeParams p = {};
   set_rope(p, r);
-  p.n_parts = 1;
   p.part[0] = Part{x->p, out->p, x->token_stride, x->head_stride, out->token_stride,
-                   out->head_stride, 0, 0, 0, 0, 0};
+                   out->head_stride, 0, 1, 0};
   p.n_tokens = n_tokens;
   p.grad = grad != 0;
   p.positions = positions;
-  const bool rot = true;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int d = r->cfg.head_dim, rd = r->cfg.rot_dim;
-  const cudaError_t e = dtype == DG_T_BF16   ? launch<__nv_bfloat16>(p, &n_heads, &rot, d, rd, s)
-                        : dtype == DG_T_FP16 ? launch<__half>(p, &n_heads, &rot, d, rd, s)
-                                             : launch<float>(p, &n_heads, &rot, d, rd, s);
+  const cudaError_t e = dtype == DG_T_BF16   ? launch<__nv_bfloat16>(p, 1, &n_heads, d, rd, s)
+                        : dtype == DG_T_FP16 ? launch<__half>(p, 1, &n_heads, d, rd, s)
+                                             : launch<float>(p, 1, &n_heads, d, rd, s);
   return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 
@@ -457,7 +472,7 @@ dg_status_t dg_kv_append(dg_kv_t* kv, int layer, const dg_rope_t* rope, const dg
   if ((st = check_heads(k)) != DG_OK || (st = check_heads(v)) != DG_OK) return st;
   if (q) {
     if (n_q_heads <= 0) return DG_ERR_INVALID_ARG;
-    if ((int64_t)n_q_heads * c.head_dim > (1 << 24)) return DG_ERR_UNSUPPORTED;
+    if (!heads_ok(n_q_heads, c.head_dim)) return DG_ERR_UNSUPPORTED;
     if ((st = check_heads(q)) != DG_OK || (st = check_heads(q_out)) != DG_OK) return st;
   }
   if (!batch->page_table) return DG_ERR_INVALID_ARG;
@@ -465,20 +480,18 @@ dg_status_t dg_kv_append(dg_kv_t* kv, int layer, const dg_rope_t* rope, const dg
   RopeParams p = {};
   p.amplitude = 1.f;
   if (rope) set_rope(p, rope);
-  int heads[3];
-  bool rotated[3];
+  int heads[3], parts = 0;
   auto add = [&](const dg_heads_t* src, int n, bool rot, const dg_kv_pool_t* pool,
                  const dg_heads_t* dst) {
-    const int i = p.n_parts++;
-    heads[i] = n;
-    rotated[i] = rot;
+    heads[parts] = n;
     if (pool)
-      p.part[i] = Part{src->p, static_cast<uint16_t*>(pool->p) + layer * pool->layer_stride,
-                       src->token_stride, src->head_stride, pool->token_stride,
-                       pool->head_stride, pool->page_stride, 0, 0, 0, 1};
+      p.part[parts] = Part{src->p, static_cast<uint16_t*>(pool->p) + layer * pool->layer_stride,
+                           src->token_stride, src->head_stride, pool->token_stride,
+                           pool->head_stride, pool->page_stride, rot, 1};
     else
-      p.part[i] = Part{src->p, dst->p, src->token_stride, src->head_stride, dst->token_stride,
-                       dst->head_stride, 0, 0, 0, 0, 0};
+      p.part[parts] = Part{src->p, dst->p, src->token_stride, src->head_stride,
+                           dst->token_stride, dst->head_stride, 0, rot, 0};
+    ++parts;
   };
   add(k, c.n_kv_heads, rope != nullptr, &c.k, nullptr);
   add(v, c.n_kv_heads, false, &c.v, nullptr);
@@ -497,8 +510,8 @@ dg_status_t dg_kv_append(dg_kv_t* kv, int layer, const dg_rope_t* rope, const dg
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int rd = rope ? rope->cfg.rot_dim : 0;
   const cudaError_t e = c.dtype == DG_T_BF16
-                            ? launch<__nv_bfloat16>(p, heads, rotated, c.head_dim, rd, s)
-                            : launch<__half>(p, heads, rotated, c.head_dim, rd, s);
+                            ? launch<__nv_bfloat16>(p, parts, heads, c.head_dim, rd, s)
+                            : launch<__half>(p, parts, heads, c.head_dim, rd, s);
   return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 
