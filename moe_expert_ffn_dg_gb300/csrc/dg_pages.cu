@@ -162,6 +162,7 @@ MoveParams move_params(const dg_kv* kv) {
 constexpr int kForkCtas = 8;
 constexpr int kForkThreads = 1024;
 constexpr int kForkMax = 4096;  // sequences
+constexpr int kBatch = 8;       // loads in flight a thread: the loops wait for memory
 
 struct ForkParams {
   dg_kv_fork_t f;
@@ -237,6 +238,7 @@ __global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kForkThreads
     }
   }
   if (f.ref_out != f.ref_in)
+#pragma unroll 8
     for (int i = gt; i < f.n_pages; i += kAll) f.ref_out[i] = __ldg(f.ref_in + i);
   cluster_sync();
 
@@ -248,12 +250,20 @@ __global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kForkThreads
     if (lane == 0 && (raw < 0 || raw > (int64_t)f.row << shift))
       report(p.status, kDevBounds, kSiteForkLen, (unsigned)s, (unsigned)raw);
     if (d == 0) continue;
-    for (int i = lane; i < pages; i += 32) {
-      const int id = __ldg(f.table_in + (int64_t)s * f.row + i);
-      if ((unsigned)id < (unsigned)f.n_pages)
-        atomicAdd(f.ref_out + id, d);
-      else
-        report(p.status, kDevBounds, kSiteForkPage, (unsigned)s, (unsigned)id);
+    const int32_t* held = f.table_in + (int64_t)s * f.row;
+    for (int i0 = lane; i0 < pages; i0 += 32 * kBatch) {
+      int id[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        id[k] = i0 + 32 * k < pages ? __ldg(held + i0 + 32 * k) : 0;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (i0 + 32 * k >= pages) break;
+        if ((unsigned)id[k] < (unsigned)f.n_pages)
+          atomicAdd(f.ref_out + id[k], d);
+        else
+          report(p.status, kDevBounds, kSiteForkPage, (unsigned)s, (unsigned)id[k]);
+      }
     }
   }
   for (int j = gt; j < f.n_new; j += kAll) {
@@ -317,12 +327,16 @@ __global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kForkThreads
   // free pages of this CTA's share, one contiguous run a warp
   const int run = (f.n_pages + kWarps - 1) / kWarps;
   const int p0 = min((int64_t)gw * run, (int64_t)f.n_pages), p1 = min(p0 + run, f.n_pages);
-  int nfree = 0;
-  for (int i = p0 + lane; i < p1; i += 32) {
-    const int r = __ldcg(f.ref_out + i);
-    nfree += r == 0;
-    if (r < 0) report(p.status, kDevBounds, kSiteForkRef, (unsigned)i, (unsigned)r);
+  int nfree = 0, least = 0;
+  for (int i0 = p0 + lane; i0 < p1; i0 += 32 * kBatch) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int r = i0 + 32 * k < p1 ? __ldcg(f.ref_out + i0 + 32 * k) : 1;
+      nfree += r == 0;
+      least = min(least, r);
+    }
   }
+  if (least < 0) report(p.status, kDevBounds, kSiteForkRef, (unsigned)p0, (unsigned)least);
   nfree = __reduce_add_sync(0xffffffffu, nfree);
   if (lane == 0) warp_free[warp] = nfree;
   __syncthreads();
@@ -350,16 +364,21 @@ __global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kForkThreads
     const bool sp = ok && split[j];
     const int stay = g.pages - (sp ? 1 : 0);
     const int want = ok ? (g.have + g.grow + ps - 1) >> shift : g.pages;
-    for (int i = lane; i < f.row; i += 32) {
-      int id = -1;
-      if (i < stay) {
-        id = __ldg(f.table_in + (int64_t)g.parent * f.row + i);
-        if ((unsigned)id >= (unsigned)f.n_pages) {
-          report(p.status, kDevBounds, kSiteForkPage, (unsigned)g.parent, (unsigned)id);
-          id = -1;
+    const int32_t* held = f.table_in + (int64_t)g.parent * f.row;
+    for (int i0 = lane; i0 < f.row; i0 += 32 * kBatch) {
+      int id[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) id[k] = i0 + 32 * k < stay ? __ldg(held + i0 + 32 * k) : -1;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + 32 * k;
+        if (i >= f.row) break;
+        if (i < stay && (unsigned)id[k] >= (unsigned)f.n_pages) {
+          report(p.status, kDevBounds, kSiteForkPage, (unsigned)g.parent, (unsigned)id[k]);
+          id[k] = -1;
         }
+        if (i < stay || i >= want) f.table_out[(int64_t)j * f.row + i] = id[k];
       }
-      if (i < stay || i >= want) f.table_out[(int64_t)j * f.row + i] = id;
     }
     if (lane == 0) {
       f.lens_out[j] = g.have + (ok ? g.grow : 0);

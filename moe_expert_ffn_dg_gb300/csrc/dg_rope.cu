@@ -141,7 +141,12 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads, VEC ? 6 : 4)
     k_rope(const __grid_constant__ RopeParams p) {
   constexpr int N = Vec<T>::N;
-  extern __shared__ float2 cs[];  // [per_block][half] cosine and sine
+  // Cosines and sines of the block's tokens.  Pair i of a token lies at column
+  // i / PAIRS of row i % PAIRS: the threads of neighbouring units read
+  // neighbouring places (in the order of the pairs they met in the same banks:
+  // an append of 64 canvases took 119 us).
+  constexpr int PAIRS = VEC ? N : 1;  // of a unit
+  extern __shared__ float2 cs[];
   __shared__ int s_pos[kMaxTokens], s_page[kMaxTokens], s_rot[kMaxTokens];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
@@ -221,17 +226,17 @@ __global__ void __launch_bounds__(kThreads, VEC ? 6 : 4)
     }
     int e0, e1;
     const bool rot = place(q, a.u, e0, e1);
-    const float2* c = cs + a.tok * p.half;
+    const float2* c = cs + a.tok * p.half + a.u;
+    const int cols = p.half / PAIRS;
     if (VEC) {
       if (rot) {
         float x[N], y[N];
         unpack<T>(va[i], x);
         unpack<T>(vb[i], y);
         if (p.interleaved) {
-          c += e0 >> 1;
 #pragma unroll
           for (int k = 0; k < N; k += 2) {
-            const float2 w = c[k >> 1], z = c[(N + k) >> 1];
+            const float2 w = c[(k >> 1) * cols], z = c[((N + k) >> 1) * cols];
             const float x0 = fmaf(x[k], w.x, -x[k + 1] * w.y);
             const float y0 = fmaf(y[k], z.x, -y[k + 1] * z.y);
             x[k + 1] = fmaf(x[k + 1], w.x, x[k] * w.y);
@@ -240,10 +245,9 @@ __global__ void __launch_bounds__(kThreads, VEC ? 6 : 4)
             y[k] = y0;
           }
         } else {
-          c += e0;
 #pragma unroll
           for (int k = 0; k < N; ++k) {
-            const float2 w = c[k];
+            const float2 w = c[k * cols];
             const float x0 = fmaf(x[k], w.x, -y[k] * w.y);
             y[k] = fmaf(y[k], w.x, x[k] * w.y);
             x[k] = x0;
@@ -255,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, VEC ? 6 : 4)
       *reinterpret_cast<uint4*>(dst + e0) = va[i];
       *reinterpret_cast<uint4*>(dst + e1) = vb[i];
     } else if (rot) {
-      const float2 w = c[a.u];
+      const float2 w = *c;
       const float x = __uint_as_float(va[i].x), y = __uint_as_float(vb[i].x);
       put(dst + e0, fmaf(x, w.x, -y * w.y));
       put(dst + e1, fmaf(y, w.x, x * w.y));
@@ -294,7 +298,8 @@ __global__ void __launch_bounds__(kThreads, VEC ? 6 : 4)
     __syncthreads();
   }
   for (int x = tid; x < nt * p.half; x += kThreads) {
-    const int t = x / p.half, i = x - t * p.half;
+    const int t = x / p.half, y = x - t * p.half, cols = p.half / PAIRS;
+    const int i = y % cols * PAIRS + y / cols;
     const int pos = p.table ? s_rot[t] : __ldg(p.positions + t0 + t);
     const uint64_t a = p.turn[i] * (uint64_t)(int64_t)pos;
     float s, c;
@@ -351,10 +356,12 @@ cudaError_t launch(RopeParams& p, int n_parts, const int* heads, int dim, int ro
   for (int i = n_parts; i < 3; ++i) p.first[i - 1] = p.heads;  // nothing from here on
   p.unit_magic = magic_of(p.units);
   p.head_magic = magic_of(p.heads);
-  // About kUnits units a thread, but several blocks an SM (of 152) before a
-  // block takes more than one token, and at most 32 KB of cosines.
+  // Several blocks an SM (of 152) before a block takes more than one token, at
+  // most 32 KB of cosines, and about kUnits units a thread, twice that where no
+  // token is looked up (16384 x 24 x 256: 63.3 us so, 67.5 with kUnits; an
+  // append of 64 canvases 90.9 and 89.4 us).
   const int64_t token_units = (int64_t)p.heads * p.units;
-  int per = (int)(kUnits * kThreads / token_units);
+  int per = (int)((p.table ? 1 : 2) * kUnits * kThreads / token_units);
   const int spread = p.n_tokens / (152 * 4);
   if (per > spread) per = spread;
   if (per > kMaxTokens) per = kMaxTokens;
