@@ -169,7 +169,8 @@ struct ForkParams {
   int page_shift;
   DevStatus* status;
   int32_t* counts;  // [kForkCtas] free pages of each CTA's share
-  int32_t* users;   // [n_pages] growing holders of a partly filled page
+  int32_t* users;   // [n_pages] growing holders of a partly filled page; later the
+                    // fresh pages in order
   int32_t* first;   // [n_pages] the lowest of them
 };
 
@@ -183,36 +184,23 @@ __device__ __forceinline__ int held_len(const dg_kv_fork_t& f, int s, int shift)
   return (int)min((int64_t)max(__ldg(f.lens_in + s), 0), (int64_t)f.row << shift);
 }
 
+// What a new sequence continues, from the inputs (shared memory, one each).
 struct Grow {
-  int parent, have, pages, grow;  // pages held so far
-  int last;                       // partly filled last page that grows, or -1
+  int parent, have, grow;
+  int last;  // its partly filled last page, if it grows from one, or -1
 };
-__device__ __forceinline__ Grow load_grow(const ForkParams& p, int j) {
-  const dg_kv_fork_t& f = p.f;
-  Grow g;
-  g.parent = __ldg(f.parent + j);
-  if (g.parent >= f.n_old) g.parent = -1;
-  g.have = g.parent < 0 ? 0 : held_len(f, g.parent, p.page_shift);
-  const int ps = 1 << p.page_shift;
-  g.pages = (g.have + ps - 1) >> p.page_shift;
-  g.grow = max(__ldg(f.grow + j), 0);
-  g.last = -1;
-  if (g.grow > 0 && (g.have & (ps - 1))) {
-    const int id = __ldg(f.table_in + (int64_t)g.parent * f.row + g.pages - 1);
-    if ((unsigned)id < (unsigned)f.n_pages) g.last = id;
-  }
-  return g;
-}
 
 __global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kForkThreads)
     k_kv_fork(const __grid_constant__ ForkParams p) {
   const dg_kv_fork_t& f = p.f;
-  extern __shared__ int dyn[];
-  int* child = dyn;                 // [kForkMax]: children of an old sequence
-  int* start = dyn;                 // [kForkMax + 1]: first fresh page's rank (after phase 1)
+  extern __shared__ __align__(16) uint8_t dyn[];
+  Grow* grow = reinterpret_cast<Grow*>(dyn);                // [n_new]
+  int* child = reinterpret_cast<int*>(grow + f.n_new);      // [n_old] children of an old sequence
+  int* start = child;                                       // [n_new + 1] rank of its first fresh
+                                                            // page, once child is done with
   __shared__ uint8_t split[kForkMax];
   __shared__ int warp_sum[32], warp_free[32], over;
-  __shared__ long long s_total;
+  __shared__ int s_total;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
   const int gt = cta * kForkThreads + tid, gw = gt >> 5;
   constexpr int kAll = kForkCtas * kForkThreads, kWarps = kAll / 32;
@@ -223,23 +211,38 @@ __global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kForkThreads
   pdl_wait();
   __syncthreads();
 
-  // children of every old sequence; scratch of the pages that may split
+  // The new sequences (every CTA, all of them); scratch of the pages that may
+  // split; children of every old sequence.
   for (int j = tid; j < f.n_new; j += kForkThreads) {
-    const int par = __ldg(f.parent + j);
-    if (par >= 0 && par < f.n_old) atomicAdd(&child[par], 1);
-    if (cta == 0 && (par < -1 || par >= f.n_old))
-      report(p.status, kDevBounds, kSiteForkParent, (unsigned)j, (unsigned)par);
-  }
-  for (int j = gt; j < f.n_new; j += kAll) {
-    const Grow g = load_grow(p, j);
-    if (g.last >= 0) {
-      p.users[g.last] = 0;
-      p.first[g.last] = INT_MAX;
+    Grow g;
+    g.parent = __ldg(f.parent + j);
+    g.grow = __ldg(f.grow + j);
+    if (cta == 0) {
+      if (g.parent < -1 || g.parent >= f.n_old)
+        report(p.status, kDevBounds, kSiteForkParent, (unsigned)j, (unsigned)g.parent);
+      if (g.grow < 0) report(p.status, kDevBounds, kSiteForkLen, (unsigned)j, (unsigned)g.grow);
     }
+    if (g.parent >= f.n_old || g.parent < 0) g.parent = -1;
+    g.grow = max(g.grow, 0);
+    g.have = g.parent < 0 ? 0 : held_len(f, g.parent, shift);
+    g.last = -1;
+    if (g.grow > 0 && (g.have & (ps - 1))) {
+      const int id = __ldg(f.table_in + (int64_t)g.parent * f.row + (g.have >> shift));
+      if ((unsigned)id < (unsigned)f.n_pages) {
+        g.last = id;
+        if (cta == 0) {
+          p.users[id] = 0;
+          p.first[id] = INT_MAX;
+        }
+      }
+    }
+    grow[j] = g;
+    if (g.parent >= 0) atomicAdd(&child[g.parent], 1);
   }
-  if (f.ref_out != f.ref_in)
+  if (f.ref_out != f.ref_in) {
 #pragma unroll 8
     for (int i = gt; i < f.n_pages; i += kAll) f.ref_out[i] = __ldg(f.ref_in + i);
+  }
   cluster_sync();
 
   // counts of held pages; growing holders of partly filled pages
@@ -267,62 +270,13 @@ __global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kForkThreads
     }
   }
   for (int j = gt; j < f.n_new; j += kAll) {
-    const Grow g = load_grow(p, j);
-    if (g.last >= 0) {
-      atomicAdd(p.users + g.last, 1);
-      atomicMin(p.first + g.last, j);
+    const int last = grow[j].last;
+    if (last >= 0) {
+      atomicAdd(p.users + last, 1);
+      atomicMin(p.first + last, j);
     }
   }
   cluster_sync();
-
-  // splits and needs of all sequences (every CTA, from the same numbers), and
-  // their prefix: start[j] = rank of the first fresh page of sequence j
-  {
-    constexpr int kEach = kForkMax / kForkThreads;
-    int need[kEach], sum = 0;
-    const int each = (f.n_new + kForkThreads - 1) / kForkThreads;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int j = tid * each + i;
-      need[i] = 0;
-      if (i < each && j < f.n_new) {
-        const Grow g = load_grow(p, j);
-        bool sp = false;
-        if (g.last >= 0)
-          sp = __ldcg(f.ref_out + g.last) > __ldcg(p.users + g.last) ||
-               __ldcg(p.first + g.last) != j;
-        split[j] = sp;
-        const int64_t want = (int64_t)g.have + g.grow;
-        if (want > (int64_t)f.row << shift) over = 1;
-        else need[i] = (int)((want + ps - 1) >> shift) - g.pages + (sp ? 1 : 0);
-        if (cta == 0 && __ldg(f.grow + j) < 0)
-          report(p.status, kDevBounds, kSiteForkLen, (unsigned)j, 0u);
-      }
-      sum += need[i];
-    }
-    // at most 4096 sequences of 2^20 pages: the sum fits 32 bits
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();  // and the last use of child
-    int before = 0;
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
-    int at = before + incl - sum;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int j = tid * each + i;
-      if (i < each && j < f.n_new) start[j] = at;
-      at += need[i];
-    }
-    if (tid == kForkThreads - 1) {
-      start[f.n_new] = at;
-      s_total = at;
-    }
-  }
 
   // free pages of this CTA's share, one contiguous run a warp
   const int run = (f.n_pages + kWarps - 1) / kWarps;
@@ -345,7 +299,54 @@ __global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kForkThreads
     for (int w = 0; w < 32; ++w) n += warp_free[w];
     p.counts[cta] = n;
   }
-  cluster_sync();
+
+  // splits and needs of all sequences (every CTA, from the same numbers), and
+  // their prefix
+  {
+    constexpr int kEach = kForkMax / kForkThreads;
+    int need[kEach], sum = 0;
+    const int each = (f.n_new + kForkThreads - 1) / kForkThreads;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int j = tid * each + i;
+      need[i] = 0;
+      if (i < each && j < f.n_new) {
+        const Grow g = grow[j];
+        bool sp = false;
+        if (g.last >= 0)
+          sp = __ldcg(f.ref_out + g.last) > __ldcg(p.users + g.last) ||
+               __ldcg(p.first + g.last) != j;
+        split[j] = sp;
+        const int64_t want = (int64_t)g.have + g.grow;
+        if (want > (int64_t)f.row << shift) over = 1;
+        else need[i] = (int)((want + ps - 1) >> shift) - ((g.have + ps - 1) >> shift) + (sp ? 1 : 0);
+      }
+      sum += need[i];
+    }
+    // at most 4096 sequences of 2^18 pages: the sum fits 32 bits
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    int at = before + incl - sum;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int j = tid * each + i;
+      if (i < each && j < f.n_new) start[j] = at;
+      at += need[i];
+    }
+    if (tid == kForkThreads - 1) {
+      start[f.n_new] = at;
+      s_total = at;
+    }
+  }
+  cluster_sync();  // the last use of users
 
   int64_t all_free = 0;
   int rank = 0;
@@ -355,15 +356,36 @@ __global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kForkThreads
     if (c < cta) rank += n;
   }
   const bool ok = !over && s_total <= all_free;
-  const int total = ok ? (int)s_total : 0;
+  const int total = ok ? s_total : 0;
   if (gt == 0) *f.short_by = over ? -1 : (ok ? 0 : (int)(s_total - all_free));
+
+  // the `total` lowest free pages, in order (they may all lie in one warp's
+  // run, so it only lists them here)
+  int* fresh = p.users;
+  for (int w = 0; w < warp; ++w) rank += warp_free[w];
+  for (int i0 = p0; i0 < p1 && rank < total; i0 += 32 * kBatch) {
+    int r[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + 32 * k + lane;
+      r[k] = i < p1 ? __ldcg(f.ref_out + i) : 1;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const unsigned b = __ballot_sync(0xffffffffu, r[k] == 0);
+      const int at = rank + __popc(b & ((1u << lane) - 1u));
+      if (r[k] == 0 && at < total) fresh[at] = i0 + 32 * k + lane;
+      rank += __popc(b);
+    }
+  }
 
   // rows of the new sequences, but for their fresh pages
   for (int j = gw; j < f.n_new; j += kWarps) {
-    const Grow g = load_grow(p, j);
+    const Grow g = grow[j];
     const bool sp = ok && split[j];
-    const int stay = g.pages - (sp ? 1 : 0);
-    const int want = ok ? (g.have + g.grow + ps - 1) >> shift : g.pages;
+    const int pages = (g.have + ps - 1) >> shift;
+    const int stay = pages - (sp ? 1 : 0);
+    const int want = ok ? (g.have + g.grow + ps - 1) >> shift : pages;
     const int32_t* held = f.table_in + (int64_t)g.parent * f.row;
     for (int i0 = lane; i0 < f.row; i0 += 32 * kBatch) {
       int id[kBatch];
@@ -388,35 +410,28 @@ __global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kForkThreads
       }
     }
   }
+  cluster_sync();
 
-  // fresh pages: the free page of rank r goes to the sequence whose range
-  // holds r.  A split page keeps a holder, so no count met here drops to 0.
-  for (int w = 0; w < warp; ++w) rank += warp_free[w];
-  for (int i0 = p0; i0 < p1 && rank < total; i0 += 32) {
-    const int i = i0 + lane;
-    const bool is_free = i < p1 && __ldcg(f.ref_out + i) == 0;
-    const unsigned b = __ballot_sync(0xffffffffu, is_free);
-    const int r = rank + __popc(b & ((1u << lane) - 1u));
-    if (is_free && r < total) {
-      int lo = 0, hi = f.n_new;  // the last j with start[j] <= r
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start[mid] <= r) lo = mid;
-        else hi = mid;
-      }
-      const Grow g = load_grow(p, lo);
-      const bool sp = split[lo];
-      const int at = g.pages - (sp ? 1 : 0) + r - start[lo];
-      f.table_out[(int64_t)lo * f.row + at] = i;
-      f.ref_out[i] = 1;
-      if (sp && r == start[lo]) {
-        f.copies[3 * lo] = g.last;
-        f.copies[3 * lo + 1] = i;
-        f.copies[3 * lo + 2] = g.have & (ps - 1);
-        atomicSub(f.ref_out + g.last, 1);
-      }
+  // fresh pages: the one of rank r goes to the sequence whose range holds r
+  for (int r = gt; r < total; r += kAll) {
+    const int page = __ldcg(fresh + r);
+    int lo = 0, hi = f.n_new;  // the last j with start[j] <= r
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid] <= r) lo = mid;
+      else hi = mid;
     }
-    rank += __popc(b);
+    const Grow g = grow[lo];
+    const bool sp = split[lo];
+    const int at = ((g.have + ps - 1) >> shift) - (sp ? 1 : 0) + r - start[lo];
+    f.table_out[(int64_t)lo * f.row + at] = page;
+    f.ref_out[page] = 1;
+    if (sp && r == start[lo]) {
+      f.copies[3 * lo] = g.last;
+      f.copies[3 * lo + 1] = page;
+      f.copies[3 * lo + 2] = g.have & (ps - 1);
+      atomicSub(f.ref_out + g.last, 1);
+    }
   }
 }
 
@@ -568,10 +583,15 @@ dg_status_t dg_kv_fork(const dg_kv_fork_t* f, void* workspace, size_t workspace_
   p.counts = reinterpret_cast<int32_t*>(ws + L.counts);
   p.users = reinterpret_cast<int32_t*>(ws + L.users);
   p.first = reinterpret_cast<int32_t*>(ws + L.first);
-  const int most = f->n_old > f->n_new ? f->n_old : f->n_new;
-  const cudaError_t e =
-      launch_pdl(k_kv_fork, dim3(kForkCtas), dim3(kForkThreads), (size_t)(most + 1) * 4,
-                 reinterpret_cast<cudaStream_t>(stream), p);
+  const int most = f->n_old > f->n_new + 1 ? f->n_old : f->n_new + 1;
+  const size_t smem = sizeof(Grow) * f->n_new + sizeof(int) * most;
+  cudaError_t e = cudaSuccess;
+  if (smem > 40 * 1024)  // beside 5 KB of static shared memory
+    e = cudaFuncSetAttribute(k_kv_fork, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(sizeof(Grow) * kForkMax + sizeof(int) * (kForkMax + 1)));
+  if (e == cudaSuccess)
+    e = launch_pdl(k_kv_fork, dim3(kForkCtas), dim3(kForkThreads), smem,
+                   reinterpret_cast<cudaStream_t>(stream), p);
   return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 
