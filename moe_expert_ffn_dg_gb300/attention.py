@@ -21,25 +21,28 @@ _SCALINGS = {"none": B.DG_ROPE_PLAIN, "linear": B.DG_ROPE_LINEAR, "base": B.DG_R
 
 
 def _stream(device, stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle alone: torch.cuda.current_stream() builds an object around it
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _heads(t: torch.Tensor, dtype, device, dim: int, what: str) -> B.dg_heads_t:
     """A [tokens, heads, dim] tensor as the library takes it."""
-    if t.dim() != 3 or t.shape[2] != dim or (dim > 1 and t.stride(2) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != dim or (stride[2] != 1 and dim > 1):
         raise ValueError(f"{what}: [tokens, heads, {dim}] with the last dimension contiguous")
     if t.dtype != dtype or t.device != device:
         raise ValueError(f"{what}: {dtype} on {device} expected, got {t.dtype} on {t.device}")
-    return B.dg_heads_t(t.data_ptr(), t.stride(0), t.stride(1))
+    return B.dg_heads_t(t.data_ptr(), stride[0], stride[1])
 
 
-def _ints(t: torch.Tensor, device, shape, what: str) -> int:
+def _ints(t: torch.Tensor, device, shape: tuple, what: str) -> int:
     """Pointer of a contiguous int32 device tensor of the given shape."""
     if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what}: contiguous int32 on {device} expected")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {shape} expected, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
@@ -222,7 +225,7 @@ class KvPager:
         self._bytes = B.dg_kv_fork_workspace_size(n_pages)
         # 4-byte elements: aligned as any allocation is
         self.workspace = torch.zeros((self._bytes + 3) // 4, dtype=torch.int32, device=device)
-        self.device = self.workspace.device
+        self.device, self._ws = self.workspace.device, self.workspace.data_ptr()
 
     def fork(self, table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor,
              parent: torch.Tensor, grow: torch.Tensor, out: KvFork = None,
@@ -233,9 +236,9 @@ class KvPager:
         ``include/dg_attn.h``).  out.ref may be ref."""
         dev, (n_old, row), n_new = self.device, table.shape, parent.shape[0]
         if out is None:
-            def new(*shape):
-                return torch.empty(shape, dtype=torch.int32, device=dev)
-            out = KvFork(new(n_new, row), new(n_new), new(self.n_pages), new(n_new, 3), new(1))
+            new = lens.new_empty  # cheaper than views of one allocation
+            out = KvFork(new((n_new, row)), new(n_new), new(self.n_pages), new((n_new, 3)),
+                         new(1))
         f = B.dg_kv_fork_t(
             self.n_pages, self.page_size, row, n_old, n_new,
             _ints(table, dev, (n_old, row), "table"), _ints(lens, dev, (n_old,), "lens"),
@@ -245,7 +248,7 @@ class KvPager:
             _ints(out.ref, dev, (self.n_pages,), "out.ref"),
             _ints(out.copies, dev, (n_new, 3), "out.copies"),
             _ints(out.short, dev, (1,), "out.short"))
-        B.dg_kv_fork(f, self.workspace.data_ptr(), self._bytes, _stream(dev, stream))
+        B.dg_kv_fork(f, self._ws, self._bytes, _stream(dev, stream))
         return out
 
     def device_status(self, stream=None):
