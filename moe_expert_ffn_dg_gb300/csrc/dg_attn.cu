@@ -436,12 +436,17 @@ __device__ __forceinline__ void find_start(const AttnParams& p, long long* cost,
     const int c = blockIdx.x / p.team;
     long long u0 = 0, u1 = 0;
     if (c < teams) {
-      u0 = (long long)c * total / teams;
-      u1 = (long long)(c + 1) * total / teams;
+      if (total < (1 << 22)) {  // at most 160 teams: 32-bit divisions will do
+        u0 = (unsigned)c * (unsigned)total / (unsigned)teams;
+        u1 = (unsigned)(c + 1) * (unsigned)total / (unsigned)teams;
+      } else {
+        u0 = (long long)c * total / teams;
+        u1 = (long long)(c + 1) * total / teams;
+      }
     }
     int h = 0, b = 0, t = 0, skip = 0;
     if (u0 < u1) {
-      h = (int)(u0 / one);
+      h = total < (1 << 22) ? (int)((unsigned)u0 / (unsigned)one) : (int)(u0 / one);
       long long r = u0 - h * one;
       const bool mine = r >= incl - sum && r < incl;
       const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
@@ -578,6 +583,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     };
     while (ok && w.next(p, g)) {
       if (g.n == 0) continue;
+      if (keys) {
+        const int qb = qn % C::kQBufs;
+        if (!acquire(&q_empty[qb], ((uint32_t)(qn / C::kQBufs) & 1u) ^ 1u)) break;
+        ++qn;
+        if (leader) {
+          mbar_arrive_expect_tx(&q_full[qb], NQ * C::kChunks * 128 * p.group * p.q_box);
+#pragma unroll 1
+          for (int x = 0; x < NQ * C::kChunks; ++x)
+            tma_load_3d(&p.qm, &q_full[qb],
+                        qbase + qb * NQ * C::kQTile + x * (kRows * 128),
+                        64 * (x % C::kChunks), g.head * p.group, g.tok0 + x / C::kChunks * p.step);
+        }
+        __syncwarp();
+      }
       // Page ids of 32 consecutive boxes, one a lane, and of the next 32.  An
       // id out of range (or of a box that no query sees, whose page may be
       // gone) becomes n_pages: the copy then reads zeros.
@@ -595,20 +614,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       };
       int base = ((g.kt0 * kKeys) >> piece_shift) & ~31;
       int ids = ids_at(base), ids_next = ids_at(base + 32);
-      if (keys) {
-        const int qb = qn % C::kQBufs;
-        if (!acquire(&q_empty[qb], ((uint32_t)(qn / C::kQBufs) & 1u) ^ 1u)) break;
-        ++qn;
-        if (leader) {
-          mbar_arrive_expect_tx(&q_full[qb], NQ * C::kChunks * 128 * p.group * p.q_box);
-#pragma unroll 1
-          for (int x = 0; x < NQ * C::kChunks; ++x)
-            tma_load_3d(&p.qm, &q_full[qb],
-                        qbase + qb * NQ * C::kQTile + x * (kRows * 128),
-                        64 * (x % C::kChunks), g.head * p.group, g.tok0 + x / C::kChunks * p.step);
-        }
-        __syncwarp();
-      }
 #pragma unroll 1
       for (int j = 0; j < g.n && ok; ++j) {
         const int rp = pos + (keys ? k_stage<PARTS>(j) : v_stage<PARTS>(j, g.n));
@@ -1036,8 +1041,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       }
       if (g.first && !g.last) {
         // unit range of team c: [c total / teams, (c + 1) total / teams)
-        rec.parts =
-            (int)((g.end * start.teams - 1) / start.total) - (int)(blockIdx.x / p.team) + 1;
+        const long long x = g.end * start.teams - 1;
+        const int lastc = start.total < (1 << 22) ? (int)((unsigned)x / (unsigned)start.total)
+                                                  : (int)(x / start.total);
+        rec.parts = lastc - (int)(blockIdx.x / p.team) + 1;
         rec.head = g.head;
         rec.tok0 = g.tok0;
         rec.ntok = g.ntok;
@@ -1074,7 +1081,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
 // Join the parts of the item that CTA blockIdx.x began: with m the largest
 // reference, o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i, parts in order.
 // A warp takes a row.
-template <int D, int NQ, bool FP16>
+// BATCH (divides 32): parts in flight.
+template <int D, int NQ, int BATCH, bool FP16>
 __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnParams p) {
   pdl_trigger();
   pdl_wait();
@@ -1090,30 +1098,48 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnP
       const int slot = 2 * ((int)blockIdx.x + k * p.team) + (k == 0 ? 1 : 0);
       return (size_t)slot * (NQ * kRows) + row;
     };
-    float m = -INFINITY;
-    for (int k = lane; k < rec.parts; k += 32) m = fmaxf(m, p.ml[prow(k)].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    // statistics of the first 32 parts, one a lane (more are read again below)
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < rec.parts) ml = p.ml[prow(lane)];
+    float m = ml.x;
+    for (int k = lane + 32; k < rec.parts; k += 32) m = fmaxf(m, p.ml[prow(k)].x);
     float l = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < rec.parts; ++k) {
-      const float2 ml = p.ml[prow(k)];
-      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
-      const float* src = p.part + prow(k) * D + lane * E;
-      float v[E];
-      if constexpr (E == 2) {
-        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
-      } else {
+    for (int k0 = 0; k0 < rec.parts; k0 += BATCH) {
+      // the loads of a batch leave before the maximum is known
+      float v[BATCH][E];
 #pragma unroll
-        for (int e = 0; e < E; e += 4)
-          *reinterpret_cast<float4*>(v + e) = *reinterpret_cast<const float4*>(src + e);
+      for (int k = 0; k < BATCH; ++k) {
+        const float* src = p.part + prow(min(k0 + k, rec.parts - 1)) * D + lane * E;
+        if constexpr (E == 2) {
+          *reinterpret_cast<float2*>(v[k]) = *reinterpret_cast<const float2*>(src);
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; e += 4)
+            *reinterpret_cast<float4*>(v[k] + e) = *reinterpret_cast<const float4*>(src + e);
+        }
       }
-      if (ml.x != -INFINITY) {  // a part that saw nothing holds nothing
-        l += f * ml.y;
+      if (k0 == 0) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += f * v[e];
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      }
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        if (k0 + k >= rec.parts) break;
+        float2 s;
+        if (k0 < 32) {
+          s.x = __shfl_sync(0xffffffffu, ml.x, k0 + k);
+          s.y = __shfl_sync(0xffffffffu, ml.y, k0 + k);
+        } else {
+          s = p.ml[prow(k0 + k)];
+        }
+        if (s.x != -INFINITY) {  // a part that saw nothing holds nothing
+          const float f = exp2f(s.x - m);
+          l += f * s.y;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += f * v[k][e];
+        }
       }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1179,9 +1205,11 @@ struct Variant {
     cfg.numAttrs = m ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, m ? many : few, p);
     if (e != cudaSuccess) return e;
+    // few rows are split into many parts, many rows into two or three
     if (m && kManyNq == 2)
-      return launch_pdl(k_attn_join<D, kManyNq, FP16>, dim3(ctas, 8), dim3(256), 0, s, p);
-    return launch_pdl(k_attn_join<D, 1, FP16>, dim3(ctas, m ? 8 : 1), dim3(256), 0, s, p);
+      return launch_pdl(k_attn_join<D, kManyNq, 2, FP16>, dim3(ctas, 8), dim3(256), 0, s, p);
+    if (m) return launch_pdl(k_attn_join<D, 1, 2, FP16>, dim3(ctas, 8), dim3(256), 0, s, p);
+    return launch_pdl(k_attn_join<D, 1, 8, FP16>, dim3(ctas), dim3(256), 0, s, p);
   }
   static cudaError_t prepare() {
     cudaError_t e = cudaFuncSetAttribute(few, cudaFuncAttributeMaxDynamicSharedMemorySize,
