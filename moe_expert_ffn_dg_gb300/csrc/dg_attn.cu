@@ -635,10 +635,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             }
             const int id = __shfl_sync(0xffffffffu, ids, x & 31);
             // the cluster's CTAs share the chunks, or the boxes of one chunk
-            const int c0 = chunks >= CL ? rank : 0;
+            const int c0 = chunks >= CL ? rank : 0, dc = chunks >= CL ? CL : 1;
             if (leader && (chunks >= CL || x % CL == rank))
 #pragma unroll 1
-              for (int c = c0; c < chunks; c += CL)
+              for (int c = c0; c < chunks; c += dc)
                 tma_load_4d<CL>(map, &full[st],
                                 ring + st * C::kStageBytes + (c * tokens + r) * 128,
                                 ((keys ? h * chunks : 0) + c) * 64, g.head, (key0 + r) & (ps - 1),
