@@ -93,12 +93,15 @@ struct AttnParams {
   DevStatus* status;
 };
 
-template <int D, int NQ>
+template <int D, int NQ, bool PAIR>
 struct Cfg {
   // ring stage: 128 keys x D up to 128; at 256 a half of a key tile (128 keys
   // x 128) or of a value tile (64 keys x 256)
   static constexpr int kParts = D == 256 ? 2 : 1;
-  static constexpr int kStageBytes = kKeys * D * 2 / kParts;
+  // of a key tile a pair's CTA holds half the keys, of a value tile half the
+  // columns
+  static constexpr int kShare = PAIR ? 2 : 1;
+  static constexpr int kStageBytes = kKeys * D * 2 / kParts / kShare;
   static constexpr int kStages = 160 * 1024 / kStageBytes;
   static constexpr int kChunks = D / 64;  // 128-byte columns of a row
   static constexpr int kQTile = kRows * D * 2;
@@ -250,6 +253,56 @@ __device__ __forceinline__ void commit_cluster(uint64_t* bar) {
     umma_commit(bar);
 }
 
+// Pair of CTAs: a box into this CTA, counted on the first CTA's barrier (`bar`
+// is its address in the cluster).
+__device__ __forceinline__ void tma_load_4d_pair(const CUtensorMap* map, uint32_t bar,
+                                                 uint32_t dst, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint32_t bar,
+                                                 uint32_t dst, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// Address of a barrier of the cluster's first CTA, and an arrival there.
+__device__ __forceinline__ uint32_t first_cta(uint64_t* bar) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(bar)));
+  return r;
+}
+template <bool PAIR>
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+  if constexpr (PAIR)
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                     first_cta(bar))
+                 : "memory");
+  else
+    mbar_arrive(bar);
+}
+
+// try_wait that also acquires what the other CTA of a pair released.
+template <bool PAIR>
+__device__ __forceinline__ bool try_wait_scope(uint64_t* bar, uint32_t parity) {
+  if constexpr (!PAIR) return mbar_try_wait(bar, parity);
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
@@ -267,7 +320,7 @@ __device__ __forceinline__ void set_max_regs_down() {
 }
 
 // log2 of the most tokens of a box.
-__host__ __device__ constexpr int key_shift_max(int d) { return d == 64 ? 6 : 7; }
+__host__ __device__ constexpr int key_shift_max(int d, bool pair) { return pair || d == 64 ? 6 : 7; }
 __host__ __device__ constexpr int value_shift_max(int d) { return d == 128 ? 7 : 6; }
 
 // Two fp32 lanes of one instruction.
@@ -313,27 +366,68 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr, uint32_t leading
   return ((smem_addr & 0x3FFFFu) >> 4) | ((leading >> 4) << 16);
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit inputs, fp32 accumulate.
+// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit inputs, fp32 accumulate.  PAIR: one
+// product of two CTAs, each with its own rows of A and D and half of B.
+template <bool PAIR>
 __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
                                         uint32_t idesc, int accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+        : "memory");
 }
 // The same with A in tensor memory.
+template <bool PAIR>
 __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
                                         uint32_t idesc, int accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "mov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+        : "memory");
+}
+
+// Arrive, when this thread's MMAs so far are done, on `bar` of this CTA, or of
+// both CTAs of a pair.
+template <bool PAIR>
+__device__ __forceinline__ void commit_own(uint64_t* bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    umma_commit(bar);
+}
+// A stage is free: to every CTA that fills it.
+template <bool PAIR, int CL>
+__device__ __forceinline__ void commit_stage(uint64_t* bar) {
+  if constexpr (PAIR) commit_own<true>(bar);
+  else commit_cluster<CL>(bar);
 }
 
 template <bool FP16>
@@ -488,10 +582,13 @@ __device__ __forceinline__ void find_start(const AttnParams& p, long long* cost,
   __syncthreads();
 }
 
-template <int D, int NQ, int CL, bool FP16>
+template <int D, int NQ, int CL, bool PAIR, bool FP16>
 __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constant__ AttnParams p) {
-  using C = Cfg<D, NQ>;
-  constexpr int NS = C::kStages, PARTS = C::kParts;
+  static_assert(!PAIR || CL == 2, "a pair is a cluster of two");
+  using C = Cfg<D, NQ, PAIR>;
+  constexpr int NS = C::kStages, PARTS = C::kParts, SH = C::kShare;
+  constexpr int MC = PAIR ? 1 : CL;             // CTAs that a copy goes to
+  constexpr int KROWS = kKeys / SH;             // keys of a tile in this CTA
   constexpr int NC = NQ == 2 ? 128 : 64;        // score columns a softmax thread
   constexpr int OC = NQ == 2 ? D : D / 2;       // output columns a softmax thread
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -500,6 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   __shared__ uint64_t full[NS], empty[NS];
   __shared__ uint64_t q_full[C::kQBufs], q_empty[C::kQBufs];
   __shared__ uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], o_full[2], o_empty[2], drain;
+  __shared__ uint64_t tail_full;  // pair, second CTA: the values that it clears
   __shared__ uint32_t tmem_holder;
   __shared__ int abort_word;
   __shared__ Start start;
@@ -515,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], CL);
+      mbar_init(&empty[i], MC);
     }
     for (int i = 0; i < C::kQBufs; ++i) {
       mbar_init(&q_full[i], 1);
@@ -523,13 +621,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_half[i], 4);
-      mbar_init(&p_full[i], NQ == 2 ? 4 : 8);
+      mbar_init(&p_half[i], 4 * SH);
+      mbar_init(&p_full[i], (NQ == 2 ? 4 : 8) * SH);
       mbar_init(&pv_done[i], 1);
       mbar_init(&o_full[i], 1);
-      mbar_init(&o_empty[i], NQ == 2 ? 4 : 8);
+      mbar_init(&o_empty[i], (NQ == 2 ? 4 : 8) * SH);
     }
     mbar_init(&drain, 1);
+    mbar_init(&tail_full, 1);
     abort_word = 0;
     fence_mbar_init();
   }
@@ -539,16 +638,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     tma_prefetch_map(&p.vm);
   }
   if (warp == 9) {
-    tmem_alloc(&tmem_holder, 512);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                       smem_u32(&tmem_holder))
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      tmem_alloc(&tmem_holder, 512);
+      tmem_relinquish();
+    }
   }
-  if (CL > 1) cluster_arrive();  // barriers must be there before a neighbour's copy or arrival
   pdl_wait();
   tc_fence_before();
   find_start<NQ>(p, reinterpret_cast<long long*>(smem), &start);
   tc_fence_after();
-  if (CL > 1) cluster_wait();
+  if (CL > 1) {  // a neighbour's copies and arrivals need the barriers, and the ring to be free
+    cluster_arrive();
+    cluster_wait();
+  }
   const uint32_t tmem = tmem_holder;
+  const int rank = CL > 1 ? blockIdx.x % CL : 0;
   Walk<NQ> w;
   w.h = start.h;
   w.b = start.b;
@@ -565,14 +674,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     // ------------------------------------------------------------ producers
     // Warp 8 fills the key stages (and the query tiles), warp 10 the value
     // stages.  Uniform loops, one elected lane issues; of the cluster's CTAs
-    // each takes its share of the 64-column chunks (of the pieces at 64).
+    // each takes its share of the 64-column chunks (of the pieces at 64), of a
+    // pair's each its own half of the tile.
     const bool leader = elect_one(), keys = warp == 8;
+    // whether stage h of a value tile holds the last keys seen, in a part of
+    // their 16-key step
+    auto clears_stage = [](int vis, int h) {
+      return vis < kKeys && (vis & 15) && vis / (kKeys / PARTS) == h;
+    };
     const int ps = 1 << p.page_shift;
-    const int piece_shift = min(p.page_shift, keys ? key_shift_max(D) : value_shift_max(D));
+    const int piece_shift =
+        min(p.page_shift, keys ? key_shift_max(D, PAIR) : value_shift_max(D));
     const int piece = 1 << piece_shift;                    // tokens of a box
-    const int rank = CL > 1 ? blockIdx.x % CL : 0;
-    const int tokens = keys ? kKeys : kKeys / PARTS;       // of a stage
-    const int chunks = keys ? C::kChunks / PARTS : C::kChunks;
+    const int tokens = keys ? KROWS : kKeys / PARTS;       // of a stage
+    const int chunks = keys ? C::kChunks / PARTS : C::kChunks / SH;
     const CUtensorMap* map = keys ? &p.km : &p.vm;
     int pos = 0, qn = 0;
     bool ok = true;
@@ -588,12 +703,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         if (!acquire(&q_empty[qb], ((uint32_t)(qn / C::kQBufs) & 1u) ^ 1u)) break;
         ++qn;
         if (leader) {
-          mbar_arrive_expect_tx(&q_full[qb], NQ * C::kChunks * 128 * p.group * p.q_box);
+          if (!PAIR || rank == 0)
+            mbar_arrive_expect_tx(&q_full[qb],
+                                  SH * NQ * C::kChunks * 128 * p.group * p.q_box);
 #pragma unroll 1
-          for (int x = 0; x < NQ * C::kChunks; ++x)
-            tma_load_3d(&p.qm, &q_full[qb],
-                        qbase + qb * NQ * C::kQTile + x * (kRows * 128),
-                        64 * (x % C::kChunks), g.head * p.group, g.tok0 + x / C::kChunks * p.step);
+          for (int x = 0; x < NQ * C::kChunks; ++x) {
+            const uint32_t dst = qbase + qb * NQ * C::kQTile + x * (kRows * 128);
+            const int c = 64 * (x % C::kChunks), row = g.tok0 + x / C::kChunks * p.step;
+            if (PAIR)
+              tma_load_3d_pair(&p.qm, first_cta(&q_full[qb]), dst, c, g.head * p.group, row);
+            else
+              tma_load_3d(&p.qm, &q_full[qb], dst, c, g.head * p.group, row);
+          }
         }
         __syncwarp();
       }
@@ -622,9 +743,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         for (int h = 0; h < PARTS; ++h) {
           const int st = (rp + h) % NS;
           if (!acquire(&empty[st], ((uint32_t)((rp + h) / NS) & 1u) ^ 1u)) break;
-          const int key0 = keys ? key_t : key_t + h * tokens;
-          const int live = max(0, min(tokens, (g.khi - key0 + piece - 1) & -piece));
-          if (leader) mbar_arrive_expect_tx(&full[st], live * 128 * chunks);
+          const int key0 = key_t + (keys ? rank * (SH - 1) * KROWS : h * tokens);
+          auto live_from = [&](int key) {  // tokens of a stage from `key` on that are fetched
+            return max(0, min(tokens, (g.khi - key + piece - 1) & -piece));
+          };
+          const int live = live_from(key0);
+          // Pair: counted in the first CTA, both shares together; but values
+          // that the second CTA clears in part, it has to wait for itself.
+          uint64_t* bar = &full[st];
+          bool other = PAIR && rank == 1;
+          if (PAIR) {
+            const bool clears = !keys && clears_stage(g.khi - key_t, h);
+            if (other && clears) bar = &tail_full;
+            if (leader && (!other || clears))
+              mbar_arrive_expect_tx(bar, (live + (keys ? live_from(key_t + KROWS)
+                                                       : (clears ? 0 : live))) *
+                                             128 * chunks);
+            other = other && !clears;
+          } else if (leader) {
+            mbar_arrive_expect_tx(bar, live * 128 * chunks);
+          }
+          const uint32_t bar_addr = other ? first_cta(bar) : smem_u32(bar);
 #pragma unroll 1
           for (int r = 0; r < live; r += piece) {
             const int x = (key0 + r) >> piece_shift;
@@ -635,14 +774,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             }
             const int id = __shfl_sync(0xffffffffu, ids, x & 31);
             // the cluster's CTAs share the chunks, or the boxes of one chunk
-            const int c0 = chunks >= CL ? rank : 0, dc = chunks >= CL ? CL : 1;
-            if (leader && (chunks >= CL || x % CL == rank))
+            const int c0 = chunks >= MC ? rank % MC : 0, dc = chunks >= MC ? MC : 1;
+            if (leader && (chunks >= MC || x % MC == rank))
 #pragma unroll 1
-              for (int c = c0; c < chunks; c += dc)
-                tma_load_4d<CL>(map, &full[st],
-                                ring + st * C::kStageBytes + (c * tokens + r) * 128,
-                                ((keys ? h * chunks : 0) + c) * 64, g.head, (key0 + r) & (ps - 1),
-                                id);
+              for (int c = c0; c < chunks; c += dc) {
+                const uint32_t dst = ring + st * C::kStageBytes + (c * tokens + r) * 128;
+                const int col = ((keys ? h : rank * (SH - 1)) * chunks + c) * 64;
+                if (PAIR)
+                  tma_load_4d_pair(map, bar_addr, dst, col, g.head, (key0 + r) & (ps - 1), id);
+                else
+                  tma_load_4d<MC>(map, bar, dst, col, g.head, (key0 + r) & (ps - 1), id);
+              }
             __syncwarp();
           }
         }
@@ -656,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     // No copy may still be landing in shared memory when the CTA exits: the
     // last use of every stage and query tile.  After a timeout some of these
     // never began; the first wait that runs out ends the list.
-    if (keys && leader) {
+    if (keys && leader && !(PAIR && rank == 1)) {
       bool done = true;
       for (int i = max(0, pos - NS); i < pos && done; ++i)
         done = wait_drain(&full[i % NS], (uint32_t)(i / NS) & 1u);
@@ -670,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     // wait releases are on the critical path of the whole CTA (with a division
     // for the ring position and warp votes around the waits 4096 tokens behind
     // 12288 took 690 us), so ring positions are running counters.
-    if (elect_one()) {
+    if ((!PAIR || rank == 0) && elect_one()) {
       struct Cursor {
         int st;
         uint32_t ph;
@@ -687,8 +829,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       uint32_t qph = 0, segs = 0;
       bool ok = true, issued = false;
       auto need = [&](uint64_t* bar, uint32_t parity) {
-        if (mbar_try_wait(bar, parity)) return true;
-        ok = mbar_wait(bar, parity, abort_flag);
+        if (try_wait_scope<PAIR>(bar, parity)) return true;
+        ok = mbar_wait(bar, parity, abort_flag) && (!PAIR || try_wait_scope<PAIR>(bar, parity));
         return ok;
       };
       while (ok && w.next(p, g)) {
@@ -705,8 +847,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         auto scores = [&](int i, int j, int keys) {
           const int buf = NQ == 2 ? i : ((at + j) & 1);
           const uint32_t d = tmem + buf * 128u;
-          const uint32_t idesc =
-              idesc_16<FP16>(128, 0, false) | ((uint32_t)min(16, (keys + 15) >> 4 << 1) << 17);
+          // only the 16-key steps that are seen; a pair's keys lie in halves
+          const uint32_t cols = PAIR ? kKeys : min(kKeys, (keys + 15) & ~15);
+          const uint32_t idesc = idesc_16<FP16>(128 * SH, 0, false) | (cols >> 3 << 17);
           Cursor c = kc;
 #pragma unroll
           for (int h = 0; h < PARTS; ++h) {
@@ -717,15 +860,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             const uint32_t b = ring_k + c.st * (C::kStageBytes / 16);
 #pragma unroll
             for (int x = 0; x < CH * 4; ++x)
-              umma_ss(d, a + ((x >> 2) * (kRows * 128) + 32 * (x & 3)) / 16,
-                      b + ((x >> 2) * (kKeys * 128) + 32 * (x & 3)) / 16, idesc, h | x);
-            if (i == NQ - 1) commit_cluster<CL>(&empty[c.st]);
+              umma_ss<PAIR>(d, a + ((x >> 2) * (kRows * 128) + 32 * (x & 3)) / 16,
+                      b + ((x >> 2) * (KROWS * 128) + 32 * (x & 3)) / 16, idesc, h | x);
+            if (i == NQ - 1) commit_stage<PAIR, CL>(&empty[c.st]);
             c.add(1);
           }
-          umma_commit(&s_full[buf]);
+          commit_own<PAIR>(&s_full[buf]);
           issued = true;
           if (i == NQ - 1) {
-            if (j == g.n - 1) umma_commit(&q_empty[qb]);
+            if (j == g.n - 1) commit_own<PAIR>(&q_empty[qb]);
             kc.add(j == 0 ? PARTS : 2 * PARTS);
           }
         };
@@ -735,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
           const uint32_t use = NQ == 2 ? (uint32_t)(at + j) : (uint32_t)(at + j) >> 1;
           const uint32_t d = tmem + C::kO + i * D;
           const uint32_t a = tmem + buf * 128u;
-          constexpr uint32_t idesc = idesc_16<FP16>(128, D, true);
+          constexpr uint32_t idesc = idesc_16<FP16>(128 * SH, D, true);
           Cursor c = vc;
           // NQ = 2: the first 64 keys' weights come ahead of the others'
           if (!need(NQ == 2 ? &p_half[buf] : &p_full[buf], use & 1u)) return;
@@ -756,10 +899,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
                   if (!need(&p_full[buf], use & 1u)) return;
                   tc_fence_after();
                 }
-                umma_ts(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc,
+                umma_ts<PAIR>(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc,
                         h + k == 0 ? j != 0 : 1);
               }
-              if (i == NQ - 1) commit_cluster<CL>(&empty[c.st]);
+              if (i == NQ - 1) commit_stage<PAIR, CL>(&empty[c.st]);
               c.add(1);
             }
           } else {  // the item's last keys: only their 16-key steps
@@ -777,13 +920,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
               const uint32_t b = ring_v + c.st * (C::kStageBytes / 16);
 #pragma unroll 1
               for (int k = 0; k < SK && h * SK + k < ks; ++k)
-                umma_ts(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc, j | h | k);
-              if (i == NQ - 1) commit_cluster<CL>(&empty[c.st]);
+                umma_ts<PAIR>(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc, j | h | k);
+              if (i == NQ - 1) commit_stage<PAIR, CL>(&empty[c.st]);
               c.add(1);
             }
           }
-          umma_commit(&pv_done[i]);
-          if (j == g.n - 1) umma_commit(&o_full[i]);
+          commit_own<PAIR>(&pv_done[i]);
+          if (j == g.n - 1) commit_own<PAIR>(&o_full[i]);
           if (i == NQ - 1) {
             if (j == g.n - 1) {
               base = vc;
@@ -824,7 +967,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       }
       // every MMA issued here must have completed before TMEM is released
       if (issued) {
-        umma_commit(&drain);
+        if constexpr (PAIR)
+          asm volatile(
+              "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                  smem_u32(&drain))
+              : "memory");
+        else
+          umma_commit(&drain);
         if (!wait_drain(&drain, 0u)) report(p.status, kDevTimeout, kSiteAttnDrain, 99u, 0u);
       }
     }
@@ -841,6 +990,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     const int tok = row / p.group, gh = row - tok * p.group;
     int pos = 0, at = 0, segs = 0;  // ring position, key tiles, segments
     int xn = 0;           // exchanges (NQ = 1)
+    uint32_t tails = 0;   // waits for tail_full
     bool ok = true;
     JoinRec rec{0, 0, 0, 0};
     while (ok && w.next(p, g)) {
@@ -870,11 +1020,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
           constexpr int VK = kKeys / PARTS;
           const int h = vis / VK;  // the stage that holds the step
           const int st = (rp + h) % NS;
-          if (!mbar_wait(&full[st], (uint32_t)((rp + h) / NS) & 1u, abort_flag)) ok = false;
+          if (PAIR && rank == 1) {
+            if (!mbar_wait(&tail_full, tails++ & 1u, abort_flag)) ok = false;
+          } else if (!mbar_wait(&full[st], (uint32_t)((rp + h) / NS) & 1u, abort_flag)) {
+            ok = false;
+          }
           const int r0 = vis - h * VK, r1 = (r0 + 15) & ~15;
           constexpr int NT = NQ == 2 ? 128 : 256;
-          for (int x = (tid & (NT - 1)); x < (r1 - r0) * C::kChunks * 8; x += NT) {
-            const int u = x & 7, r = r0 + (x >> 3) / C::kChunks, c = (x >> 3) % C::kChunks;
+          constexpr int VCH = C::kChunks / SH;
+          for (int x = (tid & (NT - 1)); x < (r1 - r0) * VCH * 8; x += NT) {
+            const int u = x & 7, r = r0 + (x >> 3) / VCH, c = (x >> 3) % VCH;
             *reinterpret_cast<uint4*>(smem + st * C::kStageBytes + c * (VK * 128) + r * 128 +
                                       u * 16) = make_uint4(0, 0, 0, 0);
           }
@@ -959,7 +1114,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
               tmem_store_wait();
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&p_half[buf]);
+              if (lane == 0) arrive_first<PAIR>(&p_half[buf]);
             }
           }
           {
@@ -969,11 +1124,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
           tmem_store_wait();
         } else if (NQ == 2) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_half[buf]);
+          if (lane == 0) arrive_first<PAIR>(&p_half[buf]);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[buf]);
+        if (lane == 0) arrive_first<PAIR>(&p_full[buf]);
       }
       // ------------------------------------------------- end of the segment
       if (g.n) {
@@ -1052,7 +1207,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       if (g.n) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&o_empty[i]);
+        if (lane == 0) arrive_first<PAIR>(&o_empty[i]);
         pos += 2 * PARTS * g.n;
         at += g.n;
       }
@@ -1066,10 +1221,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
 
   tc_fence_before();
   __syncthreads();
+  if (PAIR) {  // the first CTA has waited for the pair's products
+    cluster_arrive();
+    cluster_wait();
+  }
   if (warp == 9) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if constexpr (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    else
+      tmem_dealloc(tmem, 512);
   }
   if (CL > 1) {  // a neighbour's copies and arrivals may still come here
     __syncwarp();
@@ -1182,18 +1344,22 @@ Layout layout_of(int head_dim) {
   return L;
 }
 
+// Head sizes whose many-row variant is a pair of CTAs with shared products.
+constexpr bool pair_of(int d) { return d == 256; }
+
 // The variants of a head size: few rows (one tile, no cluster) and many rows
 // (as wide an item as fits, clusters of two).
 template <int D, bool FP16>
 struct Variant {
   static constexpr int kManyNq = D == 256 ? 1 : 2;
-  static constexpr auto few = k_paged_attn<D, 1, 1, FP16>;
-  static constexpr auto many = k_paged_attn<D, kManyNq, 2, FP16>;
+  static constexpr bool kPair = pair_of(D);
+  static constexpr auto few = k_paged_attn<D, 1, 1, false, FP16>;
+  static constexpr auto many = k_paged_attn<D, kManyNq, 2, kPair, FP16>;
   static cudaError_t run(bool m, const AttnParams& p, int ctas, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = m ? Cfg<D, kManyNq>::kSmem : Cfg<D, 1>::kSmem;
+    cfg.dynamicSmemBytes = m ? Cfg<D, kManyNq, kPair>::kSmem : Cfg<D, 1, false>::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1213,10 +1379,10 @@ struct Variant {
   }
   static cudaError_t prepare() {
     cudaError_t e = cudaFuncSetAttribute(few, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)Cfg<D, 1>::kSmem);
+                                         (int)Cfg<D, 1, false>::kSmem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(many, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)Cfg<D, kManyNq>::kSmem);
+                               (int)Cfg<D, kManyNq, kPair>::kSmem);
     return e;
   }
 };
@@ -1354,8 +1520,13 @@ dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const 
     if (!encode_tiled(&p.qm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, q->p, dims, strides, box))
       return DG_ERR_CUDA;
   }
-  const int ps = c.page_size, kmax = 1 << key_shift_max(c.head_dim),
-            vmax = 1 << value_shift_max(c.head_dim);
+  // By the average rows of a sequence: few (one tile) or many.  Many: teams of
+  // two clusters when there are that many tiles.
+  const int64_t rows = (int64_t)n_tokens * group / batch->n_seqs;
+  const bool many = rows > kRows;
+  const int ps = c.page_size;
+  const int kmax = 1 << key_shift_max(c.head_dim, many && pair_of(c.head_dim));
+  const int vmax = 1 << value_shift_max(c.head_dim);
   const uint32_t kbox = ps < kmax ? ps : kmax, vbox = ps < vmax ? ps : vmax;
   if (!encode_pages(&p.km, c, c.k, layer, kbox) || !encode_pages(&p.vm, c, c.v, layer, vbox))
     return DG_ERR_CUDA;
@@ -1382,10 +1553,6 @@ dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const 
   p.ml = reinterpret_cast<float2*>(a->ws + a->L.ml);
   p.rec = reinterpret_cast<JoinRec*>(a->ws + a->L.rec);
   p.status = reinterpret_cast<DevStatus*>(a->ws + a->L.status);
-  // By the average rows of a sequence: few (one tile) or many.  Many: teams of
-  // two clusters when there are that many tiles.
-  const int64_t rows = (int64_t)n_tokens * group / batch->n_seqs;
-  const bool many = rows > kRows;
   const int wide = c.head_dim == 256 ? kRows : 2 * kRows;
   p.team = !many ? 1 : (rows > 2 * wide ? 4 : 2);
   const int ctas = a->ctas / p.team * p.team;
