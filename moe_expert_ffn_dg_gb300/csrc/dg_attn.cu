@@ -87,7 +87,7 @@ struct AttnParams {
   uint16_t* out;
   int64_t o_tok, o_head;
   float* lse;
-  float* part;   // [2 ctas][NQ * 128][D]
+  float4* part;  // [2 ctas][D / 4][NQ * 128]: four columns of a row
   float2* ml;    // [2 ctas][NQ * 128] (m, l)
   JoinRec* rec;  // [ctas]
   DevStatus* status;
@@ -1182,10 +1182,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
               *reinterpret_cast<uint4*>(dst + e) = v;
             }
           } else {
-            float* dst = p.part + prow * D + o0 + c;
+            // four columns of all rows together, so that a warp's rows are
+            // contiguous
+            float4* dst = p.part + ((size_t)slot * (D / 4) + (o0 + c) / 4) * (NQ * kRows) +
+                          i * kRows + row;
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              dst[e / 4 * (NQ * kRows)] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
         }
         if (row_live && (NQ == 2 || wg == 0)) {
@@ -1243,83 +1246,72 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
 }
 
 // Join the parts of the item that CTA blockIdx.x began: with m the largest
-// reference, o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i, parts in order.
-// A warp takes a row.
-// BATCH (divides 32): parts in flight.
+// reference, o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i, parts in order,
+// BATCH of them in flight.  A thread takes eight columns of a row,
+// neighbouring threads neighbouring rows.
 template <int D, int NQ, int BATCH, bool FP16>
 __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnParams p) {
   pdl_trigger();
   pdl_wait();
   const JoinRec rec = p.rec[blockIdx.x];
   if (rec.parts == 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int E = D / 32;
-  for (int vr = warp + 8 * (int)blockIdx.y; vr < rec.ntok * p.group; vr += 8 * (int)gridDim.y) {
+  constexpr int ROWS = NQ * kRows;
+  const int live = rec.ntok * p.group;
+  for (int u = threadIdx.x + 256 * (int)blockIdx.y; u < live * (D / 8);
+       u += 256 * (int)gridDim.y) {
+    const int c = u / live, vr = u - c * live;  // eight columns, row
     const int tok = vr / p.group, gh = vr - tok * p.group;
     const int i = tok / p.step;
     const int row = i * kRows + (tok - i * p.step) * p.group + gh;
-    auto prow = [&](int k) {
-      const int slot = 2 * ((int)blockIdx.x + k * p.team) + (k == 0 ? 1 : 0);
-      return (size_t)slot * (NQ * kRows) + row;
-    };
-    // statistics of the first 32 parts, one a lane (more are read again below)
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (lane < rec.parts) ml = p.ml[prow(lane)];
-    float m = ml.x;
-    for (int k = lane + 32; k < rec.parts; k += 32) m = fmaxf(m, p.ml[prow(k)].x);
-    float l = 0.f, acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    float m = -INFINITY, l = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int k0 = 0; k0 < rec.parts; k0 += BATCH) {
-      // the loads of a batch leave before the maximum is known
-      float v[BATCH][E];
+      float4 v[BATCH][2];
+      float2 ml[BATCH];
+      float top = m;
 #pragma unroll
       for (int k = 0; k < BATCH; ++k) {
-        const float* src = p.part + prow(min(k0 + k, rec.parts - 1)) * D + lane * E;
-        if constexpr (E == 2) {
-          *reinterpret_cast<float2*>(v[k]) = *reinterpret_cast<const float2*>(src);
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; e += 4)
-            *reinterpret_cast<float4*>(v[k] + e) = *reinterpret_cast<const float4*>(src + e);
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (k0 + k < rec.parts) {
+          const size_t slot = 2 * ((int)blockIdx.x + (k0 + k) * p.team) + (k0 + k == 0 ? 1 : 0);
+          ml[k] = p.ml[slot * ROWS + row];
+          const float4* src = p.part + (slot * (D / 4) + 2 * c) * ROWS + row;
+          v[k][0] = src[0];
+          v[k][1] = src[ROWS];
         }
       }
-      if (k0 == 0) {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int k = 0; k < BATCH; ++k) top = fmaxf(top, ml[k].x);
+      if (m != -INFINITY) {
+        const float f = exp2f(m - top);
+        l *= f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] *= f;
       }
+      m = top;
 #pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        if (k0 + k >= rec.parts) break;
-        float2 s;
-        if (k0 < 32) {
-          s.x = __shfl_sync(0xffffffffu, ml.x, k0 + k);
-          s.y = __shfl_sync(0xffffffffu, ml.y, k0 + k);
-        } else {
-          s = p.ml[prow(k0 + k)];
+      for (int k = 0; k < BATCH; ++k)
+        if (ml[k].x != -INFINITY) {  // a part that saw nothing holds nothing
+          const float f = exp2f(ml[k].x - m);
+          l += f * ml[k].y;
+          acc[0] += f * v[k][0].x;
+          acc[1] += f * v[k][0].y;
+          acc[2] += f * v[k][0].z;
+          acc[3] += f * v[k][0].w;
+          acc[4] += f * v[k][1].x;
+          acc[5] += f * v[k][1].y;
+          acc[6] += f * v[k][1].z;
+          acc[7] += f * v[k][1].w;
         }
-        if (s.x != -INFINITY) {  // a part that saw nothing holds nothing
-          const float f = exp2f(s.x - m);
-          l += f * s.y;
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += f * v[k][e];
-        }
-      }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint32_t r[E / 2];
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-      r[e / 2] = l == 0.f ? 0u : pack16<FP16>(acc[e] * inv, acc[e + 1] * inv);
+    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+    if (l != 0.f)
+      r = make_uint4(
+          pack16<FP16>(acc[0] * inv, acc[1] * inv), pack16<FP16>(acc[2] * inv, acc[3] * inv),
+          pack16<FP16>(acc[4] * inv, acc[5] * inv), pack16<FP16>(acc[6] * inv, acc[7] * inv));
     const int trow = rec.tok0 + tok, head = rec.head * p.group + gh;
-    uint16_t* dst = p.out + trow * p.o_tok + head * p.o_head + lane * E;
-    if constexpr (E == 2)
-      *reinterpret_cast<uint32_t*>(dst) = r[0];
-    else if constexpr (E == 4)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(r[0], r[1]);
-    else
-      *reinterpret_cast<uint4*>(dst) = make_uint4(r[0], r[1], r[2], r[3]);
-    if (p.lse && lane == 0)
+    *reinterpret_cast<uint4*>(p.out + trow * p.o_tok + head * p.o_head + 8 * c) = r;
+    if (p.lse && c == 0)
       p.lse[(size_t)trow * (p.kv_heads * p.group) + head] =
           l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
   }
@@ -1551,7 +1543,7 @@ dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const 
   p.o_tok = out->token_stride;
   p.o_head = out->head_stride;
   p.lse = lse;
-  p.part = reinterpret_cast<float*>(a->ws + a->L.part);
+  p.part = reinterpret_cast<float4*>(a->ws + a->L.part);
   p.ml = reinterpret_cast<float2*>(a->ws + a->L.ml);
   p.rec = reinterpret_cast<JoinRec*>(a->ws + a->L.rec);
   p.status = reinterpret_cast<DevStatus*>(a->ws + a->L.status);
