@@ -249,7 +249,8 @@ dg_status_t dg_attn_create(const dg_attn_config_t* cfg, const dg_kv_t* kv, void*
 dg_status_t dg_attn_destroy(dg_attn_t* a);
 
 /* q, out: [n_tokens, n_q_heads, head_dim], the cache's element type, 16-byte
- * aligned, strides multiples of 8 elements; out must not overlap q.  lse:
+ * aligned, strides multiples of 8 elements (q's not zero); out must not
+ * overlap q.  lse:
  * fp32 [n_tokens, n_q_heads] contiguous, or NULL.  Rows outside every
  * sequence are left alone. */
 dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const dg_heads_t* out,

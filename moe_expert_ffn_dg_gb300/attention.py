@@ -27,6 +27,14 @@ def _stream(device, stream=None) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _new(like: torch.Tensor, stream=None) -> torch.Tensor:
+    """A contiguous tensor of the same shape for a call on `stream`."""
+    out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if stream is not None:  # allocated on the current one
+        out.record_stream(stream)
+    return out
+
+
 def _heads(t: torch.Tensor, dtype, device, dim: int, what: str) -> B.dg_heads_t:
     """A [tokens, heads, dim] tensor as the library takes it."""
     shape, stride = t.shape, t.stride()
@@ -93,7 +101,7 @@ class Rope(_Handle):
         takes a gradient of the output to the gradient of the input.  out may
         be x."""
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            out = _new(x, stream)
         if x.dtype not in _DTYPES or out.shape != x.shape:
             raise ValueError("x: bf16, fp16 or fp32, out of the same shape")
         B.dg_rope_apply(self.handle, _DTYPES[x.dtype],
@@ -163,7 +171,7 @@ class KvCache(_Handle):
         cq = co = None
         if q is not None:
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                q_out = _new(q, stream)
             if q.shape[0] != n or q_out.shape != q.shape:
                 raise ValueError("q, q_out: one row a token")
             cq = _heads(q, self.dtype, self.device, self.head_dim, "q")
@@ -239,6 +247,9 @@ class KvPager:
             new = lens.new_empty  # cheaper than views of one allocation
             out = KvFork(new((n_new, row)), new(n_new), new(self.n_pages), new((n_new, 3)),
                          new(1))
+            if stream is not None:  # allocated on the current one
+                for t in (out.table, out.lens, out.ref, out.copies, out.short):
+                    t.record_stream(stream)
         f = B.dg_kv_fork_t(
             self.n_pages, self.page_size, row, n_old, n_new,
             _ints(table, dev, (n_old, row), "table"), _ints(lens, dev, (n_old,), "lens"),
@@ -282,8 +293,8 @@ class PagedAttention(_Handle):
         query's scores; (out, lse) is returned then."""
         c = self.cache
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if q.shape[1] != self.n_q_heads or out.shape != q.shape:
+            out = _new(q, stream)
+        if q.dim() != 3 or q.shape[1] != self.n_q_heads or out.shape != q.shape:
             raise ValueError("q, out: [tokens, n_q_heads, head_dim]")
         if lse is not None and (lse.dtype != torch.float32 or lse.device != c.device
                                 or not lse.is_contiguous()

@@ -193,3 +193,146 @@ def test_pages_before_the_window_may_be_gone():
     assert attn.device_status()[0] == 0
     tol, _ = tolerance(ref, BF, 128, 600)
     assert ((out.double().cpu() - ref[0]).abs() <= tol).all()
+
+
+def handles(data, left=-1, right=0, **kw):
+    import moe_expert_ffn_dg_gb300 as pkg
+    q, k, v, table, lens, cu = data
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cache = pkg.KvCache(k[None].cuda(), v[None].cuda())
+    batch = pkg.KvBatch(table.cuda(), torch.tensor(lens, **i32), torch.tensor(cu, **i32))
+    return (pkg.PagedAttention(cache, q.shape[1], left=left, right=right, **kw), q.cuda(), batch)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_replays_and_other_streams(d):
+    """A captured call reads lens, cu and the table again at every replay; the
+    same inputs give the same bits, on any stream."""
+    attn, q, batch = handles(make([90, 1, 140], [700, 300, 140], 4, 2, d, 32, BF, 20))
+    out = torch.zeros_like(q)
+    attn.forward(q, batch, out=out)
+    torch.cuda.synchronize()
+    first = out.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    alone = attn.forward(q, batch, stream=side)
+    side.synchronize()
+    assert torch.equal(alone, first)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        attn.forward(q, batch, out=out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+    # shorter caches, in the same tensors
+    batch.lens.copy_(torch.tensor([500, 17, 140], dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    again = attn.forward(q, batch)
+    assert torch.equal(out, again) and not torch.equal(out, first)
+    assert attn.device_status()[0] == 0
+
+
+def test_rows_outside_every_sequence_are_left_alone():
+    attn, q, batch = handles(make([3, 2], [50, 60], 4, 2, 64, 16, BF, 21))
+    whole = attn.forward(q, batch)
+    batch.cu.copy_(torch.tensor([1, 3, 4], dtype=torch.int32))
+    out = torch.full_like(q, 5.0)
+    attn.forward(q, batch, out=out)
+    torch.cuda.synchronize()
+    assert (out[[0, 4]] == 5.0).all() and not (out[1:4] == 5.0).all(-1).any()
+    # rows 1, 2 are now the last two tokens of the first sequence, as before
+    assert torch.equal(out[1:3], whole[1:3]) and attn.device_status()[0] == 0
+
+
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("n", [1, 200])
+def test_bad_pages_and_lengths_are_reported(d, n):
+    """A page id out of range reads as zeros, a length past the row is the
+    row's, a negative one zero; the status word says so once."""
+    from moe_expert_ffn_dg_gb300 import binding as B
+    attn, q, batch = handles(make([n], [n + 100], 2, 1, d, 16, BF, 22))
+    good = attn.forward(q, batch).clone()
+    for bad in (-1, 10 ** 9):
+        keep = batch.page_table[0, 2].clone()
+        batch.page_table[0, 2] = bad
+        out = attn.forward(q, batch)
+        assert attn.device_status()[:2] == (B.DG_ERR_DEVICE_CHECK, 36)
+        assert torch.isfinite(out).all()
+        batch.page_table[0, 2] = keep
+    for bad in (10 ** 9, -5):
+        keep = batch.lens.clone()
+        batch.lens.fill_(bad)
+        # the row's last page may hold anything past the true length
+        attn.forward(q, batch)
+        assert attn.device_status()[:2] == (B.DG_ERR_DEVICE_CHECK, 37)
+        batch.lens.copy_(keep)
+    batch.cu.copy_(torch.tensor([0, n + 7], dtype=torch.int32))
+    attn.forward(q, batch)
+    assert attn.device_status()[:2] == (B.DG_ERR_DEVICE_CHECK, 37)
+    batch.cu.copy_(torch.tensor([0, n], dtype=torch.int32))
+    assert torch.equal(attn.forward(q, batch), good) and attn.device_status()[0] == 0
+
+
+def test_layers_of_one_cache():
+    import moe_expert_ffn_dg_gb300 as pkg
+    data = make([5], [90], 2, 1, 128, 16, FP, 23)
+    q, k, v, table, lens, cu = data
+    i32 = dict(dtype=torch.int32, device="cuda")
+    batch = pkg.KvBatch(table.cuda(), torch.tensor(lens, **i32), torch.tensor(cu, **i32))
+    zero = torch.zeros_like(k)
+    cache = pkg.KvCache(torch.stack([zero, k]).cuda(), torch.stack([zero, v]).cuda())
+    attn = pkg.PagedAttention(cache, 2)
+    ref = attn_ref.attention(*data, -1, 0, 128 ** -0.5)
+    tol, _ = tolerance(ref, FP, 128, 90)
+    assert ((attn.forward(q.cuda(), batch, layer=1).double().cpu() - ref[0]).abs() <= tol).all()
+    assert (attn.forward(q.cuda(), batch, layer=0) == 0).all()
+
+
+def test_empty_calls():
+    attn, q, batch = handles(make([0, 0], [30, 0], 2, 1, 64, 16, BF, 24))
+    assert attn.forward(q, batch).shape == (0, 2, 64) and attn.device_status()[0] == 0
+
+
+def test_refusals():
+    import moe_expert_ffn_dg_gb300 as pkg
+    from moe_expert_ffn_dg_gb300 import binding as B
+    attn, q, batch = handles(make([4], [20], 4, 2, 64, 16, BF, 25))
+    cache = attn.cache
+    for kw, code in ((dict(n_q_heads=3), 1), (dict(n_q_heads=0), 1), (dict(n_q_heads=258), 3),
+                     (dict(n_q_heads=4, scale=0.0), 1), (dict(n_q_heads=4, scale=math.nan), 1),
+                     (dict(n_q_heads=4, scale=math.inf), 1), (dict(n_q_heads=4, scale=-1.0), 1)):
+        with pytest.raises(B.DgError) as e:
+            pkg.PagedAttention(cache, **kw)
+        assert e.value.status == code
+    wide = torch.zeros(4, 4, 72, dtype=BF, device="cuda")
+    for bad in (lambda: attn.forward(q[:, :2], batch), lambda: attn.forward(q.half(), batch),
+                lambda: attn.forward(q.cpu(), batch), lambda: attn.forward(q[..., :32], batch),
+                lambda: attn.forward(q, batch, lse=torch.zeros(4, 4, device="cuda").half()),
+                lambda: attn.forward(q, batch, lse=torch.zeros(4, 3, device="cuda")),
+                lambda: pkg.KvBatch(batch.page_table.long(), batch.lens, batch.cu),
+                lambda: pkg.KvBatch(batch.page_table, batch.lens, batch.cu[:1]),
+                lambda: pkg.KvCache(cache.k_pages[0], cache.v_pages[0]),
+                lambda: pkg.KvCache(cache.k_pages, cache.v_pages.half())):
+        with pytest.raises(ValueError):
+            bad()
+    for bad, code in ((lambda: attn.forward(q, batch, layer=1), B.DG_ERR_INVALID_ARG),
+                      (lambda: attn.forward(q, batch, out=q), B.DG_ERR_INVALID_ARG),
+                      (lambda: attn.forward(wide[..., 1:65], batch), B.DG_ERR_ALIGNMENT),
+                      (lambda: attn.forward(q[:, :1].expand(4, 4, 64), batch),
+                       B.DG_ERR_UNSUPPORTED),
+                      (lambda: pkg.KvCache(cache.k_pages.float(), cache.v_pages.float()),
+                       B.DG_ERR_UNSUPPORTED)):
+        with pytest.raises(B.DgError) as e:
+            bad()
+        assert e.value.status == code
+    with pytest.raises(B.DgError) as e:  # a workspace too small or misaligned
+        B.dg_attn_create(attn.cfg, cache.handle, attn.workspace.data_ptr() // 1024 * 1024, 1 << 20)
+    assert e.value.status == B.DG_ERR_WORKSPACE
+    with pytest.raises(B.DgError) as e:
+        B.dg_attn_create(attn.cfg, cache.handle, 1024 * 1024 + 16, 1 << 30)
+    assert e.value.status == B.DG_ERR_WORKSPACE
+    torch.cuda.synchronize()
+    assert attn.device_status()[0] == 0

@@ -335,3 +335,41 @@ def test_fork_bad_inputs_are_reported():
     assert s == B.DG_ERR_DEVICE_CHECK
     f, s = go([[0, 1]], [20], [0], [1])
     assert s == 0
+
+
+def test_steps_in_a_graph():
+    """Fork, split copies, append and gather captured once and replayed on new
+    contents of the same tensors."""
+    import moe_expert_ffn_dg_gb300 as pkg
+    ps, pages = 16, 40
+    k_pool, v_pool = pools(2, pages, ps, 2, 64, BF, seed=5)
+    cache, pager = pkg.KvCache(k_pool, v_pool), pkg.KvPager(pages, ps)
+    table = i32([[3, 5, -1, -1], [7, -1, -1, -1]])
+    lens, parent, grow = i32([20, 16]), i32([0, 0]), i32([3, 5])
+    ref = i32(np.bincount([3, 5, 7], minlength=pages))
+    kv = torch.randn(8, 4, 64, dtype=BF, device="cuda")
+    cu = i32([0, 3, 8])
+    rope = pkg.Rope(64)
+
+    def step(out=None):
+        f = pager.fork(table, lens, ref, parent, grow, out=out)
+        cache.copy(f.copies)
+        cache.append(kv[:, :2], kv[:, 2:], pkg.KvBatch(f.table, f.lens, cu), layer=1, rope=rope)
+        return f
+    f = step()
+    torch.cuda.synchronize()
+    first = [t.clone() for t in (k_pool, v_pool, f.table, f.lens, f.ref, f.copies)]
+    assert f.copies.tolist() == [[-1, -1, 0], [5, 0, 4]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(f)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(first, (k_pool, v_pool, f.table, f.lens, f.ref, f.copies)):
+        assert torch.equal(a, b)
+    parent.copy_(i32([1, 0]))  # another step: nothing is shared, nothing split
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (f.copies[:, 0] == -1).all() and f.lens.tolist() == [19, 25]
+    assert int(f.short[0]) == 0
+    assert cache.device_status()[0] == 0 and pager.device_status()[0] == 0
