@@ -243,6 +243,9 @@ class KvPager:
         freed, shared partly filled pages that grow are split (see
         ``include/dg_attn.h``).  out.ref may be ref."""
         dev, (n_old, row), n_new = self.device, table.shape, parent.shape[0]
+        inputs = (_ints(table, dev, (n_old, row), "table"), _ints(lens, dev, (n_old,), "lens"),
+                  _ints(ref, dev, (self.n_pages,), "ref"), _ints(parent, dev, (n_new,), "parent"),
+                  _ints(grow, dev, (n_new,), "grow"))
         if out is None:
             new = lens.new_empty  # cheaper than views of one allocation
             out = KvFork(new((n_new, row)), new(n_new), new(self.n_pages), new((n_new, 3)),
@@ -250,15 +253,15 @@ class KvPager:
             if stream is not None:  # allocated on the current one
                 for t in (out.table, out.lens, out.ref, out.copies, out.short):
                     t.record_stream(stream)
-        f = B.dg_kv_fork_t(
-            self.n_pages, self.page_size, row, n_old, n_new,
-            _ints(table, dev, (n_old, row), "table"), _ints(lens, dev, (n_old,), "lens"),
-            _ints(ref, dev, (self.n_pages,), "ref"), _ints(parent, dev, (n_new,), "parent"),
-            _ints(grow, dev, (n_new,), "grow"), _ints(out.table, dev, (n_new, row), "out.table"),
-            _ints(out.lens, dev, (n_new,), "out.lens"),
-            _ints(out.ref, dev, (self.n_pages,), "out.ref"),
-            _ints(out.copies, dev, (n_new, 3), "out.copies"),
-            _ints(out.short, dev, (1,), "out.short"))
+            outputs = (out.table.data_ptr(), out.lens.data_ptr(), out.ref.data_ptr(),
+                       out.copies.data_ptr(), out.short.data_ptr())
+        else:
+            outputs = (_ints(out.table, dev, (n_new, row), "out.table"),
+                       _ints(out.lens, dev, (n_new,), "out.lens"),
+                       _ints(out.ref, dev, (self.n_pages,), "out.ref"),
+                       _ints(out.copies, dev, (n_new, 3), "out.copies"),
+                       _ints(out.short, dev, (1,), "out.short"))
+        f = B.dg_kv_fork_t(self.n_pages, self.page_size, row, n_old, n_new, *inputs, *outputs)
         B.dg_kv_fork(f, self._ws, self._bytes, _stream(dev, stream))
         return out
 
