@@ -998,11 +998,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     while (ok && w.next(p, g)) {
       const bool row_live = tok < p.step && tok + i * p.step < g.ntok;
       const bool live = __any_sync(0xffffffffu, row_live);
-      int lo = 0, hi = 0;
+      // rows that are not there see all of the item, so that they need no mask
+      // (a warp with one takes the masked path at every tile otherwise: 1100
+      // cycles more a tile for single tokens); nothing of theirs is kept
+      int lo = 0, hi = g.khi;
       if (row_live) {
         const int qp = g.pos + i * p.step + tok;
         lo = p.left < 0 ? 0 : max(0, qp - p.left);
-        hi = p.right < 0 ? g.kv : min(g.kv, qp + p.right + 1);
+        hi = max(lo, p.right < 0 ? g.kv : min(g.kv, qp + p.right + 1));
       }
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < g.n; ++j) {
@@ -1046,7 +1049,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
           if (!__all_sync(0xffffffffu, rl <= 0 && rh >= NC)) {
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-              if (c < rl || c >= rh) s[c] = -INFINITY;
+              if ((unsigned)(c - rl) >= (unsigned)(rh - rl)) s[c] = -INFINITY;
           }
           float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -1071,7 +1074,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
           }
           const float mt = mx * p.scale2;
           // also true of the first key that a row sees (m is -inf before it)
-          const bool grown = mt > m + 8.f;
+          const bool grown = row_live && mt > m + 8.f;
           if (__any_sync(0xffffffffu, grown)) {
             const float fac = grown && m != -INFINITY ? exp2_fast(m - mt) : 1.f;
             if (grown) m = mt;
