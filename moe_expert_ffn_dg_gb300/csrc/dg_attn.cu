@@ -17,8 +17,8 @@
 // bf16 or fp16): O, which lives in tensor memory, is rescaled a few times a
 // row instead of once a tile.
 //
-// The items of a call are cut into units of one key tile, and the units dealt
-// evenly to one CTA an SM: a CTA takes a contiguous range, so long and short
+// The items of a call are cut into units of one key tile (and a few more where
+// an item begins, for what its ends cost), and the units dealt evenly to one CTA an SM: a CTA takes a contiguous range, so long and short
 // sequences, many and few tokens balance alike.  An item that crosses a range
 // boundary leaves fp32 partial results in the workspace, joined in a fixed
 // order by k_attn_join.
@@ -82,6 +82,7 @@ struct AttnParams {
   int kv_heads, group, step;  // step: tokens of a 128-row tile
   int q_box;                  // tokens of a query box
   int team;                   // CTAs that take neighbouring tiles of a sequence
+  int over;                   // what beginning an item costs, in key tiles
   int left, right;
   float scale2;  // scale log2 e
   uint16_t* out;
@@ -162,7 +163,7 @@ struct Seg {
 // Walk over the segments of a range of units; the same in every role.
 template <int NQ>
 struct Walk {
-  int h, b, t, skip;
+  int h, b, t, skip, over;
   long long u, end;
   Seq s;
   __device__ __forceinline__ bool next(const AttnParams& p, Seg& g) {
@@ -170,8 +171,10 @@ struct Walk {
     const int item = item_tokens<NQ>(p);
     const int2 tr = tile_range<NQ>(p, s, t);
     const int mine = t * item + (int)(blockIdx.x % p.team) * NQ * p.step;
-    const int cost = max(tr.y, 1);
+    const int cost = over + max(tr.y, 1);
     const int take = (int)min((long long)(cost - skip), end - u);
+    // only the units of its beginning: the next team takes the item whole
+    if (skip + take <= over) return false;
     g.head = h;
     g.b = b;
     g.tok0 = s.n0 + mine;
@@ -181,8 +184,9 @@ struct Walk {
     g.kv = s.kv;
     g.klo = k.x;
     g.khi = k.y;
-    g.kt0 = tr.x + skip;
-    g.n = tr.y ? take : 0;
+    const int tile = max(skip - over, 0);
+    g.kt0 = tr.x + tile;
+    g.n = tr.y ? skip + take - over - tile : 0;
     g.first = skip == 0;
     g.last = skip + take == cost;
     g.end = u - skip + cost;
@@ -206,7 +210,7 @@ struct Walk {
 };
 
 struct Start {
-  int h, b, t, skip;
+  int h, b, t, skip, over;
   long long u, end, total;
   int teams;
 };
@@ -495,6 +499,8 @@ __device__ __forceinline__ int v_stage(int j, int n) {
 template <int NQ>
 __device__ __forceinline__ void find_start(const AttnParams& p, long long* cost, Start* out) {
   const int tid = threadIdx.x, lane = tid & 31;
+  // key tiles in the low bits, items from here on: both add up
+  constexpr int kItemBit = 36;
   if (tid < 256) {
     int lps = 32;  // lanes a sequence
     while (lps > 1 && lps * p.n_seqs > 256) lps >>= 1;
@@ -504,7 +510,8 @@ __device__ __forceinline__ void find_start(const AttnParams& p, long long* cost,
       long long c = 0;
       if (b < p.n_seqs) {
         const Seq s = load_seq(p, b);
-        for (int t = sub; t * item_tokens<NQ>(p) < s.n; t += lps) c += max(tile_range<NQ>(p, s, t).y, 1);
+        for (int t = sub; t * item_tokens<NQ>(p) < s.n; t += lps)
+          c += ((long long)1 << kItemBit) + max(tile_range<NQ>(p, s, t).y, 1);
         if (blockIdx.x == 0 && sub == 0) {
           const int a = __ldg(p.cu + b), e = __ldg(p.cu + b + 1), kv = __ldg(p.lens + b);
           if (a < 0 || e < a || e > p.n_tokens || kv < 0 || kv > p.cap)
@@ -526,9 +533,20 @@ __device__ __forceinline__ void find_start(const AttnParams& p, long long* cost,
       const long long v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    const long long one = __shfl_sync(0xffffffffu, incl, 31);
+    long long one = __shfl_sync(0xffffffffu, incl, 31);
+    const int most = (int)(gridDim.x / p.team);
+    // Beginnings count where every team has several times their cost to do:
+    // then no two ranges begin inside one beginning.
+    const long long tiles = (one & (((long long)1 << kItemBit) - 1)) * p.kv_heads;
+    const int over = tiles >= (long long)most * max(8, 3 * p.over) ? p.over : 0;
+    auto units = [&](long long x) {
+      return (x & (((long long)1 << kItemBit) - 1)) + over * (x >> kItemBit);
+    };
+    one = units(one);
+    incl = units(incl);
+    sum = units(sum);
     const long long total = one * p.kv_heads;
-    const int teams = (int)min((long long)(gridDim.x / p.team), total);
+    const int teams = (int)min((long long)most, total);
     const int c = blockIdx.x / p.team;
     long long u0 = 0, u1 = 0;
     if (c < teams) {
@@ -549,7 +567,7 @@ __device__ __forceinline__ void find_start(const AttnParams& p, long long* cost,
       b = b0;
       if (mine) {
         r -= incl - sum;
-        while (r >= cost[b]) r -= cost[b++];
+        while (r >= units(cost[b])) r -= units(cost[b++]);
       }
       b = __shfl_sync(0xffffffffu, b, src);
       r = __shfl_sync(0xffffffffu, r, src);
@@ -557,7 +575,7 @@ __device__ __forceinline__ void find_start(const AttnParams& p, long long* cost,
       for (int base = 0;; base += 32) {
         const int tt = base + lane;
         int cc = 0;
-        if (tt * item_tokens<NQ>(p) < s.n) cc = max(tile_range<NQ>(p, s, tt).y, 1);
+        if (tt * item_tokens<NQ>(p) < s.n) cc = over + max(tile_range<NQ>(p, s, tt).y, 1);
         long long in = cc;
         for (int o = 1; o < 32; o <<= 1) {
           const long long v = __shfl_up_sync(0xffffffffu, in, o);
@@ -578,7 +596,11 @@ __device__ __forceinline__ void find_start(const AttnParams& p, long long* cost,
         }
       }
     }
-    if (lane == 0) *out = Start{h, b, t, skip, u0, u1, total, teams};
+    if (skip <= over) {  // inside an item's beginning: all of it is this team's
+      u0 -= skip;
+      skip = 0;
+    }
+    if (lane == 0) *out = Start{h, b, t, skip, over, u0, u1, total, teams};
   }
   fence_proxy_async_smem();  // `cost` lies where copies will land
   __syncthreads();
@@ -665,6 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   w.b = start.b;
   w.t = start.t;
   w.skip = start.skip;
+  w.over = start.over;
   w.u = start.u;
   w.end = start.end;
   if (w.u < w.end) w.s = load_seq(p, w.b);
@@ -1552,6 +1575,9 @@ dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const 
   p.status = reinterpret_cast<DevStatus*>(a->ws + a->L.status);
   const int wide = c.head_dim == 256 ? kRows : 2 * kRows;
   p.team = !many ? 1 : (rows > 2 * wide ? 4 : 2);
+  // Ending one item and beginning the next, in key tiles: results to write, and
+  // a pipeline to fill again.
+  p.over = !many ? 1 : (c.head_dim == 256 ? 6 : 2);
   const int ctas = a->ctas / p.team * p.team;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = c.dtype == DG_T_FP16 ? run_dim<true>(c.head_dim, many, p, ctas, s)
