@@ -165,7 +165,12 @@ template <int NQ>
 struct Walk {
   int h, b, t, skip, over;
   long long u, end;
-  Seq s;
+  Seq s, ahead;  // this sequence and the one after it
+  __device__ __forceinline__ void begin(const AttnParams& p) {
+    if (u >= end) return;
+    s = load_seq(p, b);
+    ahead = load_seq(p, b + 1 < p.n_seqs ? b + 1 : 0);
+  }
   __device__ __forceinline__ bool next(const AttnParams& p, Seg& g) {
     if (u >= end) return false;
     const int item = item_tokens<NQ>(p);
@@ -201,7 +206,9 @@ struct Walk {
             b = 0;
             ++h;
           }
-          s = load_seq(p, b);
+          // requested an item ago; the next one now
+          s = ahead;
+          ahead = load_seq(p, b + 1 < p.n_seqs ? b + 1 : 0);
         } while (s.n == 0);
       }
     }
@@ -690,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   w.over = start.over;
   w.u = start.u;
   w.end = start.end;
-  if (w.u < w.end) w.s = load_seq(p, w.b);
+  w.begin(p);
   Seg g;
 
   if (warp >= 8) {
@@ -1183,7 +1190,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         const int head = g.head * p.group + gh;
         const int slot = 2 * blockIdx.x + (g.first ? 1 : 0);
         const size_t prow = (size_t)slot * (NQ * kRows) + i * kRows + row;
-#pragma unroll
+        // (few rows: the code is fetched again for every item, so it stays short)
+#pragma unroll(CL == 1 ? 1 : OC / 32)
         for (int c = 0; c < OC; c += 32) {
           float o[32];
           if (g.n) {
