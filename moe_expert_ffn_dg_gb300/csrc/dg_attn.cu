@@ -18,16 +18,21 @@
 // row instead of once a tile.
 //
 // The items of a call are cut into units of one key tile (and a few more where
-// an item begins, for what its ends cost), and the units dealt evenly to one CTA an SM: a CTA takes a contiguous range, so long and short
-// sequences, many and few tokens balance alike.  An item that crosses a range
-// boundary leaves fp32 partial results in the workspace, joined in a fixed
-// order by k_attn_join.
+// an item begins, for what its ends cost: 8 canvases took 115 us without those,
+// 107 with), and the units dealt evenly to one CTA an SM: a CTA takes a
+// contiguous range, so long and short sequences, many and few tokens balance
+// alike.  An item that crosses a range boundary leaves fp32 partial results in
+// the workspace, joined in a fixed order by k_attn_join.  (Joined by the last
+// CTA to come instead: 118 us, for the code and registers in the main loop.)
 //
 // Query tiles of one sequence read the same keys.  `team` CTAs take as many
 // neighbouring tiles through the same key tiles at the same time, so that the
-// keys come from memory once, and the CL CTAs of a cluster (a team is made of
-// whole clusters) share each copy: every CTA loads its part of a stage and
-// multicasts it to all, and a stage is free once all have read it.
+// keys come from memory once, and the two CTAs of a cluster (a team is made of
+// whole clusters) share them: each loads half of a stage and multicasts it to
+// both, and a stage is free once both have read it.  At head size 256, where a
+// ring of whole tiles would be too shallow, the two are a pair with one
+// tcgen05.mma of 256 rows: each holds its own rows and half of every key and
+// value tile, and the first one issues for both.
 //
 // Warps 0-3 and 4-7: softmax; 8 and 10: TMA producers of keys and values; 9: MMA
 // issuer and TMEM owner.
@@ -35,6 +40,16 @@
 // warpgroup, which take turns on the tensor core.  NQ = 1 (few rows, or head
 // size 256, whose accumulator takes half of the TMEM): one tile, its key
 // tiles double-buffered, its columns halved between the warpgroups.
+//
+// What bounds it, and what it takes on one GB300 (page size 64, 32 and 16 query
+// heads on 8 key/value heads):
+//   64 single tokens over 471k cached ones, head size 128: memory, 279 us
+//     (6.9 TB/s; 317 us at page size 16, whose copies are 2 KB);
+//   8 canvases of 256 over 20k, head size 256: the tensor core at the power
+//     limit and the ends of items, 107-121 us (1.3-1.45 PFLOP/s);
+//   4096 tokens behind 12288, head size 128: the same and the exponentials
+//     between two products, 605-622 us (1.55-1.6 PFLOP/s);
+//   one token over 777, head size 64: latency, 9.6 us with the join.
 #include <math.h>
 #include <stdio.h>
 
@@ -333,7 +348,9 @@ __device__ __forceinline__ void set_max_regs_down() {
 }
 
 // log2 of the most tokens of a box.
-__host__ __device__ constexpr int key_shift_max(int d, bool pair) { return pair || d == 64 ? 6 : 7; }
+__host__ __device__ constexpr int key_shift_max(int d, bool pair) {
+  return pair || d == 64 ? 6 : 7;
+}
 __host__ __device__ constexpr int value_shift_max(int d) { return d == 128 ? 7 : 6; }
 
 // Two fp32 lanes of one instruction.
@@ -700,316 +717,317 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   w.begin(p);
   Seg g;
 
+  // nested, so that the registers of each side are its own
   if (warp >= 8) {
     set_max_regs_down<kRegsOther>();
-  if (warp == 8 || warp == 10) {
-    // ------------------------------------------------------------ producers
-    // Warp 8 fills the key stages (and the query tiles), warp 10 the value
-    // stages.  Uniform loops, one elected lane issues; of the cluster's CTAs
-    // each takes its share of the 64-column chunks (of the pieces at 64), of a
-    // pair's each its own half of the tile.
-    const bool leader = elect_one(), keys = warp == 8;
-    // whether stage h of a value tile holds the last keys seen, in a part of
-    // their 16-key step
-    auto clears_stage = [](int vis, int h) {
-      return vis < kKeys && (vis & 15) && vis / (kKeys / PARTS) == h;
-    };
-    const int ps = 1 << p.page_shift;
-    const int piece_shift =
-        min(p.page_shift, keys ? key_shift_max(D, PAIR) : value_shift_max(D));
-    const int piece = 1 << piece_shift;                    // tokens of a box
-    const int tokens = keys ? KROWS : kKeys / PARTS;       // of a stage
-    const int chunks = keys ? C::kChunks / PARTS : C::kChunks / SH;
-    const CUtensorMap* map = keys ? &p.km : &p.vm;
-    int pos = 0, qn = 0;
-    bool ok = true;
-    auto acquire = [&](uint64_t* bar, uint32_t parity) {
-      const bool here = mbar_wait(bar, parity, abort_flag);
-      ok = __all_sync(0xffffffffu, here);
-      return ok;
-    };
-    while (ok && w.next(p, g)) {
-      if (g.n == 0) continue;
-      if (keys) {
-        const int qb = qn % C::kQBufs;
-        if (!acquire(&q_empty[qb], ((uint32_t)(qn / C::kQBufs) & 1u) ^ 1u)) break;
-        ++qn;
-        if (leader) {
-          if (!PAIR || rank == 0)
-            mbar_arrive_expect_tx(&q_full[qb],
-                                  SH * NQ * C::kChunks * 128 * p.group * p.q_box);
-#pragma unroll 1
-          for (int x = 0; x < NQ * C::kChunks; ++x) {
-            const uint32_t dst = qbase + qb * NQ * C::kQTile + x * (kRows * 128);
-            const int c = 64 * (x % C::kChunks), row = g.tok0 + x / C::kChunks * p.step;
-            if (PAIR)
-              tma_load_3d_pair(&p.qm, first_cta(&q_full[qb]), dst, c, g.head * p.group, row);
-            else
-              tma_load_3d(&p.qm, &q_full[qb], dst, c, g.head * p.group, row);
-          }
-        }
-        __syncwarp();
-      }
-      // Page ids of 32 consecutive boxes, one a lane, and of the next 32.  An
-      // id out of range (or of a box that no query sees, whose page may be
-      // gone) becomes n_pages: the copy then reads zeros.
-      auto ids_at = [&](int base) {
-        int id = p.n_pages;
-        const int key = (base + lane) << piece_shift, pg = key >> p.page_shift;
-        if (key < g.khi && ((pg + 1) << p.page_shift) > g.klo) {
-          id = __ldg(p.table + (int64_t)g.b * p.table_stride + pg);
-          if ((unsigned)id >= (unsigned)p.n_pages) {
-            report(p.status, kDevBounds, kSiteAttnPage, (unsigned)g.b, (unsigned)id);
-            id = p.n_pages;
-          }
-        }
-        return id;
+    if (warp == 8 || warp == 10) {
+      // ------------------------------------------------------------ producers
+      // Warp 8 fills the key stages (and the query tiles), warp 10 the value
+      // stages.  Uniform loops, one elected lane issues; of the cluster's CTAs
+      // each takes its share of the 64-column chunks (of the pieces at 64), of a
+      // pair's each its own half of the tile.
+      const bool leader = elect_one(), keys = warp == 8;
+      // whether stage h of a value tile holds the last keys seen, in a part of
+      // their 16-key step
+      auto clears_stage = [](int vis, int h) {
+        return vis < kKeys && (vis & 15) && vis / (kKeys / PARTS) == h;
       };
-      int base = ((g.kt0 * kKeys) >> piece_shift) & ~31;
-      int ids = ids_at(base), ids_next = ids_at(base + 32);
-#pragma unroll 1
-      for (int j = 0; j < g.n && ok; ++j) {
-        const int rp = pos + (keys ? k_stage<PARTS>(j) : v_stage<PARTS>(j, g.n));
-        const int key_t = (g.kt0 + j) * kKeys;
-#pragma unroll 1
-        for (int h = 0; h < PARTS; ++h) {
-          const int st = (rp + h) % NS;
-          if (!acquire(&empty[st], ((uint32_t)((rp + h) / NS) & 1u) ^ 1u)) break;
-          const int key0 = key_t + (keys ? rank * (SH - 1) * KROWS : h * tokens);
-          auto live_from = [&](int key) {  // tokens of a stage from `key` on that are fetched
-            return max(0, min(tokens, (g.khi - key + piece - 1) & -piece));
-          };
-          const int live = live_from(key0);
-          // Pair: counted in the first CTA, both shares together; but values
-          // that the second CTA clears in part, it has to wait for itself.
-          uint64_t* bar = &full[st];
-          bool other = PAIR && rank == 1;
-          if (PAIR) {
-            const bool clears = !keys && clears_stage(g.khi - key_t, h);
-            if (other && clears) bar = &tail_full;
-            if (leader && (!other || clears))
-              mbar_arrive_expect_tx(bar, (live + (keys ? live_from(key_t + KROWS)
-                                                       : (clears ? 0 : live))) *
-                                             128 * chunks);
-            other = other && !clears;
-          } else if (leader) {
-            mbar_arrive_expect_tx(bar, live * 128 * chunks);
-          }
-          const uint32_t bar_addr = other ? first_cta(bar) : smem_u32(bar);
-#pragma unroll 1
-          for (int r = 0; r < live; r += piece) {
-            const int x = (key0 + r) >> piece_shift;
-            if (x - base >= 32) {
-              base += 32;
-              ids = ids_next;
-              ids_next = ids_at(base + 32);
-            }
-            const int id = __shfl_sync(0xffffffffu, ids, x & 31);
-            // the cluster's CTAs share the chunks, or the boxes of one chunk
-            const int c0 = chunks >= MC ? rank % MC : 0, dc = chunks >= MC ? MC : 1;
-            if (leader && (chunks >= MC || x % MC == rank))
-#pragma unroll 1
-              for (int c = c0; c < chunks; c += dc) {
-                const uint32_t dst = ring + st * C::kStageBytes + (c * tokens + r) * 128;
-                const int col = ((keys ? h : rank * (SH - 1)) * chunks + c) * 64;
-                if (PAIR)
-                  tma_load_4d_pair(map, bar_addr, dst, col, g.head, (key0 + r) & (ps - 1), id);
-                else
-                  tma_load_4d<MC>(map, bar, dst, col, g.head, (key0 + r) & (ps - 1), id);
-              }
-            __syncwarp();
-          }
-        }
-      }
-      pos += 2 * PARTS * g.n;
-    }
-    if (!ok) {
-      if (lane == 0) report(p.status, kDevTimeout, kSiteAttnLoad, (unsigned)pos, (unsigned)warp);
-      *abort_flag = 1;
-    }
-    // No copy may still be landing in shared memory when the CTA exits: the
-    // last use of every stage and query tile.  After a timeout some of these
-    // never began; the first wait that runs out ends the list.
-    if (keys && leader && !(PAIR && rank == 1)) {
-      bool done = true;
-      for (int i = max(0, pos - NS); i < pos && done; ++i)
-        done = wait_drain(&full[i % NS], (uint32_t)(i / NS) & 1u);
-      for (int i = max(0, qn - C::kQBufs); i < qn && done; ++i)
-        done = wait_drain(&q_full[i % C::kQBufs], (uint32_t)(i / C::kQBufs) & 1u);
-      if (!done && ok) report(p.status, kDevTimeout, kSiteAttnDrain, 0u, 0u);
-    }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ MMA issuer
-    // One elected lane.  Its instructions between a wait and the MMAs that the
-    // wait releases are on the critical path of the whole CTA (with a division
-    // for the ring position and warp votes around the waits 4096 tokens behind
-    // 12288 took 690 us), so ring positions are running counters.
-    if ((!PAIR || rank == 0) && elect_one()) {
-      struct Cursor {
-        int st;
-        uint32_t ph;
-        __device__ __forceinline__ void add(int n) {
-          st += n;
-          if (st >= NS) {
-            st -= NS;
-            ph ^= 1u;
-          }
-        }
-      };
-      Cursor base{0, 0u};
-      int qb = 0, at = 0;  // query buffer, key tiles
-      uint32_t qph = 0, segs = 0;
-      bool ok = true, issued = false;
-      auto need = [&](uint64_t* bar, uint32_t parity) {
-        if (try_wait_scope<PAIR>(bar, parity)) return true;
-        ok = mbar_wait(bar, parity, abort_flag) && (!PAIR || try_wait_scope<PAIR>(bar, parity));
+      const int ps = 1 << p.page_shift;
+      const int piece_shift =
+          min(p.page_shift, keys ? key_shift_max(D, PAIR) : value_shift_max(D));
+      const int piece = 1 << piece_shift;                    // tokens of a box
+      const int tokens = keys ? KROWS : kKeys / PARTS;       // of a stage
+      const int chunks = keys ? C::kChunks / PARTS : C::kChunks / SH;
+      const CUtensorMap* map = keys ? &p.km : &p.vm;
+      int pos = 0, qn = 0;
+      bool ok = true;
+      auto acquire = [&](uint64_t* bar, uint32_t parity) {
+        const bool here = mbar_wait(bar, parity, abort_flag);
+        ok = __all_sync(0xffffffffu, here);
         return ok;
       };
       while (ok && w.next(p, g)) {
         if (g.n == 0) continue;
-        Cursor kc = base, vc = base;
-        vc.add(g.n == 1 ? PARTS : 2 * PARTS);
-        if (!need(&q_full[qb], qph)) break;
-        const uint32_t q_lo = desc_lo(qbase + qb * NQ * C::kQTile, 16);
-        const uint32_t ring_k = desc_lo(ring, 16);
-        constexpr int SK = 8 / PARTS;  // 16-key steps of a value stage
-        const uint32_t ring_v = desc_lo(ring, SK * 2048);
-        int rem = g.khi - g.kt0 * kKeys;  // keys from the tile at hand on that some row sees
-        // S_i(j) = Q_i K_j^T for the tile under kc; `keys` of it are seen
-        auto scores = [&](int i, int j, int keys) {
-          const int buf = NQ == 2 ? i : ((at + j) & 1);
-          const uint32_t d = tmem + buf * 128u;
-          // only the 16-key steps that are seen; a pair's keys lie in halves
-          const uint32_t cols = PAIR ? kKeys : min(kKeys, (keys + 15) & ~15);
-          const uint32_t idesc = idesc_16<FP16>(128 * SH, 0, false) | (cols >> 3 << 17);
-          Cursor c = kc;
-#pragma unroll
+        if (keys) {
+          const int qb = qn % C::kQBufs;
+          if (!acquire(&q_empty[qb], ((uint32_t)(qn / C::kQBufs) & 1u) ^ 1u)) break;
+          ++qn;
+          if (leader) {
+            if (!PAIR || rank == 0)
+              mbar_arrive_expect_tx(&q_full[qb],
+                                    SH * NQ * C::kChunks * 128 * p.group * p.q_box);
+#pragma unroll 1
+            for (int x = 0; x < NQ * C::kChunks; ++x) {
+              const uint32_t dst = qbase + qb * NQ * C::kQTile + x * (kRows * 128);
+              const int c = 64 * (x % C::kChunks), row = g.tok0 + x / C::kChunks * p.step;
+              if (PAIR)
+                tma_load_3d_pair(&p.qm, first_cta(&q_full[qb]), dst, c, g.head * p.group, row);
+              else
+                tma_load_3d(&p.qm, &q_full[qb], dst, c, g.head * p.group, row);
+            }
+          }
+          __syncwarp();
+        }
+        // Page ids of 32 consecutive boxes, one a lane, and of the next 32.  An
+        // id out of range (or of a box that no query sees, whose page may be
+        // gone) becomes n_pages: the copy then reads zeros.
+        auto ids_at = [&](int base) {
+          int id = p.n_pages;
+          const int key = (base + lane) << piece_shift, pg = key >> p.page_shift;
+          if (key < g.khi && ((pg + 1) << p.page_shift) > g.klo) {
+            id = __ldg(p.table + (int64_t)g.b * p.table_stride + pg);
+            if ((unsigned)id >= (unsigned)p.n_pages) {
+              report(p.status, kDevBounds, kSiteAttnPage, (unsigned)g.b, (unsigned)id);
+              id = p.n_pages;
+            }
+          }
+          return id;
+        };
+        int base = ((g.kt0 * kKeys) >> piece_shift) & ~31;
+        int ids = ids_at(base), ids_next = ids_at(base + 32);
+#pragma unroll 1
+        for (int j = 0; j < g.n && ok; ++j) {
+          const int rp = pos + (keys ? k_stage<PARTS>(j) : v_stage<PARTS>(j, g.n));
+          const int key_t = (g.kt0 + j) * kKeys;
+#pragma unroll 1
           for (int h = 0; h < PARTS; ++h) {
-            if (i == 0 && !need(&full[c.st], c.ph)) return;
-            tc_fence_after();
-            constexpr int CH = C::kChunks / PARTS;
-            const uint32_t a = q_lo + (i * C::kQTile + h * CH * (kRows * 128)) / 16;
-            const uint32_t b = ring_k + c.st * (C::kStageBytes / 16);
-#pragma unroll
-            for (int x = 0; x < CH * 4; ++x)
-              umma_ss<PAIR>(d, a + ((x >> 2) * (kRows * 128) + 32 * (x & 3)) / 16,
-                      b + ((x >> 2) * (KROWS * 128) + 32 * (x & 3)) / 16, idesc, h | x);
-            if (i == NQ - 1) commit_stage<PAIR, CL>(&empty[c.st]);
-            c.add(1);
-          }
-          commit_own<PAIR>(&s_full[buf]);
-          issued = true;
-          if (i == NQ - 1) {
-            if (j == g.n - 1) commit_own<PAIR>(&q_empty[qb]);
-            kc.add(j == 0 ? PARTS : 2 * PARTS);
-          }
-        };
-        // O_i += P_i(j) V_j for the tile under vc
-        auto values = [&](int i, int j) {
-          const int buf = NQ == 2 ? i : ((at + j) & 1);
-          const uint32_t use = NQ == 2 ? (uint32_t)(at + j) : (uint32_t)(at + j) >> 1;
-          const uint32_t d = tmem + C::kO + i * D;
-          const uint32_t a = tmem + buf * 128u;
-          constexpr uint32_t idesc = idesc_16<FP16>(128 * SH, D, true);
-          Cursor c = vc;
-          // NQ = 2: the first 64 keys' weights come ahead of the others'
-          if (!need(NQ == 2 ? &p_half[buf] : &p_full[buf], use & 1u)) return;
-          if (j == 0 && !need(&o_empty[i], (segs & 1u) ^ 1u)) return;
-          if (i == 0 && !need(&full[c.st], c.ph)) return;
-          tc_fence_after();
-          if (rem >= kKeys) {
-#pragma unroll
-            for (int h = 0; h < PARTS; ++h) {
-              if (h > 0 && i == 0) {
-                if (!need(&full[c.st], c.ph)) return;
-                tc_fence_after();
+            const int st = (rp + h) % NS;
+            if (!acquire(&empty[st], ((uint32_t)((rp + h) / NS) & 1u) ^ 1u)) break;
+            const int key0 = key_t + (keys ? rank * (SH - 1) * KROWS : h * tokens);
+            auto live_from = [&](int key) {  // tokens of a stage from `key` on that are fetched
+              return max(0, min(tokens, (g.khi - key + piece - 1) & -piece));
+            };
+            const int live = live_from(key0);
+            // Pair: counted in the first CTA, both shares together; but values
+            // that the second CTA clears in part, it has to wait for itself.
+            uint64_t* bar = &full[st];
+            bool other = PAIR && rank == 1;
+            if (PAIR) {
+              const bool clears = !keys && clears_stage(g.khi - key_t, h);
+              if (other && clears) bar = &tail_full;
+              if (leader && (!other || clears))
+                mbar_arrive_expect_tx(bar, (live + (keys ? live_from(key_t + KROWS)
+                                                         : (clears ? 0 : live))) *
+                                               128 * chunks);
+              other = other && !clears;
+            } else if (leader) {
+              mbar_arrive_expect_tx(bar, live * 128 * chunks);
+            }
+            const uint32_t bar_addr = other ? first_cta(bar) : smem_u32(bar);
+#pragma unroll 1
+            for (int r = 0; r < live; r += piece) {
+              const int x = (key0 + r) >> piece_shift;
+              if (x - base >= 32) {
+                base += 32;
+                ids = ids_next;
+                ids_next = ids_at(base + 32);
               }
-              const uint32_t b = ring_v + c.st * (C::kStageBytes / 16);
-#pragma unroll
-              for (int k = 0; k < SK; ++k) {
-                if (NQ == 2 && h * SK + k == 4) {
-                  if (!need(&p_full[buf], use & 1u)) return;
-                  tc_fence_after();
+              const int id = __shfl_sync(0xffffffffu, ids, x & 31);
+              // the cluster's CTAs share the chunks, or the boxes of one chunk
+              const int c0 = chunks >= MC ? rank % MC : 0, dc = chunks >= MC ? MC : 1;
+              if (leader && (chunks >= MC || x % MC == rank))
+#pragma unroll 1
+                for (int c = c0; c < chunks; c += dc) {
+                  const uint32_t dst = ring + st * C::kStageBytes + (c * tokens + r) * 128;
+                  const int col = ((keys ? h : rank * (SH - 1)) * chunks + c) * 64;
+                  if (PAIR)
+                    tma_load_4d_pair(map, bar_addr, dst, col, g.head, (key0 + r) & (ps - 1), id);
+                  else
+                    tma_load_4d<MC>(map, bar, dst, col, g.head, (key0 + r) & (ps - 1), id);
                 }
-                umma_ts<PAIR>(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc,
-                        h + k == 0 ? j != 0 : 1);
-              }
-              if (i == NQ - 1) commit_stage<PAIR, CL>(&empty[c.st]);
-              c.add(1);
+              __syncwarp();
             }
-          } else {  // the item's last keys: only their 16-key steps
-            if (NQ == 2) {
-              if (!need(&p_full[buf], use & 1u)) return;
-              tc_fence_after();
-            }
-            const int ks = (rem + 15) >> 4;
-#pragma unroll 1
-            for (int h = 0; h < PARTS; ++h) {
-              if (h > 0 && i == 0) {
-                if (!need(&full[c.st], c.ph)) return;
-                tc_fence_after();
-              }
-              const uint32_t b = ring_v + c.st * (C::kStageBytes / 16);
-#pragma unroll 1
-              for (int k = 0; k < SK && h * SK + k < ks; ++k)
-                umma_ts<PAIR>(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc, j | h | k);
-              if (i == NQ - 1) commit_stage<PAIR, CL>(&empty[c.st]);
-              c.add(1);
-            }
-          }
-          commit_own<PAIR>(&pv_done[i]);
-          if (j == g.n - 1) commit_own<PAIR>(&o_full[i]);
-          if (i == NQ - 1) {
-            if (j == g.n - 1) {
-              base = vc;
-              base.add(PARTS);
-            }
-            vc.add(j + 1 < g.n - 1 ? 2 * PARTS : PARTS);
-            rem -= kKeys;
-          }
-        };
-        if (NQ == 2) {
-          scores(0, 0, rem);
-          if (ok) scores(1, 0, rem);
-          for (int j = 0; j < g.n && ok; ++j) {
-            const int next = rem - kKeys;
-            values(0, j);
-            if (ok && j + 1 < g.n) scores(0, j + 1, next);
-            if (ok) values(1, j);
-            if (ok && j + 1 < g.n) scores(1, j + 1, next);
-          }
-        } else {
-          scores(0, 0, rem);
-          if (ok && g.n > 1) scores(0, 1, rem - kKeys);
-          for (int j = 0; j < g.n && ok; ++j) {
-            values(0, j);
-            if (ok && j + 2 < g.n) scores(0, j + 2, rem - kKeys);
           }
         }
-        at += g.n;
-        ++segs;
-        if (++qb == C::kQBufs) {
-          qb = 0;
-          qph ^= 1u;
-        }
+        pos += 2 * PARTS * g.n;
       }
       if (!ok) {
-        report(p.status, kDevTimeout, kSiteAttnMma, (unsigned)at, segs);
+        if (lane == 0) report(p.status, kDevTimeout, kSiteAttnLoad, (unsigned)pos, (unsigned)warp);
         *abort_flag = 1;
       }
-      // every MMA issued here must have completed before TMEM is released
-      if (issued) {
-        if constexpr (PAIR)
-          asm volatile(
-              "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                  smem_u32(&drain))
-              : "memory");
-        else
-          umma_commit(&drain);
-        if (!wait_drain(&drain, 0u)) report(p.status, kDevTimeout, kSiteAttnDrain, 99u, 0u);
+      // No copy may still be landing in shared memory when the CTA exits: the
+      // last use of every stage and query tile.  After a timeout some of these
+      // never began; the first wait that runs out ends the list.
+      if (keys && leader && !(PAIR && rank == 1)) {
+        bool done = true;
+        for (int i = max(0, pos - NS); i < pos && done; ++i)
+          done = wait_drain(&full[i % NS], (uint32_t)(i / NS) & 1u);
+        for (int i = max(0, qn - C::kQBufs); i < qn && done; ++i)
+          done = wait_drain(&q_full[i % C::kQBufs], (uint32_t)(i / C::kQBufs) & 1u);
+        if (!done && ok) report(p.status, kDevTimeout, kSiteAttnDrain, 0u, 0u);
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ MMA issuer
+      // One elected lane.  Its instructions between a wait and the MMAs that the
+      // wait releases are on the critical path of the whole CTA (with a division
+      // for the ring position and warp votes around the waits 4096 tokens behind
+      // 12288 took 690 us), so ring positions are running counters.
+      if ((!PAIR || rank == 0) && elect_one()) {
+        struct Cursor {
+          int st;
+          uint32_t ph;
+          __device__ __forceinline__ void add(int n) {
+            st += n;
+            if (st >= NS) {
+              st -= NS;
+              ph ^= 1u;
+            }
+          }
+        };
+        Cursor base{0, 0u};
+        int qb = 0, at = 0;  // query buffer, key tiles
+        uint32_t qph = 0, segs = 0;
+        bool ok = true, issued = false;
+        auto need = [&](uint64_t* bar, uint32_t parity) {
+          if (try_wait_scope<PAIR>(bar, parity)) return true;
+          ok = mbar_wait(bar, parity, abort_flag) && (!PAIR || try_wait_scope<PAIR>(bar, parity));
+          return ok;
+        };
+        while (ok && w.next(p, g)) {
+          if (g.n == 0) continue;
+          Cursor kc = base, vc = base;
+          vc.add(g.n == 1 ? PARTS : 2 * PARTS);
+          if (!need(&q_full[qb], qph)) break;
+          const uint32_t q_lo = desc_lo(qbase + qb * NQ * C::kQTile, 16);
+          const uint32_t ring_k = desc_lo(ring, 16);
+          constexpr int SK = 8 / PARTS;  // 16-key steps of a value stage
+          const uint32_t ring_v = desc_lo(ring, SK * 2048);
+          int rem = g.khi - g.kt0 * kKeys;  // keys from the tile at hand on that some row sees
+          // S_i(j) = Q_i K_j^T for the tile under kc; `keys` of it are seen
+          auto scores = [&](int i, int j, int keys) {
+            const int buf = NQ == 2 ? i : ((at + j) & 1);
+            const uint32_t d = tmem + buf * 128u;
+            // only the 16-key steps that are seen; a pair's keys lie in halves
+            const uint32_t cols = PAIR ? kKeys : min(kKeys, (keys + 15) & ~15);
+            const uint32_t idesc = idesc_16<FP16>(128 * SH, 0, false) | (cols >> 3 << 17);
+            Cursor c = kc;
+#pragma unroll
+            for (int h = 0; h < PARTS; ++h) {
+              if (i == 0 && !need(&full[c.st], c.ph)) return;
+              tc_fence_after();
+              constexpr int CH = C::kChunks / PARTS;
+              const uint32_t a = q_lo + (i * C::kQTile + h * CH * (kRows * 128)) / 16;
+              const uint32_t b = ring_k + c.st * (C::kStageBytes / 16);
+#pragma unroll
+              for (int x = 0; x < CH * 4; ++x)
+                umma_ss<PAIR>(d, a + ((x >> 2) * (kRows * 128) + 32 * (x & 3)) / 16,
+                        b + ((x >> 2) * (KROWS * 128) + 32 * (x & 3)) / 16, idesc, h | x);
+              if (i == NQ - 1) commit_stage<PAIR, CL>(&empty[c.st]);
+              c.add(1);
+            }
+            commit_own<PAIR>(&s_full[buf]);
+            issued = true;
+            if (i == NQ - 1) {
+              if (j == g.n - 1) commit_own<PAIR>(&q_empty[qb]);
+              kc.add(j == 0 ? PARTS : 2 * PARTS);
+            }
+          };
+          // O_i += P_i(j) V_j for the tile under vc
+          auto values = [&](int i, int j) {
+            const int buf = NQ == 2 ? i : ((at + j) & 1);
+            const uint32_t use = NQ == 2 ? (uint32_t)(at + j) : (uint32_t)(at + j) >> 1;
+            const uint32_t d = tmem + C::kO + i * D;
+            const uint32_t a = tmem + buf * 128u;
+            constexpr uint32_t idesc = idesc_16<FP16>(128 * SH, D, true);
+            Cursor c = vc;
+            // NQ = 2: the first 64 keys' weights come ahead of the others'
+            if (!need(NQ == 2 ? &p_half[buf] : &p_full[buf], use & 1u)) return;
+            if (j == 0 && !need(&o_empty[i], (segs & 1u) ^ 1u)) return;
+            if (i == 0 && !need(&full[c.st], c.ph)) return;
+            tc_fence_after();
+            if (rem >= kKeys) {
+#pragma unroll
+              for (int h = 0; h < PARTS; ++h) {
+                if (h > 0 && i == 0) {
+                  if (!need(&full[c.st], c.ph)) return;
+                  tc_fence_after();
+                }
+                const uint32_t b = ring_v + c.st * (C::kStageBytes / 16);
+#pragma unroll
+                for (int k = 0; k < SK; ++k) {
+                  if (NQ == 2 && h * SK + k == 4) {
+                    if (!need(&p_full[buf], use & 1u)) return;
+                    tc_fence_after();
+                  }
+                  umma_ts<PAIR>(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc,
+                          h + k == 0 ? j != 0 : 1);
+                }
+                if (i == NQ - 1) commit_stage<PAIR, CL>(&empty[c.st]);
+                c.add(1);
+              }
+            } else {  // the item's last keys: only their 16-key steps
+              if (NQ == 2) {
+                if (!need(&p_full[buf], use & 1u)) return;
+                tc_fence_after();
+              }
+              const int ks = (rem + 15) >> 4;
+#pragma unroll 1
+              for (int h = 0; h < PARTS; ++h) {
+                if (h > 0 && i == 0) {
+                  if (!need(&full[c.st], c.ph)) return;
+                  tc_fence_after();
+                }
+                const uint32_t b = ring_v + c.st * (C::kStageBytes / 16);
+#pragma unroll 1
+                for (int k = 0; k < SK && h * SK + k < ks; ++k)
+                  umma_ts<PAIR>(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc, j | h | k);
+                if (i == NQ - 1) commit_stage<PAIR, CL>(&empty[c.st]);
+                c.add(1);
+              }
+            }
+            commit_own<PAIR>(&pv_done[i]);
+            if (j == g.n - 1) commit_own<PAIR>(&o_full[i]);
+            if (i == NQ - 1) {
+              if (j == g.n - 1) {
+                base = vc;
+                base.add(PARTS);
+              }
+              vc.add(j + 1 < g.n - 1 ? 2 * PARTS : PARTS);
+              rem -= kKeys;
+            }
+          };
+          if (NQ == 2) {
+            scores(0, 0, rem);
+            if (ok) scores(1, 0, rem);
+            for (int j = 0; j < g.n && ok; ++j) {
+              const int next = rem - kKeys;
+              values(0, j);
+              if (ok && j + 1 < g.n) scores(0, j + 1, next);
+              if (ok) values(1, j);
+              if (ok && j + 1 < g.n) scores(1, j + 1, next);
+            }
+          } else {
+            scores(0, 0, rem);
+            if (ok && g.n > 1) scores(0, 1, rem - kKeys);
+            for (int j = 0; j < g.n && ok; ++j) {
+              values(0, j);
+              if (ok && j + 2 < g.n) scores(0, j + 2, rem - kKeys);
+            }
+          }
+          at += g.n;
+          ++segs;
+          if (++qb == C::kQBufs) {
+            qb = 0;
+            qph ^= 1u;
+          }
+        }
+        if (!ok) {
+          report(p.status, kDevTimeout, kSiteAttnMma, (unsigned)at, segs);
+          *abort_flag = 1;
+        }
+        // every MMA issued here must have completed before TMEM is released
+        if (issued) {
+          if constexpr (PAIR)
+            asm volatile(
+                "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                    smem_u32(&drain))
+                : "memory");
+          else
+            umma_commit(&drain);
+          if (!wait_drain(&drain, 0u)) report(p.status, kDevTimeout, kSiteAttnDrain, 99u, 0u);
+        }
       }
     }
-  }
   } else {
     set_max_regs_up<kRegsSoftmax>();
     // ------------------------------------------------------------ softmax
