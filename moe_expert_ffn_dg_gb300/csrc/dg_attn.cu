@@ -685,6 +685,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     tma_prefetch_map(&p.km);
     tma_prefetch_map(&p.vm);
   }
+  if (PAIR) {  // the pair allocates together: both CTAs have to be there
+    cluster_arrive();
+    cluster_wait();
+  }
   if (warp == 9) {
     if constexpr (PAIR) {
       asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -848,12 +852,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       // No copy may still be landing in shared memory when the CTA exits: the
       // last use of every stage and query tile.  After a timeout some of these
       // never began; the first wait that runs out ends the list.
-      if (keys && leader && !(PAIR && rank == 1)) {
+      if (keys && leader) {
         bool done = true;
-        for (int i = max(0, pos - NS); i < pos && done; ++i)
-          done = wait_drain(&full[i % NS], (uint32_t)(i / NS) & 1u);
-        for (int i = max(0, qn - C::kQBufs); i < qn && done; ++i)
-          done = wait_drain(&q_full[i % C::kQBufs], (uint32_t)(i / C::kQBufs) & 1u);
+        if (!(PAIR && rank == 1)) {
+          for (int i = max(0, pos - NS); i < pos && done; ++i)
+            done = wait_drain(&full[i % NS], (uint32_t)(i / NS) & 1u);
+          for (int i = max(0, qn - C::kQBufs); i < qn && done; ++i)
+            done = wait_drain(&q_full[i % C::kQBufs], (uint32_t)(i / C::kQBufs) & 1u);
+        }
+        // Nor may an arrival of the other CTA's products still be on its way to
+        // this one's barriers: it must not meet a CTA that has gone.
+        if (CL > 1) {
+          for (int i = max(0, pos - NS); i < pos && done; ++i)
+            done = wait_drain(&empty[i % NS], (uint32_t)(i / NS) & 1u);
+          for (int i = max(0, qn - C::kQBufs); i < qn && done; ++i)
+            done = wait_drain(&q_empty[i % C::kQBufs], (uint32_t)(i / C::kQBufs) & 1u);
+          const int tiles = pos / (2 * PARTS);
+          for (int i = 0; i < NQ && tiles > 0 && done; ++i)
+            done = wait_drain(&pv_done[i], (uint32_t)(tiles - 1) & 1u);
+        }
         if (!done && ok) report(p.status, kDevTimeout, kSiteAttnDrain, 0u, 0u);
       }
     } else if (warp == 9) {
