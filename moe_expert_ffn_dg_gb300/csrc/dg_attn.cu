@@ -644,8 +644,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   const uint32_t qbase = ring + NS * C::kStageBytes;
   __shared__ uint64_t full[NS], empty[NS];
   __shared__ uint64_t q_full[C::kQBufs], q_empty[C::kQBufs];
-  __shared__ uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], o_full[2], o_empty[2], drain;
-  __shared__ uint64_t tail_full;  // pair, second CTA: the values that it clears
+  __shared__ uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], o_full[2], drain;
+  // Pair, second CTA: the values that it clears.  One a stage: several may be on
+  // their way, and a barrier must not be armed again before its phase is over.
+  __shared__ uint64_t tail_full[PAIR ? NS : 1];
   __shared__ uint32_t tmem_holder;
   __shared__ int abort_word;
   __shared__ Start start;
@@ -673,10 +675,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       mbar_init(&p_full[i], (NQ == 2 ? 4 : 8) * SH);
       mbar_init(&pv_done[i], 1);
       mbar_init(&o_full[i], 1);
-      mbar_init(&o_empty[i], (NQ == 2 ? 4 : 8) * SH);
     }
     mbar_init(&drain, 1);
-    mbar_init(&tail_full, 1);
+    for (int i = 0; i < (PAIR ? NS : 0); ++i) mbar_init(&tail_full[i], 1);
     abort_word = 0;
     fence_mbar_init();
   }
@@ -686,6 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     tma_prefetch_map(&p.vm);
   }
   if (PAIR) {  // the pair allocates together: both CTAs have to be there
+    __syncwarp();
     cluster_arrive();
     cluster_wait();
   }
@@ -705,6 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   find_start<NQ>(p, reinterpret_cast<long long*>(smem), &start);
   tc_fence_after();
   if (CL > 1) {  // a neighbour's copies and arrivals need the barriers, and the ring to be free
+    __syncwarp();
     cluster_arrive();
     cluster_wait();
   }
@@ -808,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             bool other = PAIR && rank == 1;
             if (PAIR) {
               const bool clears = !keys && clears_stage(g.khi - key_t, h);
-              if (other && clears) bar = &tail_full;
+              if (other && clears) bar = &tail_full[PAIR ? st : 0];
               if (leader && (!other || clears))
                 mbar_arrive_expect_tx(bar, (live + (keys ? live_from(key_t + KROWS)
                                                          : (clears ? 0 : live))) *
@@ -893,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         };
         Cursor base{0, 0u};
         int qb = 0, at = 0;  // query buffer, key tiles
-        uint32_t qph = 0, segs = 0;
+        uint32_t qph = 0;
         bool ok = true, issued = false;
         auto need = [&](uint64_t* bar, uint32_t parity) {
           if (try_wait_scope<PAIR>(bar, parity)) return true;
@@ -947,9 +950,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             const uint32_t a = tmem + buf * 128u;
             constexpr uint32_t idesc = idesc_16<FP16>(128 * SH, D, true);
             Cursor c = vc;
-            // NQ = 2: the first 64 keys' weights come ahead of the others'
+            // NQ = 2: the first 64 keys' weights come ahead of the others'.  A
+            // segment's first weights also say that O has been read: a warp
+            // writes out the last segment's before it makes them.
             if (!need(NQ == 2 ? &p_half[buf] : &p_full[buf], use & 1u)) return;
-            if (j == 0 && !need(&o_empty[i], (segs & 1u) ^ 1u)) return;
             if (i == 0 && !need(&full[c.st], c.ph)) return;
             tc_fence_after();
             if (rem >= kKeys) {
@@ -1022,14 +1026,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             }
           }
           at += g.n;
-          ++segs;
           if (++qb == C::kQBufs) {
             qb = 0;
             qph ^= 1u;
           }
         }
         if (!ok) {
-          report(p.status, kDevTimeout, kSiteAttnMma, (unsigned)at, segs);
+          report(p.status, kDevTimeout, kSiteAttnMma, (unsigned)at, 0u);
           *abort_flag = 1;
         }
         // every MMA issued here must have completed before TMEM is released
@@ -1057,7 +1060,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     const int tok = row / p.group, gh = row - tok * p.group;
     int pos = 0, at = 0, segs = 0;  // ring position, key tiles, segments
     int xn = 0;           // exchanges (NQ = 1)
-    uint32_t tails = 0;   // waits for tail_full
+    uint32_t tails = 0;   // phase of each stage's tail_full
     bool ok = true;
     JoinRec rec{0, 0, 0, 0};
     while (ok && w.next(p, g)) {
@@ -1090,11 +1093,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
           constexpr int VK = kKeys / PARTS;
           const int h = vis / VK;  // the stage that holds the step
           const int st = (rp + h) % NS;
+          bool here;
           if (PAIR && rank == 1) {
-            if (!mbar_wait(&tail_full, tails++ & 1u, abort_flag)) ok = false;
-          } else if (!mbar_wait(&full[st], (uint32_t)((rp + h) / NS) & 1u, abort_flag)) {
-            ok = false;
+            here = mbar_wait(&tail_full[PAIR ? st : 0], (tails >> st) & 1u, abort_flag);
+            tails ^= 1u << st;
+          } else {
+            here = mbar_wait(&full[st], (uint32_t)((rp + h) / NS) & 1u, abort_flag);
           }
+          ok = __all_sync(0xffffffffu, here) && ok;
           const int r0 = vis - h * VK, r1 = (r0 + 15) & ~15;
           constexpr int NT = NQ == 2 ? 128 : 256;
           constexpr int VCH = C::kChunks / SH;
@@ -1279,9 +1285,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         rec.ntok = g.ntok;
       }
       if (g.n) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_first<PAIR>(&o_empty[i]);
         pos += 2 * PARTS * g.n;
         at += g.n;
       }
@@ -1296,6 +1299,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   tc_fence_before();
   __syncthreads();
   if (PAIR) {  // the first CTA has waited for the pair's products
+    __syncwarp();
     cluster_arrive();
     cluster_wait();
   }

@@ -336,3 +336,12 @@ def test_refusals():
     assert e.value.status == B.DG_ERR_WORKSPACE
     torch.cuda.synchronize()
     assert attn.device_status()[0] == 0
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_short_items_with_ragged_ends(d):
+    """A CTA goes through many items of one or two key tiles each, every one of
+    which ends inside a 16-key step (their cleared values follow one another
+    closely)."""
+    check(make([150, 141, 160], [152, 150, 163], 32, 2, d, 64, BF, 30), 90, 1)
+    check(make([97, 150], [97, 331], 24, 3, d, 256, FP, 31), 30, 0)
