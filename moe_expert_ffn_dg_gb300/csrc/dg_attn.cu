@@ -1117,10 +1117,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
           if constexpr (NC == 128) tmem_load128(ts, s);
           else tmem_load64(ts + c0, s);
           const int rl = lo - key0 - c0, rh = hi - key0 - c0;
+          // blocks of columns that every row sees need no mask
           if (!__all_sync(0xffffffffu, rl <= 0 && rh >= NC)) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-              if ((unsigned)(c - rl) >= (unsigned)(rh - rl)) s[c] = -INFINITY;
+            for (int b = 0; b < NC; b += 32)
+              if (!__all_sync(0xffffffffu, rl <= b && rh >= b + 32)) {
+#pragma unroll
+                for (int c = b; c < b + 32; ++c)
+                  if ((unsigned)(c - rl) >= (unsigned)(rh - rl)) s[c] = -INFINITY;
+              }
           }
           float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
