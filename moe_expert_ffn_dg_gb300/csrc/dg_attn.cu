@@ -1420,7 +1420,7 @@ Layout layout_of(int head_dim) {
 constexpr bool pair_of(int d) { return d == 256; }
 
 // The variants of a head size: few rows (one tile, no cluster) and many rows
-// (as wide an item as fits, clusters of two).
+// (as wide an item as fits, clusters of two; dg_attn_forward chooses).
 template <int D, bool FP16>
 struct Variant {
   static constexpr int kManyNq = D == 256 ? 1 : 2;
@@ -1592,10 +1592,13 @@ dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const 
     if (!encode_tiled(&p.qm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, q->p, dims, strides, box))
       return DG_ERR_CUDA;
   }
-  // By the average rows of a sequence: few (one tile) or many.  Many: teams of
-  // two clusters when there are that many tiles.
+  // Few rows (one tile a CTA) or many, by the average rows of a sequence.  16
+  // sequences behind 4000 cached tokens, 4 query heads a key/value head, us few
+  // / many: head size 64: 65 / 90 at 256 rows, 112 / 94 at 512; 128: 65 / 95 at
+  // 128, 103 / 102 at 192, 178 / 115 at 512; 256: 93 / 94 at 32, 101 / 97 at 64,
+  // 198 / 111 at 256.
   const int64_t rows = (int64_t)n_tokens * group / batch->n_seqs;
-  const bool many = rows > kRows;
+  const bool many = rows > (c.head_dim == 64 ? 256 : c.head_dim == 128 ? 128 : 32);
   const int ps = c.page_size;
   const int kmax = 1 << key_shift_max(c.head_dim, many && pair_of(c.head_dim));
   const int vmax = 1 << value_shift_max(c.head_dim);
@@ -1625,10 +1628,13 @@ dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const 
   p.ml = reinterpret_cast<float2*>(a->ws + a->L.ml);
   p.rec = reinterpret_cast<JoinRec*>(a->ws + a->L.rec);
   p.status = reinterpret_cast<DevStatus*>(a->ws + a->L.status);
+  // Many: teams of two clusters when there are that many tiles (head size 256,
+  // us teams of two CTAs / four: 111 / 165 at 256 rows, 194 / 174 at 512).
   const int wide = c.head_dim == 256 ? kRows : 2 * kRows;
   p.team = !many ? 1 : (rows > 2 * wide ? 4 : 2);
   // Ending one item and beginning the next, in key tiles: results to write, and
-  // a pipeline to fill again.
+  // a pipeline to fill again (8 canvases at 0, 4, 6, 8: 115, 109, 107, 108 us;
+  // the other two barely move).
   p.over = !many ? 1 : (c.head_dim == 256 ? 6 : 2);
   const int ctas = a->ctas / p.team * p.team;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
