@@ -51,7 +51,6 @@
 //     between two products, 605-622 us (1.55-1.6 PFLOP/s);
 //   one token over 777, head size 64: latency, 9.6 us with the join.
 #include <math.h>
-#include <stdio.h>
 
 #include <new>
 
