@@ -27,12 +27,11 @@
 //
 // Query tiles of one sequence read the same keys.  `team` CTAs take as many
 // neighbouring tiles through the same key tiles at the same time, so that the
-// keys come from memory once, and the two CTAs of a cluster (a team is made of
-// whole clusters) share them: each loads half of a stage and multicasts it to
-// both, and a stage is free once both have read it.  At head size 256, where a
-// ring of whole tiles would be too shallow, the two are a pair with one
-// tcgen05.mma of 256 rows: each holds its own rows and half of every key and
-// value tile, and the first one issues for both.
+// keys come from memory once and from the L2 after that; each CTA copies its
+// own stages.  At head size 256, where a ring of whole tiles would be too
+// shallow, two CTAs are a pair with one tcgen05.mma of 256 rows: each holds its
+// own rows and half of every key and value tile, and the first one issues for
+// both (a team is made of whole pairs).
 //
 // Warps 0-3 and 4-7: softmax; 8 and 10: TMA producers of keys and values; 9: MMA
 // issuer and TMEM owner.
@@ -48,7 +47,7 @@
 //   8 canvases of 256 over 20k, head size 256: the tensor core at the power
 //     limit and the ends of items, 107-121 us (1.3-1.45 PFLOP/s);
 //   4096 tokens behind 12288, head size 128: the same and the exponentials
-//     between two products, 605-622 us (1.55-1.6 PFLOP/s);
+//     between two products, 621-629 us (1.53-1.55 PFLOP/s);
 //   one token over 777, head size 64: latency, 9.6 us with the join.
 #include <math.h>
 
@@ -244,38 +243,13 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* ba
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
-// CL > 1: into the same place of every CTA of the cluster, counted on each
-// one's barrier.
-template <int CL>
 __device__ __forceinline__ void tma_load_4d(const CUtensorMap* map, uint64_t* bar, uint32_t dst,
                                             int c0, int c1, int c2, int c3) {
-  if constexpr (CL > 1)
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        ".multicast::cluster [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2),
-        "r"(c3), "h"((uint16_t)((1 << CL) - 1))
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2),
-        "r"(c3)
-        : "memory");
-}
-
-// umma_commit on the barrier of every CTA of the cluster.
-template <int CL>
-__device__ __forceinline__ void commit_cluster(uint64_t* bar) {
-  if constexpr (CL > 1)
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%0], %1;" ::"r"(smem_u32(bar)),
-        "h"((uint16_t)((1 << CL) - 1))
-        : "memory");
-  else
-    umma_commit(bar);
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
 }
 
 // Pair of CTAs: a box into this CTA, counted on the first CTA's barrier (`bar`
@@ -452,12 +426,6 @@ __device__ __forceinline__ void commit_own(uint64_t* bar) {
   else
     umma_commit(bar);
 }
-// A stage is free: to every CTA that fills it.
-template <bool PAIR, int CL>
-__device__ __forceinline__ void commit_stage(uint64_t* bar) {
-  if constexpr (PAIR) commit_own<true>(bar);
-  else commit_cluster<CL>(bar);
-}
 
 template <bool FP16>
 __device__ __forceinline__ constexpr uint32_t idesc_16(int M, int N, bool b_nmajor) {
@@ -629,12 +597,10 @@ __device__ __forceinline__ void find_start(const AttnParams& p, long long* cost,
   __syncthreads();
 }
 
-template <int D, int NQ, int CL, bool PAIR, bool FP16>
+template <int D, int NQ, bool PAIR, bool FP16>
 __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constant__ AttnParams p) {
-  static_assert(!PAIR || CL == 2, "a pair is a cluster of two");
   using C = Cfg<D, NQ, PAIR>;
   constexpr int NS = C::kStages, PARTS = C::kParts, SH = C::kShare;
-  constexpr int MC = PAIR ? 1 : CL;             // CTAs that a copy goes to
   constexpr int KROWS = kKeys / SH;             // keys of a tile in this CTA
   constexpr int NC = NQ == 2 ? 128 : 64;        // score columns a softmax thread
   constexpr int OC = NQ == 2 ? D : D / 2;       // output columns a softmax thread
@@ -662,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], MC);
+      mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < C::kQBufs; ++i) {
       mbar_init(&q_full[i], 1);
@@ -705,13 +671,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   tc_fence_before();
   find_start<NQ>(p, reinterpret_cast<long long*>(smem), &start);
   tc_fence_after();
-  if (CL > 1) {  // a neighbour's copies and arrivals need the barriers, and the ring to be free
+  if (PAIR) {  // the other CTA's copies and arrivals need the ring to be free
     __syncwarp();
     cluster_arrive();
     cluster_wait();
   }
   const uint32_t tmem = tmem_holder;
-  const int rank = CL > 1 ? blockIdx.x % CL : 0;
+  const int rank = PAIR ? blockIdx.x % 2 : 0;
   Walk<NQ> w;
   w.h = start.h;
   w.b = start.b;
@@ -729,9 +695,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     if (warp == 8 || warp == 10) {
       // ------------------------------------------------------------ producers
       // Warp 8 fills the key stages (and the query tiles), warp 10 the value
-      // stages.  Uniform loops, one elected lane issues; of the cluster's CTAs
-      // each takes its share of the 64-column chunks (of the pieces at 64), of a
-      // pair's each its own half of the tile.
+      // stages.  Uniform loops, one elected lane issues; of a pair's CTAs each
+      // takes its own half of the tile.
       const bool leader = elect_one(), keys = warp == 8;
       // whether stage h of a value tile holds the last keys seen, in a part of
       // their 16-key step
@@ -829,17 +794,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
                 ids_next = ids_at(base + 32);
               }
               const int id = __shfl_sync(0xffffffffu, ids, x & 31);
-              // the cluster's CTAs share the chunks, or the boxes of one chunk
-              const int c0 = chunks >= MC ? rank % MC : 0, dc = chunks >= MC ? MC : 1;
-              if (leader && (chunks >= MC || x % MC == rank))
+              if (leader)
 #pragma unroll 1
-                for (int c = c0; c < chunks; c += dc) {
+                for (int c = 0; c < chunks; ++c) {
                   const uint32_t dst = ring + st * C::kStageBytes + (c * tokens + r) * 128;
                   const int col = ((keys ? h : rank * (SH - 1)) * chunks + c) * 64;
                   if (PAIR)
                     tma_load_4d_pair(map, bar_addr, dst, col, g.head, (key0 + r) & (ps - 1), id);
                   else
-                    tma_load_4d<MC>(map, bar, dst, col, g.head, (key0 + r) & (ps - 1), id);
+                    tma_load_4d(map, bar, dst, col, g.head, (key0 + r) & (ps - 1), id);
                 }
               __syncwarp();
             }
@@ -862,9 +825,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
           for (int i = max(0, qn - C::kQBufs); i < qn && done; ++i)
             done = wait_drain(&q_full[i % C::kQBufs], (uint32_t)(i / C::kQBufs) & 1u);
         }
-        // Nor may an arrival of the other CTA's products still be on its way to
-        // this one's barriers: it must not meet a CTA that has gone.
-        if (CL > 1) {
+        // Nor may an arrival of the pair's products still be on its way to this
+        // CTA's barriers: it must not meet a CTA that has gone.
+        if (PAIR) {
           for (int i = max(0, pos - NS); i < pos && done; ++i)
             done = wait_drain(&empty[i % NS], (uint32_t)(i / NS) & 1u);
           for (int i = max(0, qn - C::kQBufs); i < qn && done; ++i)
@@ -931,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
               for (int x = 0; x < CH * 4; ++x)
                 umma_ss<PAIR>(d, a + ((x >> 2) * (kRows * 128) + 32 * (x & 3)) / 16,
                         b + ((x >> 2) * (KROWS * 128) + 32 * (x & 3)) / 16, idesc, h | x);
-              if (i == NQ - 1) commit_stage<PAIR, CL>(&empty[c.st]);
+              if (i == NQ - 1) commit_own<PAIR>(&empty[c.st]);
               c.add(1);
             }
             commit_own<PAIR>(&s_full[buf]);
@@ -972,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
                   umma_ts<PAIR>(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc,
                           h + k == 0 ? j != 0 : 1);
                 }
-                if (i == NQ - 1) commit_stage<PAIR, CL>(&empty[c.st]);
+                if (i == NQ - 1) commit_own<PAIR>(&empty[c.st]);
                 c.add(1);
               }
             } else {  // the item's last keys: only their 16-key steps
@@ -991,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
 #pragma unroll 1
                 for (int k = 0; k < SK && h * SK + k < ks; ++k)
                   umma_ts<PAIR>(d, a + 8 * (h * SK + k), b + k * 2048 / 16, idesc, j | h | k);
-                if (i == NQ - 1) commit_stage<PAIR, CL>(&empty[c.st]);
+                if (i == NQ - 1) commit_own<PAIR>(&empty[c.st]);
                 c.add(1);
               }
             }
@@ -1236,7 +1199,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         const int slot = 2 * blockIdx.x + (g.first ? 1 : 0);
         const size_t prow = (size_t)slot * (NQ * kRows) + i * kRows + row;
         // (few rows: the code is fetched again for every item, so it stays short)
-#pragma unroll(CL == 1 ? 1 : OC / 32)
+#pragma unroll(NQ == 1 && !PAIR ? 1 : OC / 32)
         for (int c = 0; c < OC; c += 32) {
           float o[32];
           if (g.n) {
@@ -1315,7 +1278,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     else
       tmem_dealloc(tmem, 512);
   }
-  if (CL > 1) {  // a neighbour's copies and arrivals may still come here
+  if (PAIR) {  // the other CTA's arrivals may still come here
     __syncwarp();
     cluster_arrive();
     cluster_wait();
@@ -1418,14 +1381,14 @@ Layout layout_of(int head_dim) {
 // Head sizes whose many-row variant is a pair of CTAs with shared products.
 constexpr bool pair_of(int d) { return d == 256; }
 
-// The variants of a head size: few rows (one tile, no cluster) and many rows
-// (as wide an item as fits, clusters of two; dg_attn_forward chooses).
+// The variants of a head size: few rows (one tile) and many rows (as wide an
+// item as fits; dg_attn_forward chooses).
 template <int D, bool FP16>
 struct Variant {
   static constexpr int kManyNq = D == 256 ? 1 : 2;
   static constexpr bool kPair = pair_of(D);
-  static constexpr auto few = k_paged_attn<D, 1, 1, false, FP16>;
-  static constexpr auto many = k_paged_attn<D, kManyNq, 2, kPair, FP16>;
+  static constexpr auto few = k_paged_attn<D, 1, false, FP16>;
+  static constexpr auto many = k_paged_attn<D, kManyNq, kPair, FP16>;
   static cudaError_t run(bool m, const AttnParams& p, int ctas, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
@@ -1439,7 +1402,7 @@ struct Variant {
     attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = m ? 2 : 1;
+    cfg.numAttrs = m && kPair ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, m ? many : few, p);
     if (e != cudaSuccess) return e;
     // few rows are split into many parts, many rows into two or three
@@ -1593,11 +1556,11 @@ dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const 
   }
   // Few rows (one tile a CTA) or many, by the average rows of a sequence.  16
   // sequences behind 4000 cached tokens, 4 query heads a key/value head, us few
-  // / many: head size 64: 65 / 90 at 256 rows, 112 / 94 at 512; 128: 65 / 95 at
-  // 128, 103 / 102 at 192, 178 / 115 at 512; 256: 93 / 94 at 32, 101 / 97 at 64,
-  // 198 / 111 at 256.
+  // / many: head size 64: 41 / 48 at 128 rows, 65 / 53 at 192, 112 / 94 at 512;
+  // 128: 65 / 63 at 128, 104 / 69 at 192, 180 / 123 at 512; 256: 93 / 94 at 32,
+  // 101 / 97 at 64, 198 / 111 at 256.
   const int64_t rows = (int64_t)n_tokens * group / batch->n_seqs;
-  const bool many = rows > (c.head_dim == 64 ? 256 : c.head_dim == 128 ? 128 : 32);
+  const bool many = rows > (c.head_dim == 256 ? 32 : 128);
   const int ps = c.page_size;
   const int kmax = 1 << key_shift_max(c.head_dim, many && pair_of(c.head_dim));
   const int vmax = 1 << value_shift_max(c.head_dim);
@@ -1627,10 +1590,19 @@ dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const 
   p.ml = reinterpret_cast<float2*>(a->ws + a->L.ml);
   p.rec = reinterpret_cast<JoinRec*>(a->ws + a->L.rec);
   p.status = reinterpret_cast<DevStatus*>(a->ws + a->L.status);
-  // Many: teams of two clusters when there are that many tiles (head size 256,
-  // us teams of two CTAs / four: 111 / 165 at 256 rows, 194 / 174 at 512).
+  // Many, head size 256: a pair, and teams of two pairs when there are that
+  // many tiles (us teams of two CTAs / four: 111 / 165 at 256 rows, 194 / 174 at
+  // 512).  Up to 128: every CTA by itself, unless a sequence's keys and values
+  // can be past the L2 (129 MB) and its tiles are many: then teams of four read
+  // them from memory once (heads of 128, 4 query heads on each of 8, us by
+  // itself / four: 4096 tokens behind 131072 6350 / 5712, behind 12288 572 / 615;
+  // 12 sequences of 20 to 600 283 / 357).
   const int wide = c.head_dim == 256 ? kRows : 2 * kRows;
-  p.team = !many ? 1 : (rows > 2 * wide ? 4 : 2);
+  const int64_t seq_bytes = (int64_t)batch->max_pages * ps * c.n_kv_heads * c.head_dim * 4;
+  const bool past_l2 = seq_bytes > ((int64_t)256 << 20);
+  if (!many) p.team = 1;
+  else if (c.head_dim == 256) p.team = rows > 2 * wide ? 4 : 2;
+  else p.team = rows > 4 * wide && past_l2 ? 4 : 1;
   // Ending one item and beginning the next, in key tiles: results to write, and
   // a pipeline to fill again (8 canvases at 0, 4, 6, 8: 115, 109, 107, 108 us;
   // the other two barely move).
