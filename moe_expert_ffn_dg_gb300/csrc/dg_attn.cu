@@ -277,16 +277,25 @@ __device__ __forceinline__ uint32_t first_cta(uint64_t* bar) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(bar)));
   return r;
 }
+// What a softmax warp says so to the issuer is that tensor memory has been read
+// or written.  The tcgen05 fences before the arrival and after the wait order
+// that, whatever the semantics of the two, as long as their scope holds both
+// threads: relaxed at cluster scope.  `wrote`: shared memory was written too
+// (cleared values, at the ragged end of an item), which no tcgen05 fence
+// orders: a release at cluster scope, after the writer's proxy fence.
 template <bool PAIR>
-__device__ __forceinline__ void arrive_first(uint64_t* bar) {
-  if constexpr (PAIR)
-    // What it publishes is ordered by the tcgen05 and proxy fences before it; a
-    // cluster-wide release here cost 1700 cycles a key tile.
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(
-                     first_cta(bar))
-                 : "memory");
-  else
+__device__ __forceinline__ void arrive_first(uint64_t* bar, bool wrote = false) {
+  if constexpr (PAIR) {
+    const uint32_t a = first_cta(bar);
+    if (wrote)
+      asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(a)
+                   : "memory");
+    else
+      asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(a)
+                   : "memory");
+  } else {
     mbar_arrive(bar);
+  }
 }
 
 // try_wait that also acquires what the other CTA of a pair released.
@@ -302,6 +311,14 @@ __device__ __forceinline__ bool try_wait_scope(uint64_t* bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
+}
+// mbar_wait on a barrier that a pair's products, copies or other CTA signal.
+// (The phase cannot pass before the second look: the waiter's own next arrival
+// or copy is part of every later one.)
+template <bool PAIR>
+__device__ __forceinline__ bool wait_scope(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (try_wait_scope<PAIR>(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort) && (!PAIR || try_wait_scope<PAIR>(bar, parity));
 }
 
 __device__ __forceinline__ void cluster_arrive() {
@@ -713,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       int pos = 0, qn = 0;
       bool ok = true;
       auto acquire = [&](uint64_t* bar, uint32_t parity) {
-        const bool here = mbar_wait(bar, parity, abort_flag);
+        const bool here = wait_scope<PAIR>(bar, parity, abort_flag);
         ok = __all_sync(0xffffffffu, here);
         return ok;
       };
@@ -861,8 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         uint32_t qph = 0;
         bool ok = true, issued = false;
         auto need = [&](uint64_t* bar, uint32_t parity) {
-          if (try_wait_scope<PAIR>(bar, parity)) return true;
-          ok = mbar_wait(bar, parity, abort_flag) && (!PAIR || try_wait_scope<PAIR>(bar, parity));
+          ok = wait_scope<PAIR>(bar, parity, abort_flag);
           return ok;
         };
         while (ok && w.next(p, g)) {
@@ -1042,7 +1058,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         const int buf = NQ == 2 ? i : ((at + j) & 1);
         const uint32_t use = NQ == 2 ? (uint32_t)(at + j) : (uint32_t)(at + j) >> 1;
         const int key0 = (g.kt0 + j) * kKeys;
-        if (!mbar_wait(&s_full[buf], use & 1u, abort_flag)) ok = false;
+        if (!wait_scope<PAIR>(&s_full[buf], use & 1u, abort_flag)) ok = false;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok && (NQ == 2 || !live)) break;  // a live pair leaves at its barrier
         tc_fence_after();
@@ -1050,7 +1066,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         // that were never written: their V is zeroed up to the 16-key step,
         // so that 0 * V cannot bring in a NaN.
         const int vis = g.khi - key0;
-        if (vis < kKeys && (vis & 15) && i == 0) {
+        const bool clears = vis < kKeys && (vis & 15) && i == 0;
+        if (clears) {
           const int rp = pos + v_stage<PARTS>(j, g.n);
           constexpr int VK = kKeys / PARTS;
           const int h = vis / VK;  // the stage that holds the step
@@ -1060,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             here = mbar_wait(&tail_full[PAIR ? st : 0], (tails >> st) & 1u, abort_flag);
             tails ^= 1u << st;
           } else {
-            here = mbar_wait(&full[st], (uint32_t)((rp + h) / NS) & 1u, abort_flag);
+            here = wait_scope<PAIR>(&full[st], (uint32_t)((rp + h) / NS) & 1u, abort_flag);
           }
           ok = __all_sync(0xffffffffu, here) && ok;
           const int r0 = vis - h * VK, r1 = (r0 + 15) & ~15;
@@ -1121,7 +1138,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
               // O holds the tiles before this one once their product is done.
               // The products before that one are: S of this tile was issued
               // after them, so the barrier is at most one phase behind.
-              bool here = mbar_wait(&pv_done[i], (uint32_t)(at + j - 1) & 1u, abort_flag);
+              bool here = wait_scope<PAIR>(&pv_done[i], (uint32_t)(at + j - 1) & 1u, abort_flag);
               here = __all_sync(0xffffffffu, here);
               if (!here) {
                 ok = false;
@@ -1171,11 +1188,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_first<PAIR>(&p_full[buf]);
+        if (lane == 0) arrive_first<PAIR>(&p_full[buf], clears);
       }
       // ------------------------------------------------- end of the segment
       if (g.n) {
-        if (ok && !mbar_wait(&o_full[i], (uint32_t)segs & 1u, abort_flag)) ok = false;
+        if (ok && !wait_scope<PAIR>(&o_full[i], (uint32_t)segs & 1u, abort_flag)) ok = false;
         ++segs;
         ok = __all_sync(0xffffffffu, ok);
         if (NQ == 2 && !ok) break;

@@ -41,3 +41,24 @@ def test_every_stage_is_the_ctas_own():
         for seed in range(40):
             rng = random.Random(f"own {stages} {seed}")
             protocol.Model("single", 2, 1, stages, 1, protocol.segments(rng), rng).run()
+
+
+def test_signals_between_ctas_have_their_scope():
+    """An arrival at another CTA's barrier without a scope is a release of the
+    CTA's scope, which does not hold the thread that waits for it."""
+    far = [(f, t) for f, t in asm_statements()
+           if re.match(r"\s*mbarrier\.arrive", t) and "shared::cluster" in t]
+    assert far
+    bad = [x for x in far
+           if not re.search(r"mbarrier\.arrive\.(release|relaxed)\.cluster\.shared::cluster", x[1])]
+    assert not bad, bad
+
+
+def test_waits_for_the_other_cta_have_their_scope():
+    """In k_paged_attn the barriers that a pair's products or other CTA signal
+    are waited for at cluster scope; a CTA's own `tail_full` is not among them."""
+    src = open(os.path.join(CSRC, "dg_attn.cu")).read()
+    body = src[src.index("k_paged_attn(const"):src.index("k_attn_join(const")]
+    plain = re.findall(r"\bmbar_(?:try_)?wait\(([^,]*),", body)
+    assert set(plain) == {"&tail_full[PAIR ? st : 0]"}, plain
+    assert len(re.findall(r"\bwait_scope<PAIR>\(", body)) >= 5
