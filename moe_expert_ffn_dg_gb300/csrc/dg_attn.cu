@@ -1347,7 +1347,9 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnP
       m = top;
 #pragma unroll
       for (int k = 0; k < BATCH; ++k)
-        if (ml[k].x != -INFINITY) {  // a part that saw nothing holds nothing
+        // A part that saw nothing holds nothing.  One whose scores are all NaN has
+        // no reference either, but its sum is NaN and makes the row's NaN.
+        if (!(ml[k].y == 0.f)) {
           const float f = exp2f(ml[k].x - m);
           l += f * ml[k].y;
           acc[0] += f * v[k][0].x;

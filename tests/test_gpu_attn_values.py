@@ -1,0 +1,79 @@
+"""Paged attention at values where it can go wrong: non-finite ones at places
+that are seen, in items that one CTA holds whole and in items that several
+share, and weights far below the largest one."""
+
+import math
+
+import pytest
+import torch
+
+from test_gpu_attn import BF, FP, _built, handles, make  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def run(data, left=-1, right=-1):
+    attn, q, batch = handles(data, left, right)
+    lse = torch.zeros(q.shape[:2], device="cuda")
+    out, lse = attn.forward(q, batch, lse=lse)
+    torch.cuda.synchronize()
+    assert attn.device_status()[0] == 0
+    return out.cpu(), lse.cpu()
+
+
+# one key tile (an item cannot be split) and two dozen (one tile a CTA)
+@pytest.mark.parametrize("kv", [100, 3000])
+@pytest.mark.parametrize("d,dtype", [(64, FP), (128, BF), (256, BF)])
+@pytest.mark.parametrize("n", [1, 60])
+def test_a_query_of_nan(n, d, dtype, kv):
+    data = make([n], [kv], 8, 1, d, 64, dtype, 40)
+    good = run(data)
+    data[0][n - 1, 3, 5] = math.nan
+    out, lse = run(data)
+    assert out[n - 1, 3].isnan().all() and lse[n - 1, 3].isnan()
+    rest = torch.ones(n, 8, dtype=torch.bool)
+    rest[n - 1, 3] = False
+    assert torch.equal(out[rest], good[0][rest]) and torch.equal(lse[rest], good[1][rest])
+
+
+@pytest.mark.parametrize("first,count", [(0, 100), (1024, 128), (1000, 300), (2999, 1)])
+@pytest.mark.parametrize("d,n", [(64, 1), (128, 1), (256, 1), (64, 60), (128, 60), (256, 60)])
+def test_keys_of_nan(d, n, first, count):
+    """A run of keys that fills a part, more than one, or less.  Queries whose
+    window ends before or begins after it are not touched."""
+    data = make([n], [3000], 4, 1, d, 64, BF, 41)
+    q, k, v, table, lens, cu = data
+    for left in (-1, 50):
+        good = run(data, left, 0)
+        bad = k.clone()
+        for j in range(first, first + count):
+            bad[int(table[0, j // 64]), j % 64, 0, 7] = math.nan
+        out, lse = run((q, bad, v, table, lens, cu), left, 0)
+        for i in range(n):
+            p = 3000 - n + i
+            sees = first <= p and (left < 0 or first + count > p - left)
+            if sees:
+                assert out[i].isnan().all() and lse[i].isnan().all(), i
+            else:
+                assert torch.equal(out[i], good[0][i]) and torch.equal(lse[i], good[1][i]), i
+
+
+@pytest.mark.parametrize("kv", [100, 3000])
+@pytest.mark.parametrize("n", [1, 60])
+def test_infinite_scores_and_values(n, kv):
+    """A score of +inf makes 0 / 0 of its row's weights; an infinite value
+    reaches its column, with its sign, and nothing else."""
+    data = make([n], [kv], 4, 1, 128, 64, BF, 42)
+    q, k, v, table, lens, cu = data
+    good = run(data)
+    page, row = int(table[0, 77 // 64]), 77 % 64
+    bad = v.clone()
+    bad[page, row, 0, 9] = -math.inf
+    out, lse = run((q, k, bad, table, lens, cu))
+    assert (out[..., 9] == -math.inf).all() and torch.equal(lse, good[1])
+    cols = [c for c in range(128) if c != 9]
+    assert torch.equal(out[..., cols], good[0][..., cols])
+    bad = k.clone()
+    bad[page, row, 0] = math.inf * torch.sign(q[0, 2].float()).to(BF)
+    out, lse = run((q, bad, v, table, lens, cu))
+    assert out[0, 2].isnan().all() and not (lse[0, 2] == -math.inf)
