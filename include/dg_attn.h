@@ -13,7 +13,8 @@
  *
  * Element types: bf16 and fp16 (fp32 too for dg_rope_apply).  All arithmetic
  * is fp32, rounded once on output; attention weights enter the product with V
- * in the element type, their sums stay fp32.
+ * in the element type (fp16: those below 2^-32 of their row's largest as zero),
+ * their sums stay fp32.
  */
 #ifndef DG_ATTN_H
 #define DG_ATTN_H

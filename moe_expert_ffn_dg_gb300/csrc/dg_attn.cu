@@ -15,7 +15,10 @@
 // The reference m of a row is only moved when the true maximum has grown past
 // it by more than 2^8 (P then stays below 2^8, harmless in fp32 sums and in
 // bf16 or fp16): O, which lives in tensor memory, is rescaled a few times a
-// row instead of once a tile.
+// row instead of once a tile.  For fp16 the reference lies 2^7 lower (P below
+// 2^15, of fp16's 2^16): fp16 ends at 2^-25, and a weight that is lost from
+// O but kept in l biases the row (131072 keys of 2^-26 each came out as
+// nothing); so the smallest weight kept is 2^-32 of the largest.
 //
 // The items of a call are cut into units of one key tile (and a few more where
 // an item begins, for what its ends cost: 8 canvases took 115 us without those,
@@ -456,6 +459,10 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// log2 of the largest weight of a row whose reference has just moved.
+template <bool FP16>
+constexpr float kLift = FP16 ? 7.f : 0.f;
 
 template <bool FP16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
@@ -1127,7 +1134,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             mx = fmaxf(mx, x[(wg ^ 1) * 128 + row]);
             ++xn;
           }
-          const float mt = mx * p.scale2;
+          // what the reference would be
+          const float mt = fmaf(mx, p.scale2, -kLift<FP16>);
           // also true of the first key that a row sees (m is -inf before it)
           const bool grown = row_live && mt > m + 8.f;
           if (__any_sync(0xffffffffu, grown)) {

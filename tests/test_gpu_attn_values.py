@@ -77,3 +77,44 @@ def test_infinite_scores_and_values(n, kv):
     bad[page, row, 0] = math.inf * torch.sign(q[0, 2].float()).to(BF)
     out, lse = run((q, bad, v, table, lens, cu))
     assert out[0, 2].isnan().all() and not (lse[0, 2] == -math.inf)
+
+
+@pytest.mark.parametrize("d,n", [(64, 1), (128, 1), (256, 1), (64, 150), (128, 150), (256, 40)])
+def test_one_large_weight_before_a_long_tail(d, n):
+    """fp16: the first key's weight is 2^26 times each other one's, and 131072 of
+    those make up 2^-9 of the sum.  (Many sequences share the pages, so that a
+    CTA runs through most of an item by itself.)
+
+    Tolerance: a weight in fp16 is off by up to 2^-25 absolutely where it is
+    small, which is 2^-32 of the largest weight (it lies at 2^7 or above): 2^-32
+    a key, and half a step of the output (2^-11, relative).  The sums of 131072
+    fp32 terms add 2^-23 a term relative to them (2^-6 of the tail), and scores
+    up to 18 are off by 2^-24 of themselves a rounding: 2^-18 in all."""
+    import moe_expert_ffn_dg_gb300 as pkg
+    keys, seqs, ps = 131072, 160, 256
+    pages = keys // ps
+    i32 = dict(dtype=torch.int32, device="cuda")
+    k = torch.zeros(1, pages, ps, 1, d, dtype=FP, device="cuda")
+    v = torch.ones(1, pages, ps, 1, d, dtype=FP, device="cuda")
+    v[0, 0, 0] = 0
+    scale = d ** -0.5
+    # q k scale log2 e = 26 for the first key, 0 for the others
+    q = torch.zeros(seqs * n, 2, d, dtype=FP, device="cuda")
+    q[..., 1] = 4.0
+    k[0, 0, 0, 0, 1] = 26 * math.log(2) / scale / 4
+    cache = pkg.KvCache(k, v)
+    table = torch.arange(pages, **i32).expand(seqs, pages).contiguous()
+    batch = pkg.KvBatch(table, torch.full((seqs,), keys, **i32),
+                        torch.arange(seqs + 1, **i32) * n)
+    attn = pkg.PagedAttention(cache, 2, right=-1)
+    lse = torch.zeros(seqs * n, 2, device="cuda")
+    out, lse = attn.forward(q, batch, lse=lse)
+    torch.cuda.synchronize()
+    assert attn.device_status()[0] == 0
+    top = 4.0 * float(k[0, 0, 0, 0, 1]) * scale
+    tail = (keys - 1) * math.exp(-top)
+    want = tail / (1 + tail)
+    tol = 2.0 ** -11 * want + keys * 2.0 ** -32 + want * (2.0 ** -6 + 2.0 ** -18)
+    err = (out.double() - want).abs().max()
+    assert err <= tol, (float(err), tol, want)
+    assert (lse.double() - (top + math.log1p(tail))).abs().max() <= 2.0 ** -18 * (1 + top)
