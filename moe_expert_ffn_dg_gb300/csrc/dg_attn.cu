@@ -71,7 +71,9 @@ namespace {
 constexpr int kMaxCtas = 160;
 constexpr int kThreads = 384;  // 12 warps: registers are dealt by warpgroup
 // Registers a thread: 384 x 168 at launch; the producer and MMA warpgroup
-// gives up what the two softmax warpgroups take (2 x 224 + 56 = 3 x 168).
+// gives up what the two softmax warpgroups take (2 x 200 + 104 = 3 x 168).
+// The compiler reports spills all the same: 200 bytes a thread with two tiles
+// at head size 64, 188 at 128, 32 for the pair, 12 for few rows.
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 constexpr int kRows = 128;  // rows of a query tile
 constexpr int kKeys = 128;  // keys of a key tile

@@ -129,3 +129,13 @@ def test_the_models_constants_are_the_kernels():
                 for j in range(n):
                     want = getattr(protocol, fn)(parts, *([j] if args == "j" else [j, n]))
                     assert eval(py(text), {}, {"PARTS": parts, "j": j, "n": n}) == want
+
+
+def test_registers_are_dealt_within_the_launch():
+    """setmaxnreg draws on what the block was launched with: the three
+    warpgroups' shares add up to it, as the comment beside them says."""
+    src = open(os.path.join(CSRC, "dg_attn.cu")).read()
+    soft, other = map(int, re.search(r"kRegsSoftmax = (\d+), kRegsOther = (\d+)", src).groups())
+    launch = 65536 // 384 // 8 * 8
+    assert 2 * soft + other <= 3 * launch and soft % 8 == other % 8 == 0
+    assert f"2 x {soft} + {other} = 3 x {launch}" in src
