@@ -100,10 +100,12 @@ class Rope(_Handle):
         positions (int32 [tokens]); grad=True: the transposed rotation, which
         takes a gradient of the output to the gradient of the input.  out may
         be x."""
+        if not x.is_cuda or x.dtype not in _DTYPES:
+            raise ValueError("x: bf16, fp16 or fp32 on a GPU")
         if out is None:
             out = _new(x, stream)
-        if x.dtype not in _DTYPES or out.shape != x.shape:
-            raise ValueError("x: bf16, fp16 or fp32, out of the same shape")
+        elif out.shape != x.shape:
+            raise ValueError("out: of x's shape")
         B.dg_rope_apply(self.handle, _DTYPES[x.dtype],
                         _heads(x, x.dtype, x.device, self.head_dim, "x"),
                         _heads(out, x.dtype, x.device, self.head_dim, "out"),
@@ -143,8 +145,8 @@ class KvCache(_Handle):
                 k_pages.dtype != v_pages.dtype or k_pages.device != v_pages.device:
             raise ValueError("pools: two [layers, pages, page_size, kv_heads, head_dim] tensors "
                              "of one type on one device")
-        if k_pages.stride(4) != 1 or v_pages.stride(4) != 1:
-            raise ValueError("pools: last dimension contiguous")
+        if not k_pages.is_cuda or k_pages.stride(4) != 1 or v_pages.stride(4) != 1:
+            raise ValueError("pools: on a GPU, last dimension contiguous")
         self.k_pages, self.v_pages = k_pages, v_pages
         self.dtype, self.device = k_pages.dtype, k_pages.device
         (self.n_layers, self.n_pages, self.page_size, self.n_kv_heads,
@@ -230,6 +232,8 @@ class KvPager:
 
     def __init__(self, n_pages: int, page_size: int, device="cuda"):
         self.n_pages, self.page_size = n_pages, page_size
+        if torch.device(device).type != "cuda":
+            raise ValueError(f"pager on a GPU expected, not on {device}")
         self._bytes = B.dg_kv_fork_workspace_size(n_pages)
         # 4-byte elements: aligned as any allocation is
         self.workspace = torch.zeros((self._bytes + 3) // 4, dtype=torch.int32, device=device)
