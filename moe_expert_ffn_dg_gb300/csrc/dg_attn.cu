@@ -1497,11 +1497,13 @@ struct dg_attn {
 namespace dg {
 namespace host {
 dg_status_t read_status(void* word, dg_stream_t stream, unsigned int* where, unsigned int* info) {
-  if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return DG_ERR_CUDA;
+  // all on the caller's stream: it need not be ordered with the default one
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   DevStatus st;
-  if (cudaMemcpy(&st, word, sizeof(st), cudaMemcpyDeviceToHost) != cudaSuccess) return DG_ERR_CUDA;
-  if (cudaMemset(word, 0, sizeof(st)) != cudaSuccess) return DG_ERR_CUDA;
+  if (cudaMemcpyAsync(&st, word, sizeof(st), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaMemsetAsync(word, 0, sizeof(st), s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return DG_ERR_CUDA;
   if (where) *where = st.where;
   if (info) *info = st.info0;
   if (st.code == kDevTimeout) return DG_ERR_TIMEOUT;
