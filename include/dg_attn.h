@@ -129,7 +129,9 @@ typedef struct {
 typedef struct dg_kv dg_kv_t;
 
 /* status: 256 bytes of device memory, 16-byte aligned, for the device status
- * word; cleared here with one blocking memset. */
+ * word; cleared here, through the default stream, before this returns.  No work
+ * in flight may still use that memory (the same holds for the workspace of
+ * dg_attn_create). */
 dg_status_t dg_kv_create(const dg_kv_config_t* cfg, void* status, dg_kv_t** out);
 dg_status_t dg_kv_destroy(dg_kv_t* kv);
 

@@ -27,6 +27,15 @@ def _stream(device, stream=None) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _settle(device) -> None:
+    """Before the library clears memory of a new handle, which it does through
+    the default stream: on a side stream the allocator hands out memory that
+    work queued there may still use."""
+    s = torch.cuda.current_stream(device)
+    if s.cuda_stream:
+        s.synchronize()
+
+
 def _new(like: torch.Tensor, stream=None) -> torch.Tensor:
     """A contiguous tensor of the same shape for a call on `stream`."""
     out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
@@ -155,6 +164,7 @@ class KvCache(_Handle):
         pools = [B.dg_kv_pool_t(t.data_ptr(), *t.stride()[:4]) for t in (k_pages, v_pages)]
         self.cfg = B.dg_kv_config_t(self.n_layers, self.n_pages, self.page_size, self.n_kv_heads,
                                     self.head_dim, _DTYPES.get(self.dtype, -1), *pools, 0)
+        _settle(self.device)
         self.handle = B.dg_kv_create(self.cfg, self._status.data_ptr())
 
     def append(self, k: torch.Tensor, v: torch.Tensor, batch: KvBatch, layer: int = 0,
@@ -238,6 +248,8 @@ class KvPager:
         # 4-byte elements: aligned as any allocation is
         self.workspace = torch.zeros((self._bytes + 3) // 4, dtype=torch.int32, device=device)
         self.device, self._ws = self.workspace.device, self.workspace.data_ptr()
+        # zeroed before any stream uses it
+        torch.cuda.current_stream(self.device).synchronize()
 
     def fork(self, table: torch.Tensor, lens: torch.Tensor, ref: torch.Tensor,
              parent: torch.Tensor, grow: torch.Tensor, out: KvFork = None,
@@ -291,6 +303,7 @@ class PagedAttention(_Handle):
         n = B.dg_attn_workspace_size(self.cfg, cache.handle)
         self.workspace = torch.empty(n + 1024, dtype=torch.uint8, device=cache.device)
         ptr = (self.workspace.data_ptr() + 1023) // 1024 * 1024
+        _settle(cache.device)
         self.handle = B.dg_attn_create(self.cfg, cache.handle, ptr, n)
 
     def forward(self, q: torch.Tensor, batch: KvBatch, layer: int = 0, out: torch.Tensor = None,

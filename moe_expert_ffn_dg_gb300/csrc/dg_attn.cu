@@ -1496,6 +1496,10 @@ struct dg_attn {
 
 namespace dg {
 namespace host {
+bool clear_status(void* word, size_t bytes) {
+  return cudaMemset(word, 0, bytes) == cudaSuccess && cudaStreamSynchronize(nullptr) == cudaSuccess;
+}
+
 dg_status_t read_status(void* word, dg_stream_t stream, unsigned int* where, unsigned int* info) {
   // all on the caller's stream: it need not be ordered with the default one
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -1538,7 +1542,7 @@ dg_status_t dg_attn_create(const dg_attn_config_t* cfg, const dg_kv_t* kv, void*
   const cudaError_t e = kv->cfg.dtype == DG_T_FP16 ? prepare_dim<true>(kv->cfg.head_dim)
                                                    : prepare_dim<false>(kv->cfg.head_dim);
   if (e != cudaSuccess) return DG_ERR_CUDA;
-  if (cudaMemset(static_cast<uint8_t*>(workspace) + L.status, 0, sizeof(DevStatus)) != cudaSuccess)
+  if (!clear_status(static_cast<uint8_t*>(workspace) + L.status, sizeof(DevStatus)))
     return DG_ERR_CUDA;
   dg_attn* a = new (std::nothrow) dg_attn();
   if (!a) return DG_ERR_CUDA;

@@ -57,6 +57,10 @@ inline int log2_of(int x) {
   return s;
 }
 
+// Clear the status word of a new handle: through the default stream, done when
+// this returns, whatever stream the handle's first call runs on.
+bool clear_status(void* word, size_t bytes);
+
 // Synchronise, read and clear a device status word.
 dg_status_t read_status(void* word, dg_stream_t stream, unsigned int* where, unsigned int* info);
 

@@ -486,7 +486,7 @@ dg_status_t dg_kv_create(const dg_kv_config_t* cfg, void* status, dg_kv_t** out)
   }
   if (!status) return DG_ERR_WORKSPACE;
   if (!aligned(status, 16)) return DG_ERR_WORKSPACE;
-  if (cudaMemset(status, 0, 256) != cudaSuccess) return DG_ERR_CUDA;
+  if (!clear_status(status, 256)) return DG_ERR_CUDA;
   dg_kv* kv = new (std::nothrow) dg_kv();
   if (!kv) return DG_ERR_CUDA;
   kv->cfg = c;

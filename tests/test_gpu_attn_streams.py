@@ -43,3 +43,54 @@ def test_reading_a_status_waits_for_its_stream_alone():
     torch.cuda.synchronize()
     assert cache.device_status()[0] == 0
     del keep
+
+
+def test_a_new_handle_loses_no_report():
+    """The word is clear when the handle is there: not later, behind whatever
+    the default stream has to do."""
+    import moe_expert_ffn_dg_gb300 as pkg
+    from moe_expert_ffn_dg_gb300 import binding as B
+    pools = [torch.zeros(1, 4, 16, 1, 64, dtype=BF, device="cuda") for _ in range(2)]
+    k = torch.zeros(1, 1, 64, dtype=BF, device="cuda")
+    batch = pkg.KvBatch(i32([[9]]), i32([1]), i32([0, 1]))
+    side = torch.cuda.Stream()
+    for _ in range(2):  # every kernel is loaded (which may wait for the GPU)
+        old = pkg.KvCache(*pools)
+        old.append(k, k, batch, stream=side)
+        pkg.PagedAttention(old, 1).forward(k, batch, stream=side)
+        torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    with torch.cuda.stream(side):
+        cache = pkg.KvCache(*pools)
+        attn = pkg.PagedAttention(cache, 1)
+        cache.append(k, k, batch)
+        attn.forward(k, batch)
+    torch.cuda.synchronize()
+    assert cache.device_status(side)[0] == B.DG_ERR_DEVICE_CHECK
+    assert attn.device_status(side)[0] == B.DG_ERR_DEVICE_CHECK
+
+
+@pytest.mark.parametrize("what", ["cache", "attention"])
+def test_a_new_handle_waits_for_the_memory_it_gets(what):
+    """Made on a side stream, its memory may be what an earlier kernel of that
+    stream still reads."""
+    import moe_expert_ffn_dg_gb300 as pkg
+    from moe_expert_ffn_dg_gb300 import binding as B
+    pools = [torch.zeros(1, 4, 16, 1, 64, dtype=BF, device="cuda") for _ in range(2)]
+    cache = pkg.KvCache(*pools)
+    size = 256 if what == "cache" else 1024 + B.dg_attn_workspace_size(
+        B.dg_attn_config_t(1, -1, 0, 0.1, 0), cache.handle)
+    side = torch.cuda.Stream()
+    torch.ones(size, dtype=torch.uint8, device="cuda").sum(dtype=torch.int64)  # loaded
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        x = torch.ones(size, dtype=torch.uint8, device="cuda")
+        torch.cuda._sleep(BUSY)
+        total = x.sum(dtype=torch.int64)
+        where = x.data_ptr()
+        del x
+        new = pkg.KvCache(*pools) if what == "cache" else pkg.PagedAttention(cache, 1)
+        got = (new._status if what == "cache" else new.workspace).data_ptr()
+    torch.cuda.synchronize()
+    assert got == where, "the allocator gave other memory: nothing was tried"
+    assert int(total) == size
