@@ -63,6 +63,24 @@ def _ints(t: torch.Tensor, device, shape: tuple, what: str) -> int:
     return t.data_ptr()
 
 
+class _Memory:
+    """Owner of device memory that its calls use, on whatever stream."""
+
+    def _own(self, memory: torch.Tensor):
+        self._held, self._seen = memory, set()
+
+    def _use(self, stream) -> int:
+        """The stream of a call.  The allocator is told of every stream but the
+        one that the memory was allocated on, so that it gives the memory out
+        again, once this object is dropped, only when the calls there are done."""
+        raw = _stream(self.device, stream)
+        if raw not in self._seen:
+            self._held.record_stream(torch.cuda.current_stream(self.device) if stream is None
+                                     else stream)
+            self._seen.add(raw)
+        return raw
+
+
 class _Handle:
     """Owner of a C handle."""
 
@@ -142,7 +160,7 @@ class KvBatch:
                                  _ints(cu, device, (n + 1,), "cu"), n, page_table.shape[1])
 
 
-class KvCache(_Handle):
+class KvCache(_Handle, _Memory):
     """Paged key/value cache of several layers over the caller's pools
     [n_layers, n_pages, page_size, n_kv_heads, head_dim] (bf16 or fp16, the
     last dimension contiguous)."""
@@ -161,6 +179,7 @@ class KvCache(_Handle):
         (self.n_layers, self.n_pages, self.page_size, self.n_kv_heads,
          self.head_dim) = k_pages.shape
         self._status = torch.zeros(256, dtype=torch.uint8, device=self.device)
+        self._own(self._status)
         pools = [B.dg_kv_pool_t(t.data_ptr(), *t.stride()[:4]) for t in (k_pages, v_pages)]
         self.cfg = B.dg_kv_config_t(self.n_layers, self.n_pages, self.page_size, self.n_kv_heads,
                                     self.head_dim, _DTYPES.get(self.dtype, -1), *pools, 0)
@@ -191,7 +210,7 @@ class KvCache(_Handle):
         B.dg_kv_append(self.handle, layer, rope.handle if rope is not None else None, ck, cv, cq,
                        co, q.shape[1] if q is not None else 0, self._batch(batch),
                        _ints(positions, self.device, (n,), "positions")
-                       if positions is not None else None, n, _stream(self.device, stream))
+                       if positions is not None else None, n, self._use(stream))
         return q_out
 
     def _batch(self, batch: KvBatch):
@@ -203,7 +222,7 @@ class KvCache(_Handle):
         """Copy pages, all layers: copies int32 [n, 3] rows (source page,
         destination page, tokens); rows with a negative source do nothing."""
         B.dg_kv_copy(self.handle, _ints(copies, self.device, (copies.shape[0], 3), "copies"),
-                     copies.shape[0], _stream(self.device, stream))
+                     copies.shape[0], self._use(stream))
 
     def gather(self, src_table: torch.Tensor, dst_table: torch.Tensor, cu: torch.Tensor,
                keep: torch.Tensor, stream=None) -> None:
@@ -217,11 +236,11 @@ class KvCache(_Handle):
                        dst_table.shape[1], dst_table.shape[1],
                        _ints(cu, self.device, (n + 1,), "cu"), n,
                        _ints(keep, self.device, (keep.shape[0],), "keep"), keep.shape[0],
-                       _stream(self.device, stream))
+                       self._use(stream))
 
     def device_status(self, stream=None):
         """(status, where, info) of the device status word; clears it."""
-        return B.dg_kv_last_device_status(self.handle, _stream(self.device, stream))
+        return B.dg_kv_last_device_status(self.handle, self._use(stream))
 
 
 class KvFork:
@@ -235,10 +254,11 @@ class KvFork:
         self.table, self.lens, self.ref, self.copies, self.short = table, lens, ref, copies, short
 
 
-class KvPager:
+class KvPager(_Memory):
     """Bookkeeping of n_pages pages: which sequence holds which, shared ones
     counted.  The state (table, lens, ref) is the caller's; ``fork`` takes it
-    one step further."""
+    one step further.  Calls of one instance share a workspace: they must not
+    overlap."""
 
     def __init__(self, n_pages: int, page_size: int, device="cuda"):
         self.n_pages, self.page_size = n_pages, page_size
@@ -248,6 +268,7 @@ class KvPager:
         # 4-byte elements: aligned as any allocation is
         self.workspace = torch.zeros((self._bytes + 3) // 4, dtype=torch.int32, device=device)
         self.device, self._ws = self.workspace.device, self.workspace.data_ptr()
+        self._own(self.workspace)
         # zeroed before any stream uses it
         torch.cuda.current_stream(self.device).synchronize()
 
@@ -278,15 +299,14 @@ class KvPager:
                        _ints(out.copies, dev, (n_new, 3), "out.copies"),
                        _ints(out.short, dev, (1,), "out.short"))
         f = B.dg_kv_fork_t(self.n_pages, self.page_size, row, n_old, n_new, *inputs, *outputs)
-        B.dg_kv_fork(f, self._ws, self._bytes, _stream(dev, stream))
+        B.dg_kv_fork(f, self._ws, self._bytes, self._use(stream))
         return out
 
     def device_status(self, stream=None):
-        return B.dg_kv_fork_last_device_status(self.workspace.data_ptr(),
-                                               _stream(self.device, stream))
+        return B.dg_kv_fork_last_device_status(self._ws, self._use(stream))
 
 
-class PagedAttention(_Handle):
+class PagedAttention(_Handle, _Memory):
     """Attention of new tokens over a :class:`KvCache`.  A query at position p
     sees the keys p - left .. p + right of its sequence; negative: no limit
     (right=0: causal).  scale defaults to head_dim ** -0.5.  Calls of one
@@ -296,12 +316,13 @@ class PagedAttention(_Handle):
 
     def __init__(self, cache: KvCache, n_q_heads: int, left: int = -1, right: int = 0,
                  scale: float = None):
-        self.cache, self.n_q_heads = cache, n_q_heads
+        self.cache, self.n_q_heads, self.device = cache, n_q_heads, cache.device
         self.cfg = B.dg_attn_config_t(n_q_heads, left, right,
                                       1.0 / math.sqrt(cache.head_dim) if scale is None else scale,
                                       0)
         n = B.dg_attn_workspace_size(self.cfg, cache.handle)
         self.workspace = torch.empty(n + 1024, dtype=torch.uint8, device=cache.device)
+        self._own(self.workspace)
         ptr = (self.workspace.data_ptr() + 1023) // 1024 * 1024
         _settle(cache.device)
         self.handle = B.dg_attn_create(self.cfg, cache.handle, ptr, n)
@@ -323,9 +344,9 @@ class PagedAttention(_Handle):
         B.dg_attn_forward(self.handle, layer, _heads(q, c.dtype, c.device, c.head_dim, "q"),
                           _heads(out, c.dtype, c.device, c.head_dim, "out"),
                           lse.data_ptr() if lse is not None else None, c._batch(batch),
-                          q.shape[0], _stream(c.device, stream))
+                          q.shape[0], self._use(stream))
         return (out, lse) if lse is not None else out
 
     def device_status(self, stream=None):
         """(status, where, info) of the device status word; clears it."""
-        return B.dg_attn_last_device_status(self.handle, _stream(self.cache.device, stream))
+        return B.dg_attn_last_device_status(self.handle, self._use(stream))

@@ -4,7 +4,7 @@ workspaces and results."""
 import pytest
 import torch
 
-from test_gpu_attn import BF, _built  # noqa: F401
+from test_gpu_attn import BF, _built, handles, make  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 BUSY = 200_000_000  # cycles: about 0.1 s
@@ -94,3 +94,59 @@ def test_a_new_handle_waits_for_the_memory_it_gets(what):
     torch.cuda.synchronize()
     assert got == where, "the allocator gave other memory: nothing was tried"
     assert int(total) == size
+
+
+def overwritten(size, old):
+    """New memory of the size just given back, filled: must not be the old one
+    while another stream may use it."""
+    new = torch.empty(size, dtype=torch.uint8, device="cuda")
+    new.fill_(255)
+    return new.data_ptr() == old
+
+
+@pytest.mark.parametrize("named", [True, False])
+def test_memory_of_a_dropped_handle_outlives_its_calls(named):
+    """A handle that is dropped while a call runs on another stream: its memory
+    is not given out again before that call is done."""
+    import moe_expert_ffn_dg_gb300 as pkg
+    attn, q, batch = handles(make([2], [9000], 2, 1, 64, 64, BF, 60))
+    cache, pager = attn.cache, pkg.KvPager(1 << 16, 16)
+    table, lens, ref = i32([[0, 1, -1, -1]]), i32([20]), i32([1, 1] + [0] * ((1 << 16) - 2))
+    parent, grow = i32([0, 0]), i32([30, 1])
+    want = attn.forward(q, batch)
+    step = pager.fork(table, lens, ref, parent, grow)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    sizes = [(attn.workspace.nbytes, attn.workspace.data_ptr()),
+             (pager.workspace.nbytes, pager.workspace.data_ptr())]
+    out = torch.zeros_like(q)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+        if not named:
+            attn.forward(q, batch, out=out)
+            again = pager.fork(table, lens, ref, parent, grow)
+    if named:
+        attn.forward(q, batch, out=out, stream=side)
+        again = pager.fork(table, lens, ref, parent, grow, stream=side)
+    del attn, pager
+    assert not any([overwritten(*s) for s in sizes])
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and cache.device_status()[0] == 0
+    for name in again.__slots__:
+        assert torch.equal(getattr(again, name), getattr(step, name))
+
+
+def test_two_attentions_on_two_streams():
+    """Each has a workspace of its own: calls on two streams may overlap."""
+    import moe_expert_ffn_dg_gb300 as pkg
+    data = [make([2, 90], [9000, 700], 4, 2, 128, 64, BF, 61),
+            make([1, 1, 1], [5000, 3000, 40], 4, 2, 128, 64, BF, 62)]
+    both = [handles(d) for d in data]
+    want = [a.forward(q, b).clone() for a, q, b in both]
+    streams = [torch.cuda.Stream() for _ in both]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        outs = [a.forward(q, b, stream=s) for (a, q, b), s in zip(both, streams)]
+    torch.cuda.synchronize()
+    for got, w, (a, _, _) in zip(outs, want, both):
+        assert torch.equal(got, w) and a.device_status()[0] == 0
