@@ -3,7 +3,8 @@ positions, the paged key/value cache and its page operations, and attention of
 new tokens over the cache.
 
 PyTorch only allocates device memory and supplies the CUDA stream; every step
-runs in the CUDA library through the C ABI (``include/dg_attn.h``).
+runs in the CUDA library through the C ABI (``include/dg_attn.h``).  The cache and
+the attention over it are for serving: autograd records nothing of their calls.
 """
 
 from __future__ import annotations
@@ -126,10 +127,13 @@ class Rope(_Handle):
         """x [tokens, heads, head_dim] (bf16, fp16 or fp32) rotated by
         positions (int32 [tokens]); grad=True: the transposed rotation, which
         takes a gradient of the output to the gradient of the input.  out may
-        be x."""
+        be x.  Autograd records the call if x requires a gradient and no out is
+        given."""
         if not x.is_cuda or x.dtype not in _DTYPES:
             raise ValueError("x: bf16, fp16 or fp32 on a GPU")
         if out is None:
+            if x.requires_grad and torch.is_grad_enabled():
+                return _Rotation.apply(x, self, positions, grad, stream)
             out = _new(x, stream)
         elif out.shape != x.shape:
             raise ValueError("out: of x's shape")
@@ -139,6 +143,22 @@ class Rope(_Handle):
                         _ints(positions, x.device, (x.shape[0],), "positions"), x.shape[0],
                         x.shape[1], int(grad), _stream(x.device, stream))
         return out
+
+
+class _Rotation(torch.autograd.Function):
+    """A rotation that autograd records: its gradient is the transposed one."""
+
+    @staticmethod
+    def forward(ctx, x, rope, positions, grad, stream):
+        ctx.save_for_backward(positions)
+        ctx.rope, ctx.grad = rope, grad
+        return rope.apply(x, positions, grad=grad, stream=stream)
+
+    @staticmethod
+    def backward(ctx, g):
+        if g.stride(2) != 1:  # a broadcast one
+            g = g.contiguous()
+        return ctx.rope.apply(g, *ctx.saved_tensors, grad=not ctx.grad), None, None, None, None
 
 
 class KvBatch:
