@@ -118,3 +118,30 @@ def test_one_large_weight_before_a_long_tail(d, n):
     err = (out.double() - want).abs().max()
     assert err <= tol, (float(err), tol, want)
     assert (lse.double() - (top + math.log1p(tail))).abs().max() <= 2.0 ** -18 * (1 + top)
+
+
+@pytest.mark.parametrize("n", [1, 90])
+def test_tables_with_a_row_stride(n):
+    """Rows of a wider table, and of one whose first columns are another's: an
+    append and an attention as with a table of their own."""
+    import moe_expert_ffn_dg_gb300 as pkg
+    data = make([n, 0, n], [400, 30, 290], 4, 2, 128, 32, BF, 43)
+    attn, q, batch = handles(data)
+    want = attn.forward(q, batch)
+    table = batch.page_table
+    wide = torch.full((3, 2 * table.shape[1] + 5), 10 ** 9, dtype=torch.int32, device="cuda")
+    part = wide[:, 3:3 + table.shape[1]]
+    part.copy_(table)
+    other = pkg.KvBatch(part, batch.lens, batch.cu)
+    assert part.stride(0) != part.shape[1]
+    assert torch.equal(attn.forward(q, other), want)
+    cache = attn.cache
+    kv = torch.randn(2 * n, 4, 128, device="cuda").to(BF)
+    got = []
+    for b in (batch, other):
+        cache.k_pages.zero_(), cache.v_pages.zero_()
+        cache.append(kv[:, :2], kv[:, 2:], b, rope=pkg.Rope(128))
+        got.append((cache.k_pages.clone(), cache.v_pages.clone()))
+    assert got[0][0].any() and torch.equal(got[0][0], got[1][0])
+    assert torch.equal(got[0][1], got[1][1])
+    assert cache.device_status()[0] == 0 and attn.device_status()[0] == 0
