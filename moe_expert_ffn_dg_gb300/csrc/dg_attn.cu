@@ -21,8 +21,8 @@
 // nothing); so the smallest weight kept is 2^-32 of the largest.
 //
 // The items of a call are cut into units of one key tile (and a few more where
-// an item begins, for what its ends cost: 8 canvases took 115 us without those,
-// 107 with), and the units dealt evenly to one CTA an SM: a CTA takes a
+// an item begins, for what its ends cost: 8 canvases take 120 us without those,
+// 111 with), and the units dealt evenly to one CTA an SM: a CTA takes a
 // contiguous range, so long and short sequences, many and few tokens balance
 // alike.  An item that crosses a range boundary leaves fp32 partial results in
 // the workspace, joined in a fixed order by k_attn_join.  (Joined by the last
@@ -48,9 +48,9 @@
 //   64 single tokens over 471k cached ones, head size 128: memory, 279 us
 //     (6.9 TB/s; 317 us at page size 16, whose copies are 2 KB);
 //   8 canvases of 256 over 20k, head size 256: the tensor core at the power
-//     limit and the ends of items, 107-121 us (1.3-1.45 PFLOP/s);
+//     limit and the ends of items, 111-122 us (1.28-1.4 PFLOP/s);
 //   4096 tokens behind 12288, head size 128: the same and the exponentials
-//     between two products, 621-629 us (1.53-1.55 PFLOP/s);
+//     between two products, 610-629 us (1.53-1.58 PFLOP/s);
 //   one token over 777, head size 64: latency, 9.6 us with the join.
 #include <math.h>
 
@@ -1592,8 +1592,8 @@ dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const 
   // Few rows (one tile a CTA) or many, by the average rows of a sequence.  16
   // sequences behind 4000 cached tokens, 4 query heads a key/value head, us few
   // / many: head size 64: 41 / 48 at 128 rows, 65 / 53 at 192, 112 / 94 at 512;
-  // 128: 65 / 63 at 128, 104 / 69 at 192, 180 / 123 at 512; 256: 93 / 94 at 32,
-  // 101 / 97 at 64, 198 / 111 at 256.
+  // 128: 65 / 63 at 128, 104 / 69 at 192, 180 / 123 at 512; 256: 93 / 95 at 32,
+  // 102 / 99 at 64, 199 / 113 at 256.
   const int64_t rows = (int64_t)n_tokens * group / batch->n_seqs;
   const bool many = rows > (c.head_dim == 256 ? 32 : 128);
   const int ps = c.page_size;
@@ -1626,7 +1626,7 @@ dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const 
   p.rec = reinterpret_cast<JoinRec*>(a->ws + a->L.rec);
   p.status = reinterpret_cast<DevStatus*>(a->ws + a->L.status);
   // Many, head size 256: a pair, and teams of two pairs when there are that
-  // many tiles (us teams of two CTAs / four: 111 / 165 at 256 rows, 194 / 174 at
+  // many tiles (us teams of two CTAs / four: 113 / 174 at 256 rows, 202 / 181 at
   // 512).  Up to 128: every CTA by itself, unless a sequence's keys and values
   // can be past the L2 (129 MB) and its tiles are many: then teams of four read
   // them from memory once (heads of 128, 4 query heads on each of 8, us by
@@ -1639,8 +1639,8 @@ dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const 
   else if (c.head_dim == 256) p.team = rows > 2 * wide ? 4 : 2;
   else p.team = rows > 4 * wide && past_l2 ? 4 : 1;
   // Ending one item and beginning the next, in key tiles: results to write, and
-  // a pipeline to fill again (8 canvases at 0, 4, 6, 8: 115, 109, 107, 108 us;
-  // the other two barely move).
+  // a pipeline to fill again (8 canvases at 0, 2, 4, 6, 8: 120, 117, 114, 111,
+  // 110 us; the other two barely move).
   p.over = !many ? 1 : (c.head_dim == 256 ? 6 : 2);
   const int ctas = a->ctas / p.team * p.team;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
