@@ -168,7 +168,8 @@ dg_status_t dg_moe_workspace_size(const dg_moe_config_t* cfg, size_t* bytes);
  * memory of at least dg_moe_workspace_size() bytes, 1024-byte aligned,
  * used only by this handle, or shared by handles of one shape whose
  * forwards run one after another on one stream (a layer stack).  Allocates no device memory and launches no
- * kernel; clears the workspace's status word with one blocking memset.
+ * kernel; clears the workspace's status word through the default stream before
+ * it returns (no work in flight may still use that memory).
  * Validation errors are returned before any CUDA call.  On error *out is
  * set to NULL. */
 dg_status_t dg_moe_create(const dg_moe_config_t* cfg, const dg_moe_weights_t* weights,

@@ -14,6 +14,7 @@ import math
 import torch
 
 from . import binding as B
+from .block import _settle
 
 _DTYPES = {torch.bfloat16: B.DG_T_BF16, torch.float16: B.DG_T_FP16, torch.float32: B.DG_T_FP32}
 _LAYOUTS = {"half": B.DG_ROPE_HALF, "interleaved": B.DG_ROPE_INTERLEAVED}
@@ -26,15 +27,6 @@ def _stream(device, stream=None) -> int:
         return stream.cuda_stream
     # the handle alone: torch.cuda.current_stream() builds an object around it
     return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _settle(device) -> None:
-    """Before the library clears memory of a new handle, which it does through
-    the default stream: on a side stream the allocator hands out memory that
-    work queued there may still use."""
-    s = torch.cuda.current_stream(device)
-    if s.cuda_stream:
-        s.synchronize()
 
 
 def _new(like: torch.Tensor, stream=None) -> torch.Tensor:

@@ -17,6 +17,15 @@ VECTORS = ("router_scale", "per_expert_scale", "w_pre_ff", "w_pre_ff2", "w_post_
            "w_post_ff2", "w_post_ff")
 
 
+def _settle(device) -> None:
+    """Before the library clears memory of a new handle, which it does through
+    the default stream: on a side stream the allocator hands out memory that
+    work queued there may still use."""
+    s = torch.cuda.current_stream(device)
+    if s.cuda_stream:
+        s.synchronize()
+
+
 def _to_device(a: np.ndarray, device) -> torch.Tensor:
     """numpy array -> device tensor with the same bytes (bf16 bits stay bits)."""
     a = np.ascontiguousarray(a)
@@ -113,6 +122,7 @@ class MoEBlock:
             w["w_pre_ff"].data_ptr(), w["w_pre_ff2"].data_ptr(), w["w_post_ff1"].data_ptr(),
             w["w_post_ff2"].data_ptr(), w["w_post_ff"].data_ptr(),
             w["router_bias"].data_ptr() if w.get("router_bias") is not None else None)
+        _settle(self.device)
         self.handle = B.dg_moe_create(self.cfg, self.cw, self._ws_ptr, ws_bytes)
 
     @classmethod
@@ -232,6 +242,7 @@ class ScMlp:
         ptr = (self.workspace.data_ptr() + 1023) // 1024 * 1024
         self.cw = B.dg_sc_mlp_weights_t(_qt(weights["gate"]), _qt(weights["up"]),
                                         _qt(weights["down"]), weights["pre_norm"].data_ptr())
+        _settle(self.device)
         self.handle = B.dg_sc_mlp_create(self.cfg, self.cw, ptr, ws_bytes)
 
     @classmethod

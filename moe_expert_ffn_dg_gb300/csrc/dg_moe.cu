@@ -296,9 +296,10 @@ dg_status_t dg_moe_create(const dg_moe_config_t* cfg, const dg_moe_weights_t* we
     delete m;
     return DG_ERR_CUDA;
   }
-  // the device status word starts clear
+  // the device status word starts clear, whatever stream the first call runs on
   if (cudaMemset(ws + L.status, 0, sizeof(DevStatus)) != cudaSuccess ||
-      cudaMemset(ws + L.zero16, 0, 16) != cudaSuccess) {
+      cudaMemset(ws + L.zero16, 0, 16) != cudaSuccess ||
+      cudaStreamSynchronize(nullptr) != cudaSuccess) {
     delete m;
     return DG_ERR_CUDA;
   }

@@ -278,7 +278,8 @@ dg_status_t dg_sc_mlp_create(const dg_sc_mlp_config_t* cfg, const dg_sc_mlp_weig
   m->dn.xb_exp128 = m->dn.xb_d128;
   m->dn.xb_exp32 = m->dn.xb_d32;
   if (cudaMemset(ws + L.status, 0, sizeof(DevStatus)) != cudaSuccess ||
-      cudaMemset(ws + L.zero, 0, 16) != cudaSuccess) {
+      cudaMemset(ws + L.zero, 0, 16) != cudaSuccess ||
+      cudaStreamSynchronize(nullptr) != cudaSuccess) {
     delete m;
     return DG_ERR_CUDA;
   }
