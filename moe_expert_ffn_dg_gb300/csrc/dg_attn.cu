@@ -26,7 +26,7 @@
 // contiguous range, so long and short sequences, many and few tokens balance
 // alike.  An item that crosses a range boundary leaves fp32 partial results in
 // the workspace, joined in a fixed order by k_attn_join.  (Joined by the last
-// CTA to come instead: 118 us, for the code and registers in the main loop.)
+// CTA to come instead: 6 us more, for the code and registers in the main loop.)
 //
 // Query tiles of one sequence read the same keys.  `team` CTAs take as many
 // neighbouring tiles through the same key tiles at the same time, so that the
