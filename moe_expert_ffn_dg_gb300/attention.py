@@ -14,19 +14,12 @@ import math
 import torch
 
 from . import binding as B
-from .block import _settle
+from .block import _Memory, _settle, _stream
 
 _DTYPES = {torch.bfloat16: B.DG_T_BF16, torch.float16: B.DG_T_FP16, torch.float32: B.DG_T_FP32}
 _LAYOUTS = {"half": B.DG_ROPE_HALF, "interleaved": B.DG_ROPE_INTERLEAVED}
 _SCALINGS = {"none": B.DG_ROPE_PLAIN, "linear": B.DG_ROPE_LINEAR, "base": B.DG_ROPE_BASE,
              "ramp": B.DG_ROPE_RAMP}
-
-
-def _stream(device, stream=None) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    # the handle alone: torch.cuda.current_stream() builds an object around it
-    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _new(like: torch.Tensor, stream=None) -> torch.Tensor:
@@ -54,24 +47,6 @@ def _ints(t: torch.Tensor, device, shape: tuple, what: str) -> int:
     if t.shape != shape:
         raise ValueError(f"{what}: shape {shape} expected, got {tuple(t.shape)}")
     return t.data_ptr()
-
-
-class _Memory:
-    """Owner of device memory that its calls use, on whatever stream."""
-
-    def _own(self, memory: torch.Tensor):
-        self._held, self._seen = memory, set()
-
-    def _use(self, stream) -> int:
-        """The stream of a call.  The allocator is told of every stream but the
-        one that the memory was allocated on, so that it gives the memory out
-        again, once this object is dropped, only when the calls there are done."""
-        raw = _stream(self.device, stream)
-        if raw not in self._seen:
-            self._held.record_stream(torch.cuda.current_stream(self.device) if stream is None
-                                     else stream)
-            self._seen.add(raw)
-        return raw
 
 
 class _Handle:

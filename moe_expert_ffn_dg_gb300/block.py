@@ -26,6 +26,31 @@ def _settle(device) -> None:
         s.synchronize()
 
 
+def _stream(device, stream=None) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle alone: torch.cuda.current_stream() builds an object around it
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+class _Memory:
+    """Owner of device memory that its calls use, on whatever stream."""
+
+    def _own(self, memory: torch.Tensor):
+        self._held, self._seen = memory, set()
+
+    def _use(self, stream) -> int:
+        """The stream of a call.  The allocator is told of every stream but the
+        one that the memory was allocated on, so that it gives the memory out
+        again, once this object is dropped, only when the calls there are done."""
+        raw = _stream(self.device, stream)
+        if raw not in self._seen:
+            self._held.record_stream(torch.cuda.current_stream(self.device) if stream is None
+                                     else stream)
+            self._seen.add(raw)
+        return raw
+
+
 def _to_device(a: np.ndarray, device) -> torch.Tensor:
     """numpy array -> device tensor with the same bytes (bf16 bits stay bits)."""
     a = np.ascontiguousarray(a)
@@ -86,7 +111,7 @@ def _qt(w) -> B.dg_qtensor_t:
     return B.dg_qtensor_t(w.data_ptr(), None, None)
 
 
-class MoEBlock:
+class MoEBlock(_Memory):
     """One layer: device weights (borrowed by the C handle), a workspace and
     the handle.  ``forward`` runs the block on a bf16 [T, H] device tensor."""
 
@@ -111,6 +136,7 @@ class MoEBlock:
         elif workspace.numel() < ws_bytes + 1024 or workspace.device != self.device:
             raise ValueError("shared workspace too small or on another device")
         self.workspace = workspace
+        self._own(workspace)
         base = self.workspace.data_ptr()
         self._ws_ptr = (base + 1023) // 1024 * 1024
         self._ws_bytes = ws_bytes
@@ -142,10 +168,6 @@ class MoEBlock:
                                 expert_fmt, dense_fmt, router_fmt, rms_eps, 0)
         return B.dg_moe_workspace_size(cfg) + 1024
 
-    def _stream(self, stream=None) -> int:
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        return s.cuda_stream
-
     def forward(self, h: torch.Tensor, layer_scalar: float = 1.0, out: torch.Tensor = None,
                 debug: bool = False, stream=None):
         """h: bf16 [T, H] on the device.  Returns out (bf16 [T, H]) and, with
@@ -174,7 +196,7 @@ class MoEBlock:
                 "idx", "w", "logits", "offsets", "perm", "xd", "xe_perm", "y_moe", "y_dense",
                 "n_refined")])
         B.dg_moe_forward(self.handle, h.data_ptr(), out.data_ptr(), T, float(layer_scalar),
-                         self._stream(stream), dbg)
+                         self._use(stream), dbg)
         return (out, tensors) if debug else out
 
     def forward_neighbours(self, x: torch.Tensor, attn_out: torch.Tensor, w_post_attn: torch.Tensor,
@@ -199,7 +221,7 @@ class MoEBlock:
                                    next_in.data_ptr() if w_next_in is not None else None,
                                    h_mid.data_ptr() if h_mid is not None else None)
         B.dg_moe_forward_neighbours(self.handle, x.data_ptr(), nb, out.data_ptr(), T,
-                                    float(layer_scalar), self._stream(stream))
+                                    float(layer_scalar), self._use(stream))
         return out, (next_in if w_next_in is not None else None)
 
     def forward_host(self, h_host: torch.Tensor, out_host: torch.Tensor, layer_scalar: float = 1.0,
@@ -207,11 +229,11 @@ class MoEBlock:
         """End to end from host memory: copy in, forward, copy out, synchronise."""
         assert h_host.device.type == "cpu" and out_host.device.type == "cpu"
         B.dg_moe_forward_host(self.handle, h_host.data_ptr(), out_host.data_ptr(), h_host.shape[0],
-                              float(layer_scalar), self._stream(stream))
+                              float(layer_scalar), self._use(stream))
         return out_host
 
     def device_status(self, stream=None):
-        return B.dg_moe_last_device_status(self.handle, self._stream(stream))
+        return B.dg_moe_last_device_status(self.handle, self._use(stream))
 
     def close(self):
         if getattr(self, "handle", None):
@@ -225,7 +247,7 @@ class MoEBlock:
             pass
 
 
-class ScMlp:
+class ScMlp(_Memory):
     """The self-conditioning MLP (before layer 0 of a decode step): device
     weights (borrowed by the C handle), a workspace and the handle.
     ``forward(embeds, signal)`` returns the bf16 [T, H] result."""
@@ -239,6 +261,7 @@ class ScMlp:
         self.device = weights["pre_norm"].device
         ws_bytes = B.dg_sc_mlp_workspace_size(self.cfg)
         self.workspace = torch.empty(ws_bytes + 1024, dtype=torch.uint8, device=self.device)
+        self._own(self.workspace)
         ptr = (self.workspace.data_ptr() + 1023) // 1024 * 1024
         self.cw = B.dg_sc_mlp_weights_t(_qt(weights["gate"]), _qt(weights["up"]),
                                         _qt(weights["down"]), weights["pre_norm"].data_ptr())
@@ -267,14 +290,12 @@ class ScMlp:
         assert embeds.shape == signal.shape
         if out is None:
             out = torch.empty_like(embeds)
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
         B.dg_sc_mlp_forward(self.handle, embeds.data_ptr(), signal.data_ptr(), out.data_ptr(),
-                            embeds.shape[0], s.cuda_stream)
+                            embeds.shape[0], self._use(stream))
         return out
 
     def device_status(self, stream=None) -> int:
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        return B.dg_sc_mlp_last_device_status(self.handle, s.cuda_stream)
+        return B.dg_sc_mlp_last_device_status(self.handle, self._use(stream))
 
     def close(self):
         if getattr(self, "handle", None):

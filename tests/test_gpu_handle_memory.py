@@ -74,3 +74,24 @@ def test_a_new_handle_is_clear_before_its_first_call(kind):
     assert end.query()
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("kind", ["moe", "sc"])
+def test_memory_of_a_dropped_handle_outlives_its_calls(kind):
+    """A handle that is dropped while a call runs on another stream: its
+    workspace is not given out again before that call is done."""
+    make, run = maker(kind)
+    new = make()
+    want = run(new).clone()
+    size, where = new.workspace.numel(), new.workspace.data_ptr()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+        got = run(new)
+    del new
+    other = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert other.data_ptr() != where
+    other.fill_(255)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
