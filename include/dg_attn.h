@@ -168,6 +168,38 @@ dg_status_t dg_kv_gather(dg_kv_t* kv, const int32_t* src_table, int64_t src_stri
                          const int32_t* cu, int n_seqs, const int32_t* keep, int n_keep,
                          dg_stream_t stream);
 
+/* The tokens that stay when sequences are thinned, in the form that
+ * dg_kv_gather takes.  Of sequence s, n = min(lens[s], budget) tokens stay: all
+ * of them if there are no more, else its first `first` and last `last` tokens
+ * and of those between the budget - first - last with the largest weights,
+ * equal ones in the order of their places (NaN counts as larger than any
+ * number, -0 as 0).  keep: their places, ascending, sequence after sequence
+ * from cu[s] on, -1 behind the last; lens_out: n; weights_out[s]: their weights,
+ * then zeros up to the budget.  Supported: n_seqs * budget up to 2^28. */
+typedef struct {
+  const float* weights; /* [n_seqs, width], row stride in elements */
+  int64_t weights_stride;
+  const int32_t* lens; /* [n_seqs], at most width */
+  int n_seqs, width;
+  int budget, first, last; /* first + last <= budget; one past width is width */
+  int32_t* keep;           /* [n_seqs * budget] */
+  int32_t* cu;             /* [n_seqs + 1] */
+  int32_t* lens_out;       /* [n_seqs] */
+  float* weights_out;      /* [n_seqs, budget]; must not overlap weights */
+  int64_t out_stride;
+} dg_kv_select_t;
+
+dg_status_t dg_kv_select(dg_kv_t* kv, const dg_kv_select_t* s, dg_stream_t stream);
+
+/* What the sequences of a group have in common.  Group g is the sequences
+ * groups[g] .. groups[g + 1] of the batch (groups: int32 [n_groups + 1],
+ * ascending; sequences may lie outside all groups).  prefix[s] (int32
+ * [n_seqs]) is the number of tokens, from the first on, that lie in the same
+ * pages in every sequence of s's group and that each of them had before this
+ * call's new ones; 0 in a group of one and outside the groups. */
+dg_status_t dg_kv_shared(dg_kv_t* kv, const dg_kv_batch_t* batch, const int32_t* groups,
+                         int n_groups, int32_t* prefix, dg_stream_t stream);
+
 /* ------------------------------------------------------------------------
  * Bookkeeping of pages: which sequence holds which page, shared pages counted.
  *
@@ -258,6 +290,34 @@ dg_status_t dg_attn_destroy(dg_attn_t* a);
  * sequence are left alone. */
 dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const dg_heads_t* out,
                             float* lse, const dg_kv_batch_t* batch, int n_tokens,
+                            dg_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention weight that each cached token receives:
+ *
+ *   out[s][j] = decay in[s][j] + sum over query heads h and new tokens i of
+ *               sequence s that see j of exp(scale q_ih k_j - lse_ih)
+ *
+ * for the tokens j < lens[s] of every sequence (j < width: more are a length
+ * out of range, which the status word records), with the handle's scale and
+ * limits.  fresh != 0: in[s][j] of this call's own new tokens counts as 0 and
+ * is not read; 0: it counts as it is (the layers of a step after the first, if
+ * they share the weights).  Nor is anything read where decay is 0.  Other
+ * elements of out are left alone.  lse: fp32 [n_tokens, n_q_heads], as
+ * dg_attn_forward writes it.  Sums are fp32 and do not depend on the order in
+ * which blocks run.  Keys that no token sees may hold anything.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  const float* in; /* [n_seqs, width], row strides in elements */
+  float* out;      /* may be in, with the same stride; else they do not overlap */
+  int64_t in_stride, out_stride;
+  int width;
+  float decay; /* >= 0 */
+  int fresh;
+} dg_attn_weights_t;
+
+dg_status_t dg_attn_weights(dg_attn_t* a, int layer, const dg_heads_t* q, const float* lse,
+                            const dg_attn_weights_t* w, const dg_kv_batch_t* batch, int n_tokens,
                             dg_stream_t stream);
 
 dg_status_t dg_attn_last_device_status(dg_attn_t* a, dg_stream_t stream, unsigned int* where,

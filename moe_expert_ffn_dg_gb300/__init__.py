@@ -20,7 +20,8 @@ def __getattr__(name):
     if name in ("MoEBlock", "ScMlp", "params_to_device"):
         from . import block
         return getattr(block, name)
-    if name in ("Rope", "KvBatch", "KvCache", "KvFork", "KvPager", "PagedAttention"):
+    if name in ("Rope", "KvBatch", "KvCache", "KvFork", "KvKeep", "KvPager", "KvShared",
+                "PagedAttention"):
         from . import attention
         return getattr(attention, name)
     raise AttributeError(name)

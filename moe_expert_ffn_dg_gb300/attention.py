@@ -49,6 +49,15 @@ def _ints(t: torch.Tensor, device, shape: tuple, what: str) -> int:
     return t.data_ptr()
 
 
+def _weights(t: torch.Tensor, device, n: int, what: str):
+    """Pointer and row stride of an fp32 [n, width] tensor with contiguous rows."""
+    if t.dim() != 2 or t.shape[0] != n or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: [n_seqs, width] with contiguous rows")
+    if t.dtype != torch.float32 or t.device != device:
+        raise ValueError(f"{what}: fp32 on {device} expected, got {t.dtype} on {t.device}")
+    return t.data_ptr(), t.stride(0) if n > 1 else t.shape[1]
+
+
 class _Handle:
     """Owner of a C handle."""
 
@@ -147,6 +156,29 @@ class KvBatch:
                                  _ints(cu, device, (n + 1,), "cu"), n, page_table.shape[1])
 
 
+class KvShared:
+    """What the sequences of a batch's groups have in common (of
+    :meth:`KvCache.shared`): prefix int32 [n_seqs], the tokens that lie in the
+    same pages in all of a sequence's group.  It holds for the batch's tensors as
+    they were then."""
+
+    __slots__ = ("batch", "groups", "prefix")
+
+    def __init__(self, batch, groups, prefix):
+        self.batch, self.groups, self.prefix = batch, groups, prefix
+
+
+class KvKeep:
+    """The tokens that stay (of :meth:`KvCache.select`): their places keep
+    [n_seqs * budget] (-1 behind the last), cu [n_seqs + 1] and lens [n_seqs],
+    all int32, and their weights [n_seqs, budget]."""
+
+    __slots__ = ("keep", "cu", "lens", "weights")
+
+    def __init__(self, keep, cu, lens, weights):
+        self.keep, self.cu, self.lens, self.weights = keep, cu, lens, weights
+
+
 class KvCache(_Handle, _Memory):
     """Paged key/value cache of several layers over the caller's pools
     [n_layers, n_pages, page_size, n_kv_heads, head_dim] (bf16 or fp16, the
@@ -224,6 +256,59 @@ class KvCache(_Handle, _Memory):
                        _ints(cu, self.device, (n + 1,), "cu"), n,
                        _ints(keep, self.device, (keep.shape[0],), "keep"), keep.shape[0],
                        self._use(stream))
+
+    def select(self, weights: torch.Tensor, lens: torch.Tensor, budget: int, first: int = 0,
+               last: int = 0, out: KvKeep = None, stream=None) -> KvKeep:
+        """Which tokens of each sequence stay when it is thinned to ``budget``:
+        its first ``first`` and last ``last`` ones and, of the others, those
+        with the largest weights (fp32 [n_seqs, width], of lens int32 [n_seqs]
+        tokens), equal ones in the order of their places; all of them if there
+        are no more.  keep and cu are what :meth:`gather` takes.  out.weights
+        may be wider than the budget: what lies behind stays as it is."""
+        n, dev = lens.shape[0], self.device
+        w, stride = _weights(weights, dev, n, "weights")
+        width = weights.shape[1]
+        most = min(budget, width)
+        if budget < 0 or first < 0 or last < 0 or first + last > budget:
+            raise ValueError("budget: at least first + last, none of them negative")
+        if out is None:
+            new = lens.new_empty
+            out = KvKeep(new(n * most), new(n + 1), new(n), weights.new_empty((n, most)))
+            if stream is not None:  # allocated on the current one
+                for t in (out.keep, out.cu, out.lens, out.weights):
+                    t.record_stream(stream)
+        elif out.weights.dim() != 2 or out.weights.shape[1] < most:
+            raise ValueError(f"out.weights: [n_seqs, {most}] or wider")
+        w_out, out_stride = _weights(out.weights, dev, n, "out.weights")
+        cu = _ints(out.cu, dev, (n + 1,), "out.cu")
+        if n == 0:
+            out.cu.zero_()
+        B.dg_kv_select(self.handle, B.dg_kv_select_t(
+            w, stride, _ints(lens, dev, (n,), "lens"), n, width, budget, first, last,
+            _ints(out.keep, dev, (n * most,), "out.keep"), cu,
+            _ints(out.lens, dev, (n,), "out.lens"), w_out, out_stride), self._use(stream))
+        return out
+
+    def shared(self, batch: KvBatch, groups: torch.Tensor, out: KvShared = None,
+               stream=None) -> KvShared:
+        """What the sequences groups[g] .. groups[g + 1] of the batch (int32
+        [n_groups + 1], ascending) have in common, for every group: the tokens
+        from the first on that lie in the same pages and that all of them had
+        before this call's new ones.  For :meth:`PagedAttention.forward`."""
+        n = batch.lens.shape[0]
+        if out is None:
+            out = KvShared(batch, groups, batch.lens.new_empty(n))
+            if stream is not None:  # allocated on the current one
+                out.prefix.record_stream(stream)
+        else:
+            out.batch, out.groups = batch, groups
+        if groups.shape[0] < 1:
+            raise ValueError("groups: [n_groups + 1]")
+        B.dg_kv_shared(self.handle, self._batch(batch),
+                       _ints(groups, self.device, (groups.shape[0],), "groups"),
+                       groups.shape[0] - 1, _ints(out.prefix, self.device, (n,), "out.prefix"),
+                       self._use(stream))
+        return out
 
     def device_status(self, stream=None):
         """(status, where, info) of the device status word; clears it."""
@@ -333,6 +418,36 @@ class PagedAttention(_Handle, _Memory):
                           lse.data_ptr() if lse is not None else None, c._batch(batch),
                           q.shape[0], self._use(stream))
         return (out, lse) if lse is not None else out
+
+    def weights(self, q: torch.Tensor, lse: torch.Tensor, batch: KvBatch, weights: torch.Tensor,
+                layer: int = 0, decay: float = 1.0, fresh: bool = True, out: torch.Tensor = None,
+                stream=None) -> torch.Tensor:
+        """Attention weight that each cached token receives: out[s, j] = decay *
+        weights[s, j] + the sum over heads and new tokens that see token j of
+        exp(scale q k_j - lse), for every token of the batch's sequences.  lse:
+        what :meth:`forward` gave for these q.  weights: fp32 [n_seqs, width];
+        fresh: those of the call's own new tokens count as 0, whatever they
+        hold (pass False for the layers after a step's first, if they share the
+        weights).  out may be weights (the default)."""
+        c = self.cache
+        if q.dim() != 3 or q.shape[1] != self.n_q_heads:
+            raise ValueError("q: [tokens, n_q_heads, head_dim]")
+        if lse.dtype != torch.float32 or lse.device != c.device or not lse.is_contiguous() \
+                or lse.shape != (q.shape[0], self.n_q_heads):
+            raise ValueError("lse: contiguous fp32 [tokens, n_q_heads]")
+        if out is None:
+            out = weights
+        if out.shape != weights.shape:
+            raise ValueError("out: of weights' shape")
+        n = batch.lens.shape[0]
+        w, w_stride = _weights(weights, c.device, n, "weights")
+        o, o_stride = _weights(out, c.device, n, "out")
+        B.dg_attn_weights(self.handle, layer, _heads(q, c.dtype, c.device, c.head_dim, "q"),
+                          lse.data_ptr(),
+                          B.dg_attn_weights_t(w, o, w_stride, o_stride, weights.shape[1], decay,
+                                              int(fresh)), c._batch(batch), q.shape[0],
+                          self._use(stream))
+        return out
 
     def device_status(self, stream=None):
         """(status, where, info) of the device status word; clears it."""

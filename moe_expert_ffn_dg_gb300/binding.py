@@ -55,9 +55,9 @@ DG_ROPE_RAMP = 3
 EXPORTED_ATTN = (
     "dg_rope_create", "dg_rope_destroy", "dg_rope_apply",
     "dg_kv_create", "dg_kv_destroy", "dg_kv_last_device_status", "dg_kv_append", "dg_kv_copy",
-    "dg_kv_gather", "dg_kv_fork_workspace_size", "dg_kv_fork", "dg_kv_fork_last_device_status",
+    "dg_kv_gather", "dg_kv_select", "dg_kv_shared", "dg_kv_fork_workspace_size", "dg_kv_fork", "dg_kv_fork_last_device_status",
     "dg_attn_workspace_size", "dg_attn_create", "dg_attn_destroy", "dg_attn_forward",
-    "dg_attn_last_device_status",
+    "dg_attn_weights", "dg_attn_last_device_status",
 )
 
 
@@ -143,6 +143,18 @@ class dg_attn_config_t(ctypes.Structure):
                 ("flags", c_uint)]
 
 
+class dg_kv_select_t(ctypes.Structure):
+    _fields_ = [("weights", c_void_p), ("weights_stride", c_int64), ("lens", c_void_p),
+                ("n_seqs", c_int), ("width", c_int), ("budget", c_int), ("first", c_int),
+                ("last", c_int), ("keep", c_void_p), ("cu", c_void_p), ("lens_out", c_void_p),
+                ("weights_out", c_void_p), ("out_stride", c_int64)]
+
+
+class dg_attn_weights_t(ctypes.Structure):
+    _fields_ = [("in", c_void_p), ("out", c_void_p), ("in_stride", c_int64),
+                ("out_stride", c_int64), ("width", c_int), ("decay", c_float), ("fresh", c_int)]
+
+
 class DgError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -207,6 +219,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dg_kv_copy.argtypes = [c_void_p, c_void_p, c_int, c_void_p]
     lib.dg_kv_gather.argtypes = [c_void_p, c_void_p, c_int64, c_int, c_void_p, c_int64, c_int,
                                  c_void_p, c_int, c_void_p, c_int, c_void_p]
+    lib.dg_kv_select.argtypes = [c_void_p, POINTER(dg_kv_select_t), c_void_p]
+    lib.dg_kv_shared.argtypes = [c_void_p, POINTER(dg_kv_batch_t), c_void_p, c_int, c_void_p,
+                                 c_void_p]
     lib.dg_kv_fork_workspace_size.argtypes = [c_int, POINTER(c_size_t)]
     lib.dg_kv_fork.argtypes = [POINTER(dg_kv_fork_t), c_void_p, c_size_t, c_void_p]
     lib.dg_kv_fork_last_device_status.argtypes = status_of
@@ -216,6 +231,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                    POINTER(c_void_p)]
     lib.dg_attn_destroy.argtypes = [c_void_p]
     lib.dg_attn_forward.argtypes = [c_void_p, c_int, heads, heads, c_void_p,
+                                    POINTER(dg_kv_batch_t), c_int, c_void_p]
+    lib.dg_attn_weights.argtypes = [c_void_p, c_int, heads, c_void_p, POINTER(dg_attn_weights_t),
                                     POINTER(dg_kv_batch_t), c_int, c_void_p]
     lib.dg_attn_last_device_status.argtypes = status_of
     for name in EXPORTED_ATTN:
@@ -430,6 +447,16 @@ def dg_kv_gather(handle: int, src_table: int, src_stride: int, src_pages: int, d
            "dg_kv_gather")
 
 
+def dg_kv_select(handle: int, s: dg_kv_select_t, stream: int) -> None:
+    _check(load_library().dg_kv_select(handle, s, stream), "dg_kv_select")
+
+
+def dg_kv_shared(handle: int, batch: dg_kv_batch_t, groups: int, n_groups: int, prefix: int,
+                 stream: int) -> None:
+    _check(load_library().dg_kv_shared(handle, batch, groups, n_groups, prefix, stream),
+           "dg_kv_shared")
+
+
 def dg_kv_fork_workspace_size(n_pages: int) -> int:
     n = c_size_t(0)
     _check(load_library().dg_kv_fork_workspace_size(n_pages, ctypes.byref(n)),
@@ -463,6 +490,12 @@ def dg_attn_forward(handle: int, layer: int, q: dg_heads_t, out: dg_heads_t, lse
                     batch: dg_kv_batch_t, n_tokens: int, stream: int) -> None:
     _check(load_library().dg_attn_forward(handle, layer, q, out, lse, batch, n_tokens, stream),
            "dg_attn_forward")
+
+
+def dg_attn_weights(handle: int, layer: int, q: dg_heads_t, lse: int, w: dg_attn_weights_t,
+                    batch: dg_kv_batch_t, n_tokens: int, stream: int) -> None:
+    _check(load_library().dg_attn_weights(handle, layer, q, lse, w, batch, n_tokens, stream),
+           "dg_attn_weights")
 
 
 def _device_status(fn, handle: int, stream: int):

@@ -59,6 +59,7 @@
 #include <cuda_fp16.h>
 
 #include "../../include/dg_attn.h"
+#include "dg_attn_dev.cuh"
 #include "dg_attn_host.h"
 #include "dg_common.cuh"
 #include "dg_tmem.cuh"
@@ -68,26 +69,17 @@ using namespace dg::host;
 
 namespace {
 
-constexpr int kMaxCtas = 160;
 constexpr int kThreads = 384;  // 12 warps: registers are dealt by warpgroup
 // Registers a thread: 384 x 168 at launch; the producer and MMA warpgroup
 // gives up what the two softmax warpgroups take (2 x 200 + 104 = 3 x 168).
 // The compiler reports spills all the same: 200 bytes a thread with two tiles
 // at head size 64, 188 at 128, 32 for the pair, 12 for few rows.
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;
-constexpr int kRows = 128;  // rows of a query tile
-constexpr int kKeys = 128;  // keys of a key tile
 
 // Sites of the device status word.
 enum : unsigned int {
   kSiteAttnLoad = 32, kSiteAttnMma = 33, kSiteAttnSoftmax = 34, kSiteAttnDrain = 35,
   kSiteAttnPage = 36, kSiteAttnLen = 37,
-};
-
-// An item that several CTAs worked on, written by the CTA that begins it.
-struct JoinRec {
-  int parts;  // 0: none
-  int head, tok0, ntok;
 };
 
 struct AttnParams {
@@ -240,23 +232,6 @@ struct Start {
   int teams;
 };
 
-__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, uint32_t dst,
-                                            int c0, int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_4d(const CUtensorMap* map, uint64_t* bar, uint32_t dst,
-                                            int c0, int c1, int c2, int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
-
 // Pair of CTAs: a box into this CTA, counted on the first CTA's barrier (`bar`
 // is its address in the cluster).
 __device__ __forceinline__ void tma_load_4d_pair(const CUtensorMap* map, uint32_t bar,
@@ -348,71 +323,6 @@ __host__ __device__ constexpr int key_shift_max(int d, bool pair) {
 }
 __host__ __device__ constexpr int value_shift_max(int d) { return d == 128 ? 7 : 6; }
 
-// Two fp32 lanes of one instruction.
-__device__ __forceinline__ uint64_t f2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unf2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(r));
-  return r != 0;
-}
-
-// Shared-memory matrix descriptors with the 128-byte swizzle (8-row x 128-byte
-// atoms, 1024 bytes from one to the next).  The high word is the same for all:
-// stride offset 1024, version 1, swizzle mode 2.  The low word holds the start
-// address and the leading offset, which only N-major operands use (rows of
-// 64 N elements, one row a k: the step from one 64-element column to the next).
-// Shared-memory addresses carry the CTA's rank of a cluster above 18 bits.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr, uint32_t leading) {
-  return ((smem_addr & 0x3FFFFu) >> 4) | ((leading >> 4) << 16);
-}
-
-// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit inputs, fp32 accumulate.  PAIR: one
-// product of two CTAs, each with its own rows of A and D and half of B.
-template <bool PAIR>
-__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
-                                        uint32_t idesc, int accumulate) {
-  if constexpr (PAIR)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
-        : "memory");
-}
 // The same with A in tensor memory.
 template <bool PAIR>
 __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
@@ -449,32 +359,9 @@ __device__ __forceinline__ void commit_own(uint64_t* bar) {
     umma_commit(bar);
 }
 
-template <bool FP16>
-__device__ __forceinline__ constexpr uint32_t idesc_16(int M, int N, bool b_nmajor) {
-  const uint32_t t = FP16 ? 0u : 1u;
-  return (1u << 4) | (t << 7) | (t << 10) | ((b_nmajor ? 1u : 0u) << 16) |
-         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // log2 of the largest weight of a row whose reference has just moved.
 template <bool FP16>
 constexpr float kLift = FP16 ? 7.f : 0.f;
-
-template <bool FP16>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
-  uint32_t r;
-  if (FP16)
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 // Barrier of the two warps that share 32 rows (NQ = 1), with an OR of `stop`.
 __device__ __forceinline__ bool pair_barrier(int id, bool stop) {
@@ -488,16 +375,6 @@ __device__ __forceinline__ bool pair_barrier(int id, bool stop) {
       : "r"((uint32_t)stop), "r"(id)
       : "memory");
   return r != 0;
-}
-
-__device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = globaltimer_ns();
-  while (true) {
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
-  }
 }
 
 // Ring position, inside its segment of n tiles, of the first stage of key
@@ -1388,25 +1265,6 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnP
 
 // ------------------------------------------------------------------ host
 
-struct Layout {
-  size_t status, rec, ml, part, total;
-};
-Layout layout_of(int head_dim) {
-  Layout L;
-  const size_t rows = head_dim == 256 ? kRows : 2 * kRows;
-  size_t at = 0;
-  L.status = at;
-  at += 256;
-  L.rec = at;
-  at = round_up(at + sizeof(JoinRec) * kMaxCtas, 256);
-  L.ml = at;
-  at = round_up(at + 2 * kMaxCtas * rows * sizeof(float2), 256);
-  L.part = at;
-  at += 2 * kMaxCtas * rows * head_dim * sizeof(float);
-  L.total = at;
-  return L;
-}
-
 // Head sizes whose many-row variant is a pair of CTAs with shared products.
 constexpr bool pair_of(int d) { return d == 256; }
 
@@ -1472,27 +1330,7 @@ dg_status_t check_config(const dg_attn_config_t* c, const dg_kv* kv) {
   return DG_OK;
 }
 
-// Pages of one layer as (64-column block, head, token of the page, page).
-bool encode_pages(CUtensorMap* map, const dg_kv_config_t& c, const dg_kv_pool_t& pool, int layer,
-                  uint32_t box_tokens) {
-  const uint16_t* base = static_cast<const uint16_t*>(pool.p) + layer * pool.layer_stride;
-  const uint64_t dims[4] = {(uint64_t)c.head_dim, (uint64_t)c.n_kv_heads, (uint64_t)c.page_size,
-                            (uint64_t)c.n_pages};
-  const uint64_t strides[3] = {(uint64_t)pool.head_stride * 2, (uint64_t)pool.token_stride * 2,
-                               (uint64_t)pool.page_stride * 2};
-  const uint32_t box[4] = {64, 1, box_tokens, 1};
-  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, base, dims, strides, box);
-}
-
 }  // namespace
-
-struct dg_attn {
-  dg_attn_config_t cfg;
-  const dg_kv* kv;
-  uint8_t* ws;
-  Layout L;
-  int ctas;
-};
 
 namespace dg {
 namespace host {
@@ -1541,7 +1379,7 @@ dg_status_t dg_attn_create(const dg_attn_config_t* cfg, const dg_kv_t* kv, void*
     return DG_ERR_CUDA;
   const cudaError_t e = kv->cfg.dtype == DG_T_FP16 ? prepare_dim<true>(kv->cfg.head_dim)
                                                    : prepare_dim<false>(kv->cfg.head_dim);
-  if (e != cudaSuccess) return DG_ERR_CUDA;
+  if (e != cudaSuccess || prepare_weights(kv->cfg.head_dim) != cudaSuccess) return DG_ERR_CUDA;
   if (!clear_status(static_cast<uint8_t*>(workspace) + L.status, sizeof(DevStatus)))
     return DG_ERR_CUDA;
   dg_attn* a = new (std::nothrow) dg_attn();
@@ -1577,18 +1415,8 @@ dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const 
   AttnParams p;
   p.step = kRows / group;
   p.q_box = p.step < n_tokens ? p.step : n_tokens;
-  {
-    // a size-1 dimension's stride is never used, but must be a valid one
-    const uint64_t hs = a->cfg.n_q_heads > 1 ? q->head_stride : c.head_dim;
-    const uint64_t ts = n_tokens > 1 ? q->token_stride : c.head_dim;
-    if (hs == 0 || ts == 0) return DG_ERR_UNSUPPORTED;
-    const uint64_t dims[3] = {(uint64_t)c.head_dim, (uint64_t)a->cfg.n_q_heads,
-                              (uint64_t)n_tokens};
-    const uint64_t strides[2] = {hs * 2, ts * 2};
-    const uint32_t box[3] = {64, (uint32_t)group, (uint32_t)p.q_box};
-    if (!encode_tiled(&p.qm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, q->p, dims, strides, box))
-      return DG_ERR_CUDA;
-  }
+  st = encode_queries(&p.qm, *q, a->cfg.n_q_heads, c.head_dim, n_tokens, group, p.q_box);
+  if (st != DG_OK) return st;
   // Few rows (one tile a CTA) or many, by the average rows of a sequence.  16
   // sequences behind 4000 cached tokens, 4 query heads a key/value head, us few
   // / many: head size 64: 41 / 48 at 128 rows, 65 / 53 at 192, 112 / 94 at 512;

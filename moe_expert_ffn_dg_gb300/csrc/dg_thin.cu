@@ -1,0 +1,432 @@
+// Bookkeeping of forked and thinned sequences (include/dg_attn.h): the pages
+// that the sequences of a group have in common, and the choice of the tokens
+// that stay when a cache is thinned.
+#include "../../include/dg_attn.h"
+#include "dg_attn_host.h"
+#include "dg_common.cuh"
+
+using namespace dg;
+using namespace dg::host;
+
+namespace {
+
+enum : unsigned int { kSiteSharedLen = 56, kSiteSharedGroups = 57, kSiteSelectLen = 58 };
+
+constexpr int kThinThreads = 1024;
+constexpr unsigned kAllLanes = 0xffffffffu;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_ctas() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+// An int of another CTA's shared memory.
+__device__ __forceinline__ int peer_int(const int* p, uint32_t rank) {
+  uint32_t a;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Sums over the block; `warps` holds one entry a warp.  Ends with a barrier.
+__device__ __forceinline__ int block_sum(int v, int* warps) {
+  v = __reduce_add_sync(kAllLanes, v);
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = __reduce_add_sync(kAllLanes, warps[threadIdx.x & 31]);
+  __syncthreads();
+  return v;
+}
+// Sum over the threads before this one, and over all.  Ends with a barrier.
+__device__ __forceinline__ int block_before(int v, int* warps, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kAllLanes, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) warps[warp] = incl;
+  __syncthreads();
+  const int w = warps[lane];
+  const int before = __reduce_add_sync(kAllLanes, lane < warp ? w : 0);
+  *total = __reduce_add_sync(kAllLanes, w);
+  __syncthreads();
+  return before + incl - v;
+}
+
+// ------------------------------------------------------------------ shared
+
+struct SharedParams {
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t *lens, *cu, *groups;
+  int32_t* prefix;
+  int n_seqs, n_groups, page_shift, cap;
+  DevStatus* status;
+};
+
+// prefix = min(page_size * (leading columns in which all rows of the group are
+// equal), fewest tokens that a member had before this call).
+//
+// A block a group.  What is read is little (four bytes a page), so latency
+// bounds it: a warp takes 128 columns of a member against the first one, the
+// columns of all members before the next ones, and none past the nearest
+// difference found.
+__global__ void __launch_bounds__(kThinThreads) k_kv_shared(const __grid_constant__ SharedParams p) {
+  __shared__ int warps[32], least, bad;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_trigger();
+  if (tid == 0) {
+    least = p.cap;
+    bad = 0;
+  }
+  pdl_wait();
+  __syncthreads();
+  // groups that are not ranges of sequences in ascending order share nothing
+  for (int g = tid; g <= p.n_groups; g += kThinThreads) {
+    const int a = __ldg(p.groups + g);
+    const int b = g < p.n_groups ? __ldg(p.groups + g + 1) : p.n_seqs;
+    if (a < 0 || a > b || b > p.n_seqs) bad = 1;
+  }
+  __syncthreads();
+  if (bad) {
+    for (int s = blockIdx.x * kThinThreads + tid; s < p.n_seqs; s += gridDim.x * kThinThreads)
+      p.prefix[s] = 0;
+    if (blockIdx.x == 0 && tid == 0)
+      report(p.status, kDevBounds, kSiteSharedGroups, (unsigned)p.n_groups, (unsigned)p.n_seqs);
+    return;
+  }
+  const int a = __ldg(p.groups + blockIdx.x), b = __ldg(p.groups + blockIdx.x + 1);
+  if (blockIdx.x == 0)
+    for (int s = tid; s < a; s += kThinThreads) p.prefix[s] = 0;
+  if ((int)blockIdx.x == p.n_groups - 1)
+    for (int s = b + tid; s < p.n_seqs; s += kThinThreads) p.prefix[s] = 0;
+  if (b - a < 2) {
+    if (b > a && tid == 0) p.prefix[a] = 0;
+    return;
+  }
+  int past = p.cap;
+  for (int s = a + tid; s < b; s += kThinThreads) {
+    const int kv = __ldg(p.lens + s), n = __ldg(p.cu + s + 1) - __ldg(p.cu + s);
+    if (kv < 0 || kv > p.cap || n < 0 || n > kv)
+      report(p.status, kDevBounds, kSiteSharedLen, (unsigned)s, (unsigned)kv);
+    past = min(past, max(0, min(max(kv, 0), p.cap) - max(n, 0)));
+  }
+  past = __reduce_min_sync(kAllLanes, past);
+  if (lane == 0) atomicMin(&least, past);
+  __syncthreads();
+  past = least;
+  __syncthreads();
+  const int pages = (past + (1 << p.page_shift) - 1) >> p.page_shift;
+  if (tid == 0) least = pages;  // now the first column that differs
+  __syncthreads();
+  constexpr int kCols = 128;
+  const int32_t* first = p.table + a * p.table_stride;
+  const long long tasks = (long long)(b - a - 1) * ((pages + kCols - 1) / kCols);
+  for (long long t = warp; t < tasks; t += kThinThreads / 32) {
+    const int c0 = (int)(t / (b - a - 1)) * kCols, m = (int)(t % (b - a - 1)) + 1;
+    if (c0 >= *(volatile int*)&least) break;  // later tasks lie no further left
+    const int32_t* row = first + m * p.table_stride;
+    int x[kCols / 32], y[kCols / 32], at = pages;
+#pragma unroll
+    for (int k = 0; k < kCols / 32; ++k) {
+      const int c = c0 + lane + 32 * k;
+      x[k] = c < pages ? __ldg(first + c) : 0;
+      y[k] = c < pages ? __ldg(row + c) : 0;
+    }
+#pragma unroll
+    for (int k = kCols / 32 - 1; k >= 0; --k)
+      if (x[k] != y[k]) at = c0 + lane + 32 * k;
+    at = __reduce_min_sync(kAllLanes, at);
+    if (lane == 0 && at < pages) atomicMin(&least, at);
+  }
+  __syncthreads();
+  const int prefix = min((int)min((long long)least << p.page_shift, (long long)past), past);
+  for (int s = a + tid; s < b; s += kThinThreads) p.prefix[s] = prefix;
+}
+
+// ------------------------------------------------------------------ select
+
+struct SelectParams {
+  dg_kv_select_t s;
+  int slice;  // weights of a CTA that are kept in shared memory, 0: none
+  DevStatus* status;
+};
+
+// An unsigned order of the weights: NaN above everything, -0 as 0.
+__device__ __forceinline__ uint32_t order_of(float w) {
+  if (w != w) return 0xffffffffu;
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Digits of the order, from the top: 11, 11 and 10 bits.
+constexpr int kDigits = 3;
+constexpr int kBins = 2048;
+__device__ __forceinline__ int digit_shift(int d) { return d == 0 ? 21 : d == 1 ? 10 : 0; }
+__device__ __forceinline__ int digit_bits(int d) { return d == 2 ? 10 : 11; }
+
+// Kept of a sequence of L tokens, B = budget < L: the first `first`, the last
+// `last`, and the m = B - first - last largest weights of those between, equal
+// ones in the order of their places.  The m-th largest is found digit by digit
+// of its order, a histogram each; what lies above it is kept, and of what
+// equals it as much as is missing, from the front.  Then one pass in the order
+// of the places, each kept token's rank from a running count.
+//
+// A cluster a sequence (one CTA where rows are short): each CTA takes a slice
+// of the row, keeps it in shared memory, and adds up the others' histograms
+// through distributed shared memory.
+template <bool CACHED>
+__global__ void __launch_bounds__(kThinThreads) k_kv_select(const __grid_constant__ SelectParams p) {
+  extern __shared__ float kept[];
+  __shared__ int hist[kBins], warps[32], found[3], counts[2];
+  const dg_kv_select_t& q = p.s;
+  const int tid = threadIdx.x;
+  const int ctas = (int)cluster_ctas(), rank = (int)cluster_rank();
+  const int seq = blockIdx.x / ctas;
+  pdl_trigger();
+  pdl_wait();
+  // kept tokens of the sequences before this one, and of all
+  int before = 0, all = 0;
+  for (int s = tid; s < q.n_seqs; s += kThinThreads) {
+    const int c = min(min(max(__ldg(q.lens + s), 0), q.width), q.budget);
+    all += c;
+    if (s < seq) before += c;
+  }
+  before = block_sum(before, warps);
+  all = block_sum(all, warps);
+  const int raw = __ldg(q.lens + seq);
+  const int L = min(max(raw, 0), q.width), count = min(L, q.budget);
+  if (rank == 0 && tid == 0) {
+    if (raw < 0 || raw > q.width)
+      report(p.status, kDevBounds, kSiteSelectLen, (unsigned)seq, (unsigned)raw);
+    q.cu[seq] = before;
+    q.lens_out[seq] = count;
+    if (seq == q.n_seqs - 1) q.cu[q.n_seqs] = all;
+  }
+  const int64_t room = (int64_t)q.n_seqs * q.budget;
+  for (int64_t i = all + (int64_t)blockIdx.x * kThinThreads + tid; i < room;
+       i += (int64_t)gridDim.x * kThinThreads)
+    q.keep[i] = -1;
+  const float* row = q.weights + seq * q.weights_stride;
+  int32_t* keep = q.keep + before;
+  float* out = q.weights_out + seq * q.out_stride;
+  const int wide = ctas * kThinThreads, at = rank * kThinThreads + tid;
+  for (int i = count + at; i < q.budget; i += wide) out[i] = 0.f;
+  if (L <= q.budget) {  // the same for every CTA of the cluster
+    for (int i = at; i < L; i += wide) {
+      keep[i] = i;
+      out[i] = __ldg(row + i);
+    }
+    return;
+  }
+  for (int i = at; i < q.first; i += wide) {
+    keep[i] = i;
+    out[i] = __ldg(row + i);
+  }
+  for (int i = at; i < q.last; i += wide) {
+    keep[count - q.last + i] = L - q.last + i;
+    out[count - q.last + i] = __ldg(row + L - q.last + i);
+  }
+  int m = q.budget - q.first - q.last;
+  if (m == 0) return;
+  // this CTA's slice of the tokens between
+  const int mid = L - q.first - q.last, each = (mid + ctas - 1) / ctas;
+  const int lo = min(rank * each, mid), n = min(each, mid - lo);
+  const float* src = row + q.first + lo;
+  if (CACHED) {
+#pragma unroll 8
+    for (int i = tid; i < n; i += kThinThreads) kept[i] = __ldg(src + i);
+  }
+  auto weight = [&](int i) { return CACHED ? kept[i] : __ldg(src + i); };
+  uint32_t top = 0;        // the digits found so far
+  int above = 0, equal = 0;  // of this slice: larger than the m-th largest, equal to it
+  for (int d = 0; d < kDigits; ++d) {
+    const int shift = digit_shift(d), bits = digit_bits(d);
+    for (int i = tid; i < kBins; i += kThinThreads) hist[i] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = tid; i < n; i += kThinThreads) {
+      const uint32_t u = order_of(weight(i));
+      if (d == 0 || u >> (shift + bits) == top) atomicAdd(&hist[u >> shift & ((1u << bits) - 1)], 1);
+    }
+    if (ctas > 1) cluster_sync();
+    else __syncthreads();
+    // bins from the largest down, two a thread
+    const int b0 = kBins - 1 - 2 * tid, b1 = b0 - 1;
+    const int own0 = hist[b0], own1 = hist[b1];
+    int all0 = own0, all1 = own1;
+    for (int r = 0; r < ctas; ++r)
+      if (r != rank) {
+        all0 += peer_int(&hist[b0], r);
+        all1 += peer_int(&hist[b1], r);
+      }
+    int total;
+    const int over = block_before(all0 + all1, warps, &total);
+    if (over < m && over + all0 + all1 >= m) {
+      const bool second = over + all0 < m;
+      found[0] = second ? b1 : b0;
+      found[1] = m - over - (second ? all0 : 0);
+    }
+    __syncthreads();
+    const int bin = found[0];
+    m = found[1];
+    // what of this slice lies in the bins above, and in the bin itself
+    const int higher = (b0 > bin ? own0 : 0) + (b1 > bin ? own1 : 0);
+    above += block_sum(higher, warps);
+    equal = hist[bin];
+    top = top << bits | (uint32_t)bin;
+    // no CTA clears its histogram while another one reads it
+    if (ctas > 1) cluster_sync();
+    else __syncthreads();
+  }
+  // tokens kept of the slices before this one
+  int gt = 0, eq = 0;
+  if (ctas > 1) {
+    if (tid == 0) {
+      counts[0] = above;
+      counts[1] = equal;
+    }
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) {
+      gt += peer_int(&counts[0], r);
+      eq += peer_int(&counts[1], r);
+    }
+  }
+  constexpr int kEach = 4;
+  for (int t0 = 0; t0 < n; t0 += kEach * kThinThreads) {
+    const int i0 = t0 + kEach * tid;
+    float w[kEach];
+    int sum = 0;  // larger ones; equal ones in the high half
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      w[k] = i0 + k < n ? weight(i0 + k) : 0.f;
+      const uint32_t u = order_of(w[k]);
+      sum += i0 + k < n ? (u > top ? 1 : u == top ? 1 << 16 : 0) : 0;
+    }
+    int total;
+    const int off = block_before(sum, warps, &total);
+    int g = gt + (off & 0xffff), e = eq + (off >> 16);
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      if (i0 + k >= n) break;
+      const uint32_t u = order_of(w[k]);
+      if (u > top || (u == top && e < m)) {
+        const int to = q.first + g + min(e, m);
+        keep[to] = q.first + lo + i0 + k;
+        out[to] = w[k];
+      }
+      g += u > top;
+      e += u == top;
+    }
+    gt += total & 0xffff;
+    eq += total >> 16;
+  }
+  // another CTA may still read this one's counts
+  if (ctas > 1) cluster_sync();
+}
+
+// Weights that a CTA holds in shared memory at most: two CTAs an SM.
+constexpr int kSliceMost = 24 * 1024;
+
+int select_ctas(int n_seqs, int width, int sms) {
+  int c = 1;
+  while (c < 8 && width > c * 4096 && n_seqs * c < 2 * sms) c *= 2;
+  return c;
+}
+
+}  // namespace
+
+extern "C" {
+
+dg_status_t dg_kv_shared(dg_kv_t* kv, const dg_kv_batch_t* batch, const int32_t* groups,
+                         int n_groups, int32_t* prefix, dg_stream_t stream) {
+  if (!kv || n_groups < 0) return DG_ERR_INVALID_ARG;
+  const dg_status_t st = check_batch(batch, kv->cfg);
+  if (st != DG_OK) return st;
+  if (n_groups > kMaxSeqs) return DG_ERR_UNSUPPORTED;
+  if (batch->n_seqs == 0) return DG_OK;
+  if (!prefix || (n_groups && !groups)) return DG_ERR_INVALID_ARG;
+  if (!aligned(prefix, 4) || !aligned(groups, 4)) return DG_ERR_ALIGNMENT;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (n_groups == 0)
+    return cudaMemsetAsync(prefix, 0, sizeof(int32_t) * batch->n_seqs, s) == cudaSuccess
+               ? DG_OK : DG_ERR_CUDA;
+  SharedParams p;
+  p.table = batch->page_table;
+  p.table_stride = batch->table_stride;
+  p.lens = batch->lens;
+  p.cu = batch->cu;
+  p.groups = groups;
+  p.prefix = prefix;
+  p.n_seqs = batch->n_seqs;
+  p.n_groups = n_groups;
+  p.page_shift = log2_of(kv->cfg.page_size);
+  p.cap = batch->max_pages * kv->cfg.page_size;
+  p.status = static_cast<DevStatus*>(kv->status);
+  return launch_pdl(k_kv_shared, dim3(n_groups), dim3(kThinThreads), 0, s, p) == cudaSuccess
+             ? DG_OK : DG_ERR_CUDA;
+}
+
+dg_status_t dg_kv_select(dg_kv_t* kv, const dg_kv_select_t* q, dg_stream_t stream) {
+  if (!kv || !q || q->n_seqs < 0 || q->width < 0 || q->budget < 0 || q->first < 0 || q->last < 0)
+    return DG_ERR_INVALID_ARG;
+  if (q->n_seqs == 0) return DG_OK;
+  if (q->n_seqs > kMaxSeqs || q->width > kMaxKvTokens) return DG_ERR_UNSUPPORTED;
+  SelectParams p;
+  p.s = *q;
+  if (p.s.budget > p.s.width) p.s.budget = p.s.width;
+  if ((int64_t)q->first + q->last > q->budget) return DG_ERR_INVALID_ARG;
+  if ((int64_t)q->n_seqs * p.s.budget > kMaxKvTokens) return DG_ERR_UNSUPPORTED;
+  if (!q->lens || !q->cu || !q->lens_out) return DG_ERR_INVALID_ARG;
+  if (p.s.budget > 0 && (!q->weights || !q->keep || !q->weights_out)) return DG_ERR_INVALID_ARG;
+  if (q->weights_stride < 0 || q->out_stride < 0 ||
+      (q->n_seqs > 1 && (q->weights_stride < q->width || q->out_stride < p.s.budget)))
+    return DG_ERR_INVALID_ARG;
+  for (const void* x : {(const void*)q->weights, (const void*)q->lens, (const void*)q->keep,
+                        (const void*)q->cu, (const void*)q->lens_out, (const void*)q->weights_out})
+    if (!aligned(x, 4)) return DG_ERR_ALIGNMENT;
+  if (p.s.budget > 0 && q->weights == q->weights_out) return DG_ERR_INVALID_ARG;
+  if (q->lens == q->lens_out || q->lens == q->cu) return DG_ERR_INVALID_ARG;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return DG_ERR_CUDA;
+  const int ctas = select_ctas(q->n_seqs, q->width, sms);
+  const int slice = (q->width + ctas - 1) / ctas;
+  const bool cached = slice <= kSliceMost;
+  p.slice = cached ? slice : 0;
+  p.status = static_cast<DevStatus*>(kv->status);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(q->n_seqs * ctas);
+  cfg.blockDim = dim3(kThinThreads);
+  cfg.dynamicSmemBytes = sizeof(float) * p.slice;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaSuccess;
+  if (cfg.dynamicSmemBytes > 32 * 1024)  // beside 9 KB of static shared memory
+    e = cudaFuncSetAttribute(k_kv_select<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sizeof(float) * kSliceMost);
+  if (e == cudaSuccess)
+    e = cudaLaunchKernelEx(&cfg, cached ? k_kv_select<true> : k_kv_select<false>, p);
+  return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+}
+
+}  // extern "C"
