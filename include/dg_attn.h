@@ -292,6 +292,28 @@ dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const 
                             float* lse, const dg_kv_batch_t* batch, int n_tokens,
                             dg_stream_t stream);
 
+/* The same for sequences of which groups share a prefix (dg_kv_shared):
+ * groups and prefix as it has them, for this batch.  The prefix of a group is
+ * read once for all of its sequences; results are dg_attn_forward's but for
+ * the order of fp32 sums.  Calls with a left limit, or with many rows a
+ * sequence, where nothing is gained, take the sequences one by one.  workspace:
+ * 1024-byte aligned, for n_tokens tokens at least; calls that share it must not
+ * overlap. */
+typedef struct {
+  const int32_t* groups; /* [n_groups + 1] */
+  const int32_t* prefix; /* [n_seqs] */
+  int n_groups;
+  void* workspace;
+  size_t workspace_bytes;
+} dg_attn_shared_t;
+
+dg_status_t dg_attn_shared_workspace_size(const dg_attn_config_t* cfg, const dg_kv_t* kv,
+                                          int n_tokens, size_t* bytes);
+dg_status_t dg_attn_forward_shared(dg_attn_t* a, int layer, const dg_heads_t* q,
+                                   const dg_heads_t* out, float* lse, const dg_kv_batch_t* batch,
+                                   const dg_attn_shared_t* shared, int n_tokens,
+                                   dg_stream_t stream);
+
 /* ------------------------------------------------------------------------
  * Attention weight that each cached token receives:
  *

@@ -381,29 +381,39 @@ class KvPager(_Memory):
 class PagedAttention(_Handle, _Memory):
     """Attention of new tokens over a :class:`KvCache`.  A query at position p
     sees the keys p - left .. p + right of its sequence; negative: no limit
-    (right=0: causal).  scale defaults to head_dim ** -0.5.  Calls of one
-    instance share a workspace: they must not overlap."""
+    (right=0: causal).  scale defaults to head_dim ** -0.5.  shared_tokens: new
+    tokens that a call with shared prefixes may have (0: no such calls).  Calls
+    of one instance share a workspace: they must not overlap."""
 
     _destroy = staticmethod(B.dg_attn_destroy)
 
     def __init__(self, cache: KvCache, n_q_heads: int, left: int = -1, right: int = 0,
-                 scale: float = None):
+                 scale: float = None, shared_tokens: int = 0):
         self.cache, self.n_q_heads, self.device = cache, n_q_heads, cache.device
         self.cfg = B.dg_attn_config_t(n_q_heads, left, right,
                                       1.0 / math.sqrt(cache.head_dim) if scale is None else scale,
                                       0)
         n = B.dg_attn_workspace_size(self.cfg, cache.handle)
+        self.shared_tokens = shared_tokens
+        self._pre_bytes, room = 0, (n + 1023) // 1024 * 1024
+        if shared_tokens:
+            self._pre_bytes = B.dg_attn_shared_workspace_size(self.cfg, cache.handle,
+                                                              shared_tokens)
+            n = room + self._pre_bytes
         self.workspace = torch.empty(n + 1024, dtype=torch.uint8, device=cache.device)
         self._own(self.workspace)
         ptr = (self.workspace.data_ptr() + 1023) // 1024 * 1024
+        self._pre = ptr + room
         _settle(cache.device)
         self.handle = B.dg_attn_create(self.cfg, cache.handle, ptr, n)
 
     def forward(self, q: torch.Tensor, batch: KvBatch, layer: int = 0, out: torch.Tensor = None,
-                lse: torch.Tensor = None, stream=None):
+                lse: torch.Tensor = None, stream=None, shared: KvShared = None):
         """q [tokens, n_q_heads, head_dim] -> out of the same shape.  lse: an
         fp32 [tokens, n_q_heads] tensor that receives log sum exp of each
-        query's scores; (out, lse) is returned then."""
+        query's scores; (out, lse) is returned then.  shared: what groups of the
+        batch's sequences have in common (:meth:`KvCache.shared`), which is read
+        once for all of a group."""
         c = self.cache
         if out is None:
             out = _new(q, stream)
@@ -413,10 +423,22 @@ class PagedAttention(_Handle, _Memory):
                                 or not lse.is_contiguous()
                                 or lse.shape != (q.shape[0], self.n_q_heads)):
             raise ValueError("lse: contiguous fp32 [tokens, n_q_heads]")
-        B.dg_attn_forward(self.handle, layer, _heads(q, c.dtype, c.device, c.head_dim, "q"),
-                          _heads(out, c.dtype, c.device, c.head_dim, "out"),
-                          lse.data_ptr() if lse is not None else None, c._batch(batch),
-                          q.shape[0], self._use(stream))
+        args = (self.handle, layer, _heads(q, c.dtype, c.device, c.head_dim, "q"),
+                _heads(out, c.dtype, c.device, c.head_dim, "out"),
+                lse.data_ptr() if lse is not None else None, c._batch(batch))
+        if shared is None:
+            B.dg_attn_forward(*args, q.shape[0], self._use(stream))
+        else:
+            if shared.batch is not batch:
+                raise ValueError("shared: of another batch")
+            if q.shape[0] > self.shared_tokens:
+                raise ValueError(f"{q.shape[0]} tokens with shared prefixes, room for "
+                                 f"{self.shared_tokens} (shared_tokens)")
+            n = shared.groups.shape[0]
+            B.dg_attn_forward_shared(*args, B.dg_attn_shared_t(
+                _ints(shared.groups, c.device, (n,), "groups"),
+                _ints(shared.prefix, c.device, (batch.lens.shape[0],), "prefix"), n - 1,
+                self._pre, self._pre_bytes), q.shape[0], self._use(stream))
         return (out, lse) if lse is not None else out
 
     def weights(self, q: torch.Tensor, lse: torch.Tensor, batch: KvBatch, weights: torch.Tensor,

@@ -57,7 +57,8 @@ EXPORTED_ATTN = (
     "dg_kv_create", "dg_kv_destroy", "dg_kv_last_device_status", "dg_kv_append", "dg_kv_copy",
     "dg_kv_gather", "dg_kv_select", "dg_kv_shared", "dg_kv_fork_workspace_size", "dg_kv_fork", "dg_kv_fork_last_device_status",
     "dg_attn_workspace_size", "dg_attn_create", "dg_attn_destroy", "dg_attn_forward",
-    "dg_attn_weights", "dg_attn_last_device_status",
+    "dg_attn_shared_workspace_size", "dg_attn_forward_shared", "dg_attn_weights",
+    "dg_attn_last_device_status",
 )
 
 
@@ -150,6 +151,11 @@ class dg_kv_select_t(ctypes.Structure):
                 ("weights_out", c_void_p), ("out_stride", c_int64)]
 
 
+class dg_attn_shared_t(ctypes.Structure):
+    _fields_ = [("groups", c_void_p), ("prefix", c_void_p), ("n_groups", c_int),
+                ("workspace", c_void_p), ("workspace_bytes", c_size_t)]
+
+
 class dg_attn_weights_t(ctypes.Structure):
     _fields_ = [("in", c_void_p), ("out", c_void_p), ("in_stride", c_int64),
                 ("out_stride", c_int64), ("width", c_int), ("decay", c_float), ("fresh", c_int)]
@@ -232,6 +238,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dg_attn_destroy.argtypes = [c_void_p]
     lib.dg_attn_forward.argtypes = [c_void_p, c_int, heads, heads, c_void_p,
                                     POINTER(dg_kv_batch_t), c_int, c_void_p]
+    lib.dg_attn_shared_workspace_size.argtypes = [POINTER(dg_attn_config_t), c_void_p, c_int,
+                                                  POINTER(c_size_t)]
+    lib.dg_attn_forward_shared.argtypes = [c_void_p, c_int, heads, heads, c_void_p,
+                                           POINTER(dg_kv_batch_t), POINTER(dg_attn_shared_t),
+                                           c_int, c_void_p]
     lib.dg_attn_weights.argtypes = [c_void_p, c_int, heads, c_void_p, POINTER(dg_attn_weights_t),
                                     POINTER(dg_kv_batch_t), c_int, c_void_p]
     lib.dg_attn_last_device_status.argtypes = status_of
@@ -490,6 +501,21 @@ def dg_attn_forward(handle: int, layer: int, q: dg_heads_t, out: dg_heads_t, lse
                     batch: dg_kv_batch_t, n_tokens: int, stream: int) -> None:
     _check(load_library().dg_attn_forward(handle, layer, q, out, lse, batch, n_tokens, stream),
            "dg_attn_forward")
+
+
+def dg_attn_shared_workspace_size(cfg: dg_attn_config_t, kv: int, n_tokens: int) -> int:
+    n = c_size_t(0)
+    _check(load_library().dg_attn_shared_workspace_size(ctypes.byref(cfg), kv, n_tokens,
+                                                        ctypes.byref(n)),
+           "dg_attn_shared_workspace_size")
+    return n.value
+
+
+def dg_attn_forward_shared(handle: int, layer: int, q: dg_heads_t, out: dg_heads_t,
+                           lse: int | None, batch: dg_kv_batch_t, shared: dg_attn_shared_t,
+                           n_tokens: int, stream: int) -> None:
+    _check(load_library().dg_attn_forward_shared(handle, layer, q, out, lse, batch, shared,
+                                                 n_tokens, stream), "dg_attn_forward_shared")
 
 
 def dg_attn_weights(handle: int, layer: int, q: dg_heads_t, lse: int, w: dg_attn_weights_t,

@@ -55,6 +55,7 @@
 #include <math.h>
 
 #include <new>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -75,6 +76,9 @@ constexpr int kThreads = 384;  // 12 warps: registers are dealt by warpgroup
 // The compiler reports spills all the same: 200 bytes a thread with two tiles
 // at head size 64, 188 at 128, 32 for the pair, 12 for few rows.
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;
+
+constexpr int kMinShared = 128;  // tokens of a prefix that are taken together
+constexpr int kMaxSharedRows = 128;  // rows of a sequence whose prefix is
 
 // Sites of the device status word.
 enum : unsigned int {
@@ -125,6 +129,7 @@ struct Cfg {
 
 struct Seq {
   int n0, n, kv;
+  int lo;  // its tokens look at keys from here on
 };
 
 __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
@@ -133,13 +138,14 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
   s.n0 = min(max(a, 0), p.n_tokens);
   s.n = max(min(e, p.n_tokens) - s.n0, 0);
   s.kv = min(max(kv, 0), p.cap);
+  s.lo = 0;
   return s;
 }
 
 // Keys [x, y) that the tokens [first, first + n) of a sequence see together.
 __device__ __forceinline__ int2 key_range(const AttnParams& p, const Seq& s, int first, int n) {
   const int pos = s.kv - s.n + first;
-  const int lo = p.left < 0 ? 0 : max(0, pos - p.left);
+  const int lo = p.left < 0 ? s.lo : max(s.lo, pos - p.left);
   const int hi = p.right < 0 ? s.kv : min(s.kv, pos + n + p.right);
   return make_int2(lo, max(hi, 0));
 }
@@ -171,17 +177,17 @@ struct Seg {
 };
 
 // Walk over the segments of a range of units; the same in every role.
-template <int NQ>
+template <int NQ, class P = AttnParams>
 struct Walk {
   int h, b, t, skip, over;
   long long u, end;
   Seq s, ahead;  // this sequence and the one after it
-  __device__ __forceinline__ void begin(const AttnParams& p) {
+  __device__ __forceinline__ void begin(const P& p) {
     if (u >= end) return;
     s = load_seq(p, b);
     ahead = load_seq(p, b + 1 < p.n_seqs ? b + 1 : 0);
   }
-  __device__ __forceinline__ bool next(const AttnParams& p, Seg& g) {
+  __device__ __forceinline__ bool next(const P& p, Seg& g) {
     if (u >= end) return false;
     const int item = item_tokens<NQ>(p);
     const int2 tr = tile_range<NQ>(p, s, t);
@@ -231,6 +237,72 @@ struct Start {
   long long u, end, total;
   int teams;
 };
+
+// Row of the page table of sequence b, and what is wrong with it.
+__device__ __forceinline__ int table_row(const AttnParams&, int b) { return b; }
+__device__ __forceinline__ void check_seq(const AttnParams& p, int b) {
+  const int a = __ldg(p.cu + b), e = __ldg(p.cu + b + 1), kv = __ldg(p.lens + b);
+  if (a < 0 || e < a || e > p.n_tokens || kv < 0 || kv > p.cap)
+    report(p.status, kDevBounds, kSiteAttnLen, (unsigned)b, (unsigned)kv);
+}
+
+// Attention that reads a prefix once for all sequences that share it, in two
+// launches.  In the first a "sequence" is a group: its rows are the new tokens of
+// all of its members, its keys the prefix, all of which every row sees.  Its
+// results stay as they are, fp32 and with their (m, l), in `pre`.  In the second
+// every sequence attends to what lies behind its prefix and takes the first
+// one's result in as one more part.  Rows of one key/value head lie together in
+// `pre`, in the order in which tiles hold them, four columns of all rows at a
+// time, so that a warp's accesses are contiguous.
+struct PreParams : AttnParams {
+  float4* pre;    // [D / 4][kv_heads * n_tokens * group]
+  float2* pre_ml;
+  const int32_t* prefix;  // [n_real]
+  const int32_t* groups;  // [n_groups + 1]
+  int n_real;             // sequences of the batch
+  __device__ __forceinline__ size_t pre_rows() const {
+    return (size_t)kv_heads * n_tokens * group;
+  }
+  __device__ __forceinline__ size_t pre_row(int head, int token, int gh) const {
+    return ((size_t)head * n_tokens + token) * group + gh;
+  }
+  // Tokens that are taken together; a shorter prefix costs more than it saves.
+  __device__ __forceinline__ int shared(int b) const {
+    const int n = __ldg(prefix + b);
+    return n >= kMinShared ? min(n, cap) : 0;
+  }
+};
+struct PrefixParams : PreParams {};  // n_seqs: groups
+struct SuffixParams : PreParams {};
+
+__device__ __forceinline__ int table_row(const PrefixParams& p, int g) {
+  return min(max(__ldg(p.groups + g), 0), p.n_real - 1);
+}
+__device__ __forceinline__ Seq load_seq(const PrefixParams& p, int g) {
+  const int a = min(max(__ldg(p.groups + g), 0), p.n_real);
+  const int b = min(max(__ldg(p.groups + g + 1), a), p.n_real);
+  Seq s{0, 0, 0, 0};
+  if (b - a < 2) return s;
+  const int x = __ldg(p.cu + a), e = __ldg(p.cu + b);
+  s.kv = p.shared(a);
+  s.n0 = min(max(x, 0), p.n_tokens);
+  s.n = s.kv > 0 ? max(min(e, p.n_tokens) - s.n0, 0) : 0;
+  return s;
+}
+__device__ __forceinline__ void check_seq(const PrefixParams&, int) {}  // in the second launch
+
+__device__ __forceinline__ Seq load_seq(const SuffixParams& p, int b) {
+  Seq s = load_seq(static_cast<const AttnParams&>(p), b);
+  s.lo = p.shared(b);
+  return s;
+}
+__device__ __forceinline__ void check_seq(const SuffixParams& p, int b) {
+  check_seq(static_cast<const AttnParams&>(p), b);
+  // a prefix that some of the new tokens lie in
+  const int past = __ldg(p.lens + b) - (__ldg(p.cu + b + 1) - __ldg(p.cu + b));
+  if (p.shared(b) > max(past, 0))
+    report(p.status, kDevBounds, kSiteAttnLen, (unsigned)b, (unsigned)past);
+}
 
 // Pair of CTAs: a box into this CTA, counted on the first CTA's barrier (`bar`
 // is its address in the cluster).
@@ -390,8 +462,8 @@ __device__ __forceinline__ int v_stage(int j, int n) {
 
 // Where this CTA's range of units begins.  Sequence costs go through `cost`
 // (shared memory, n_seqs entries).  All threads; ends with a barrier.
-template <int NQ>
-__device__ __forceinline__ void find_start(const AttnParams& p, long long* cost, Start* out) {
+template <int NQ, class P>
+__device__ __forceinline__ void find_start(const P& p, long long* cost, Start* out) {
   const int tid = threadIdx.x, lane = tid & 31;
   // key tiles in the low bits, items from here on: both add up
   constexpr int kItemBit = 36;
@@ -406,11 +478,7 @@ __device__ __forceinline__ void find_start(const AttnParams& p, long long* cost,
         const Seq s = load_seq(p, b);
         for (int t = sub; t * item_tokens<NQ>(p) < s.n; t += lps)
           c += ((long long)1 << kItemBit) + max(tile_range<NQ>(p, s, t).y, 1);
-        if (blockIdx.x == 0 && sub == 0) {
-          const int a = __ldg(p.cu + b), e = __ldg(p.cu + b + 1), kv = __ldg(p.lens + b);
-          if (a < 0 || e < a || e > p.n_tokens || kv < 0 || kv > p.cap)
-            report(p.status, kDevBounds, kSiteAttnLen, (unsigned)b, (unsigned)kv);
-        }
+        if (blockIdx.x == 0 && sub == 0) check_seq(p, b);
       }
       for (int o = lps >> 1; o; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
       if (b < p.n_seqs && sub == 0) cost[b] = c;
@@ -500,9 +568,11 @@ __device__ __forceinline__ void find_start(const AttnParams& p, long long* cost,
   __syncthreads();
 }
 
-template <int D, int NQ, bool PAIR, bool FP16>
-__global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constant__ AttnParams p) {
+template <int D, int NQ, bool PAIR, bool FP16, class P = AttnParams>
+__global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constant__ P p) {
   using C = Cfg<D, NQ, PAIR>;
+  constexpr bool PREFIX = std::is_same<P, PrefixParams>::value;
+  constexpr bool SUFFIX = std::is_same<P, SuffixParams>::value;
   constexpr int NS = C::kStages, PARTS = C::kParts, SH = C::kShare;
   constexpr int KROWS = kKeys / SH;             // keys of a tile in this CTA
   constexpr int NC = NQ == 2 ? 128 : 64;        // score columns a softmax thread
@@ -581,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   }
   const uint32_t tmem = tmem_holder;
   const int rank = PAIR ? blockIdx.x % 2 : 0;
-  Walk<NQ> w;
+  Walk<NQ, P> w;
   w.h = start.h;
   w.b = start.b;
   w.t = start.t;
@@ -649,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
           int id = p.n_pages;
           const int key = (base + lane) << piece_shift, pg = key >> p.page_shift;
           if (key < g.khi && ((pg + 1) << p.page_shift) > g.klo) {
-            id = __ldg(p.table + (int64_t)g.b * p.table_stride + pg);
+            id = __ldg(p.table + (int64_t)table_row(p, g.b) * p.table_stride + pg);
             if ((unsigned)id >= (unsigned)p.n_pages) {
               report(p.status, kDevBounds, kSiteAttnPage, (unsigned)g.b, (unsigned)id);
               id = p.n_pages;
@@ -926,7 +996,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     int xn = 0;           // exchanges (NQ = 1)
     uint32_t tails = 0;   // phase of each stage's tail_full
     bool ok = true;
-    JoinRec rec{0, 0, 0, 0};
+    JoinRec rec{0, 0, 0, 0, 0};
     while (ok && w.next(p, g)) {
       const bool row_live = tok < p.step && tok + i * p.step < g.ntok;
       const bool live = __any_sync(0xffffffffu, row_live);
@@ -937,6 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       if (row_live) {
         const int qp = g.pos + i * p.step + tok;
         lo = p.left < 0 ? 0 : max(0, qp - p.left);
+        if constexpr (SUFFIX) lo = max(lo, g.klo);
         hi = max(lo, p.right < 0 ? g.kv : min(g.kv, qp + p.right + 1));
       }
       float m = -INFINITY, l = 0.f;
@@ -1097,6 +1168,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
           ++xn;
         }
         const bool whole = g.first && g.last;
+        // the part of a shared prefix, and what this one counts beside it
+        bool pre = false;
+        size_t pre_at = 0;
+        float own = 1.f, pre_f = 0.f;
+        if constexpr (PREFIX || SUFFIX) {
+          pre_at = p.pre_row(g.head, g.tok0 + i * p.step + tok, gh);
+          if (SUFFIX && whole && row_live && g.klo > 0) {
+            const float2 q = p.pre_ml[pre_at];
+            pre = !(q.y == 0.f);  // one that saw nothing holds nothing
+            if (pre) {
+              const float top = fmaxf(m, q.x);
+              own = l == 0.f ? 0.f : exp2f(m - top);
+              pre_f = exp2f(q.x - top);
+              l = (l == 0.f ? 0.f : own * l) + pre_f * q.y;
+              m = top;
+            }
+          }
+        }
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
         const int trow = g.tok0 + i * p.step + tok;
         const int head = g.head * p.group + gh;
@@ -1114,7 +1203,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             for (int e = 0; e < 32; ++e) o[e] = 0.f;
           }
           if (!row_live) continue;
-          if (whole) {
+          if constexpr (SUFFIX) {
+            if (pre) {
+              const float4* src = p.pre + (size_t)((o0 + c) / 4) * p.pre_rows() + pre_at;
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 x = src[e / 4 * p.pre_rows()];
+                const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)  // (O may hold anything where nothing was seen)
+                  o[e + k] = (own == 0.f ? 0.f : own * o[e + k]) + pre_f * y[k];
+              }
+            }
+          }
+          if (PREFIX && whole) {
+            if constexpr (PREFIX) {
+              float4* dst = p.pre + (size_t)((o0 + c) / 4) * p.pre_rows() + pre_at;
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                dst[e / 4 * p.pre_rows()] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+          } else if (whole) {
             uint16_t* dst = p.out + trow * p.o_tok + head * p.o_head + o0 + c;
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
@@ -1140,6 +1249,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         if (row_live && (NQ == 2 || wg == 0)) {
           if (!whole)
             p.ml[prow] = make_float2(m, l);
+          else if constexpr (PREFIX)
+            p.pre_ml[pre_at] = make_float2(m, l);
           else if (p.lse)
             p.lse[(size_t)trow * (p.kv_heads * p.group) + head] =
                 l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
@@ -1154,6 +1265,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         rec.head = g.head;
         rec.tok0 = g.tok0;
         rec.ntok = g.ntok;
+        if constexpr (SUFFIX) rec.shared = g.klo > 0;
       }
       if (g.n) {
         pos += 2 * PARTS * g.n;
@@ -1164,7 +1276,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       if (lane == 0) report(p.status, kDevTimeout, kSiteAttnSoftmax, (unsigned)at, (unsigned)warp);
       *abort_flag = 1;
     }
-    if (tid == 0) p.rec[blockIdx.x] = ok ? rec : JoinRec{0, 0, 0, 0};
+    if (tid == 0) p.rec[blockIdx.x] = ok ? rec : JoinRec{0, 0, 0, 0, 0};
   }
 
   tc_fence_before();
@@ -1193,8 +1305,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
 // reference, o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i, parts in order,
 // BATCH of them in flight.  A thread takes eight columns of a row,
 // neighbouring threads neighbouring rows.
-template <int D, int NQ, int BATCH, bool FP16>
-__global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnParams p) {
+template <int D, int NQ, int BATCH, bool FP16, class P = AttnParams>
+__global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ P p) {
+  constexpr bool PREFIX = std::is_same<P, PrefixParams>::value;
+  constexpr bool SUFFIX = std::is_same<P, SuffixParams>::value;
   pdl_trigger();
   pdl_wait();
   const JoinRec rec = p.rec[blockIdx.x];
@@ -1249,13 +1363,37 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnP
           acc[7] += f * v[k][1].w;
         }
     }
+    const int trow = rec.tok0 + tok, head = rec.head * p.group + gh;
+    if constexpr (PREFIX) {
+      const size_t at = p.pre_row(rec.head, trow, gh);
+      p.pre[2 * c * p.pre_rows() + at] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      p.pre[(2 * c + 1) * p.pre_rows() + at] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      if (c == 0) p.pre_ml[at] = make_float2(m, l);
+      continue;
+    }
+    if constexpr (SUFFIX) {
+      if (rec.shared) {
+        const size_t at = p.pre_row(rec.head, trow, gh);
+        const float2 q = p.pre_ml[at];
+        const float4 x = p.pre[2 * c * p.pre_rows() + at];
+        const float4 y = p.pre[(2 * c + 1) * p.pre_rows() + at];
+        if (!(q.y == 0.f)) {
+          const float top = fmaxf(m, q.x), f = exp2f(q.x - top);
+          const float own = l == 0.f ? 0.f : exp2f(m - top);  // (acc is 0 with l)
+          const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+          l = own * l + f * q.y;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] = own * acc[e] + f * z[e];
+          m = top;
+        }
+      }
+    }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint4 r = make_uint4(0u, 0u, 0u, 0u);
     if (l != 0.f)
       r = make_uint4(
           pack16<FP16>(acc[0] * inv, acc[1] * inv), pack16<FP16>(acc[2] * inv, acc[3] * inv),
           pack16<FP16>(acc[4] * inv, acc[5] * inv), pack16<FP16>(acc[6] * inv, acc[7] * inv));
-    const int trow = rec.tok0 + tok, head = rec.head * p.group + gh;
     *reinterpret_cast<uint4*>(p.out + trow * p.o_tok + head * p.o_head + 8 * c) = r;
     if (p.lse && c == 0)
       p.lse[(size_t)trow * (p.kv_heads * p.group) + head] =
@@ -1276,7 +1414,14 @@ struct Variant {
   static constexpr bool kPair = pair_of(D);
   static constexpr auto few = k_paged_attn<D, 1, false, FP16>;
   static constexpr auto many = k_paged_attn<D, kManyNq, kPair, FP16>;
-  static cudaError_t run(bool m, const AttnParams& p, int ctas, cudaStream_t s) {
+  template <class P>
+  static constexpr auto few_of = k_paged_attn<D, 1, false, FP16, P>;
+  template <class P>
+  static constexpr auto many_of = k_paged_attn<D, kManyNq, kPair, FP16, P>;
+  // P: plain, PrefixParams, or SuffixParams (few rows alone)
+  template <class P>
+  static cudaError_t run(bool m, const P& p, int ctas, cudaStream_t s) {
+    constexpr bool kSuffix = std::is_same<P, SuffixParams>::value;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
@@ -1290,20 +1435,30 @@ struct Variant {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = m && kPair ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, m ? many : few, p);
+    cudaError_t e;
+    if constexpr (kSuffix)
+      e = cudaLaunchKernelEx(&cfg, few_of<P>, p);
+    else
+      e = cudaLaunchKernelEx(&cfg, m ? many_of<P> : few_of<P>, p);
     if (e != cudaSuccess) return e;
     // few rows are split into many parts, many rows into two or three
-    if (m && kManyNq == 2)
-      return launch_pdl(k_attn_join<D, kManyNq, 2, FP16>, dim3(ctas, 8), dim3(256), 0, s, p);
-    if (m) return launch_pdl(k_attn_join<D, 1, 2, FP16>, dim3(ctas, 8), dim3(256), 0, s, p);
-    return launch_pdl(k_attn_join<D, 1, 8, FP16>, dim3(ctas), dim3(256), 0, s, p);
+    if constexpr (!kSuffix) {
+      if (m && kManyNq == 2)
+        return launch_pdl(k_attn_join<D, kManyNq, 2, FP16, P>, dim3(ctas, 8), dim3(256), 0, s, p);
+      if (m) return launch_pdl(k_attn_join<D, 1, 2, FP16, P>, dim3(ctas, 8), dim3(256), 0, s, p);
+    }
+    return launch_pdl(k_attn_join<D, 1, 8, FP16, P>, dim3(ctas), dim3(256), 0, s, p);
+  }
+  template <class K>
+  static cudaError_t limit(K kernel, size_t smem) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   }
   static cudaError_t prepare() {
-    cudaError_t e = cudaFuncSetAttribute(few, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)Cfg<D, 1, false>::kSmem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(many, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)Cfg<D, kManyNq, kPair>::kSmem);
+    cudaError_t e = limit(few, Cfg<D, 1, false>::kSmem);
+    if (e == cudaSuccess) e = limit(many, Cfg<D, kManyNq, kPair>::kSmem);
+    if (e == cudaSuccess) e = limit(few_of<PrefixParams>, Cfg<D, 1, false>::kSmem);
+    if (e == cudaSuccess) e = limit(many_of<PrefixParams>, Cfg<D, kManyNq, kPair>::kSmem);
+    if (e == cudaSuccess) e = limit(few_of<SuffixParams>, Cfg<D, 1, false>::kSmem);
     return e;
   }
 };
@@ -1314,11 +1469,33 @@ cudaError_t prepare_dim(int d) {
          : d == 128 ? Variant<128, FP16>::prepare()
                     : Variant<64, FP16>::prepare();
 }
-template <bool FP16>
-cudaError_t run_dim(int d, bool many, const AttnParams& p, int ctas, cudaStream_t s) {
+template <bool FP16, class P>
+cudaError_t run_dim(int d, bool many, const P& p, int ctas, cudaStream_t s) {
   return d == 256   ? Variant<256, FP16>::run(many, p, ctas, s)
          : d == 128 ? Variant<128, FP16>::run(many, p, ctas, s)
                     : Variant<64, FP16>::run(many, p, ctas, s);
+}
+template <class P>
+dg_status_t run_call(const dg_attn* a, bool many, const P& p, dg_stream_t stream) {
+  const dg_kv_config_t& c = a->kv->cfg;
+  const int ctas = a->ctas / p.team * p.team;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = c.dtype == DG_T_FP16 ? run_dim<true>(c.head_dim, many, p, ctas, s)
+                                             : run_dim<false>(c.head_dim, many, p, ctas, s);
+  return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+}
+
+// Results of the shared prefixes: fp32 rows, and their (m, l).
+struct PreLayout {
+  size_t o, ml, total;
+};
+PreLayout pre_layout(const dg_attn_config_t& a, const dg_kv_config_t& c, int n_tokens) {
+  const size_t rows = (size_t)n_tokens * a.n_q_heads;
+  PreLayout L;
+  L.o = 0;
+  L.ml = round_up(rows * c.head_dim * sizeof(float), 256);
+  L.total = L.ml + rows * sizeof(float2);
+  return L;
 }
 
 dg_status_t check_config(const dg_attn_config_t* c, const dg_kv* kv) {
@@ -1327,6 +1504,91 @@ dg_status_t check_config(const dg_attn_config_t* c, const dg_kv* kv) {
     return DG_ERR_INVALID_ARG;
   if (c->n_q_heads % kv->cfg.n_kv_heads) return DG_ERR_INVALID_ARG;
   if (c->n_q_heads / kv->cfg.n_kv_heads > kRows) return DG_ERR_UNSUPPORTED;
+  return DG_OK;
+}
+
+// Checks of a call's arguments; *done: nothing to do.
+dg_status_t check_call(const dg_attn* a, int layer, const dg_heads_t* q, const dg_heads_t* out,
+                       const float* lse, const dg_kv_batch_t* batch, int n_tokens, bool* done) {
+  *done = false;
+  if (!a) return DG_ERR_INVALID_ARG;
+  const dg_kv_config_t& c = a->kv->cfg;
+  if (layer < 0 || layer >= c.n_layers || n_tokens < 0) return DG_ERR_INVALID_ARG;
+  dg_status_t st = check_batch(batch, c);
+  if (st != DG_OK) return st;
+  if (n_tokens > kMaxKvTokens) return DG_ERR_UNSUPPORTED;
+  *done = n_tokens == 0 || batch->n_seqs == 0;
+  if (*done) return DG_OK;
+  if ((st = check_heads(q)) != DG_OK || (st = check_heads(out)) != DG_OK) return st;
+  if (lse && !aligned(lse, 4)) return DG_ERR_ALIGNMENT;
+  if (q->p == out->p) return DG_ERR_INVALID_ARG;
+  return DG_OK;
+}
+
+// The parameters of a launch over sequences of `rows` rows on average, and
+// whether it takes the variant for many.
+dg_status_t set_up(const dg_attn* a, int layer, const dg_heads_t* q, const dg_heads_t* out,
+                   float* lse, const dg_kv_batch_t* batch, int n_tokens, int64_t rows,
+                   AttnParams& p, bool* takes_many) {
+  const dg_kv_config_t& c = a->kv->cfg;
+  const int group = a->cfg.n_q_heads / c.n_kv_heads;
+  p.step = kRows / group;
+  p.q_box = p.step < n_tokens ? p.step : n_tokens;
+  const dg_status_t st = encode_queries(&p.qm, *q, a->cfg.n_q_heads, c.head_dim, n_tokens, group, p.q_box);
+  if (st != DG_OK) return st;
+  // Few rows (one tile a CTA) or many, by the average rows of a sequence.  16
+  // sequences behind 4000 cached tokens, 4 query heads a key/value head, us few
+  // / many: head size 64: 41 / 48 at 128 rows, 65 / 53 at 192, 112 / 94 at 512;
+  // 128: 65 / 63 at 128, 104 / 69 at 192, 180 / 123 at 512; 256: 93 / 95 at 32,
+  // 102 / 99 at 64, 199 / 113 at 256.
+  const bool many = rows > (c.head_dim == 256 ? 32 : 128);
+  const int ps = c.page_size;
+  const int kmax = 1 << key_shift_max(c.head_dim, many && pair_of(c.head_dim));
+  const int vmax = 1 << value_shift_max(c.head_dim);
+  const uint32_t kbox = ps < kmax ? ps : kmax, vbox = ps < vmax ? ps : vmax;
+  if (!encode_pages(&p.km, c, c.k, layer, kbox) || !encode_pages(&p.vm, c, c.v, layer, vbox))
+    return DG_ERR_CUDA;
+  p.table = batch->page_table;
+  p.table_stride = batch->table_stride;
+  p.lens = batch->lens;
+  p.cu = batch->cu;
+  p.n_seqs = batch->n_seqs;
+  p.cap = batch->max_pages * c.page_size;
+  p.n_tokens = n_tokens;
+  p.n_pages = c.n_pages;
+  p.page_shift = log2_of(c.page_size);
+  p.kv_heads = c.n_kv_heads;
+  p.group = group;
+  // a limit past every distance is none
+  p.left = a->cfg.left >= p.cap + n_tokens ? -1 : a->cfg.left;
+  p.right = a->cfg.right >= p.cap + n_tokens ? -1 : a->cfg.right;
+  p.scale2 = a->cfg.scale * 1.4426950408889634f;
+  p.out = static_cast<uint16_t*>(out->p);
+  p.o_tok = out->token_stride;
+  p.o_head = out->head_stride;
+  p.lse = lse;
+  p.part = reinterpret_cast<float4*>(a->ws + a->L.part);
+  p.ml = reinterpret_cast<float2*>(a->ws + a->L.ml);
+  p.rec = reinterpret_cast<JoinRec*>(a->ws + a->L.rec);
+  p.status = reinterpret_cast<DevStatus*>(a->ws + a->L.status);
+  // Many, head size 256: a pair, and teams of two pairs when there are that
+  // many tiles (us teams of two CTAs / four: 113 / 174 at 256 rows, 202 / 181 at
+  // 512).  Up to 128: every CTA by itself, unless a sequence's keys and values
+  // can be past the L2 (129 MB) and its tiles are many: then teams of four read
+  // them from memory once (heads of 128, 4 query heads on each of 8, us by
+  // itself / four: 4096 tokens behind 131072 6350 / 5712, behind 12288 572 / 615;
+  // 12 sequences of 20 to 600 283 / 357).
+  const int wide = c.head_dim == 256 ? kRows : 2 * kRows;
+  const int64_t seq_bytes = (int64_t)batch->max_pages * ps * c.n_kv_heads * c.head_dim * 4;
+  const bool past_l2 = seq_bytes > ((int64_t)256 << 20);
+  if (!many) p.team = 1;
+  else if (c.head_dim == 256) p.team = rows > 2 * wide ? 4 : 2;
+  else p.team = rows > 4 * wide && past_l2 ? 4 : 1;
+  // Ending one item and beginning the next, in key tiles: results to write, and
+  // a pipeline to fill again (8 canvases at 0, 2, 4, 6, 8: 120, 117, 114, 111,
+  // 110 us; the other two barely move).
+  p.over = !many ? 1 : (c.head_dim == 256 ? 6 : 2);
+  *takes_many = many;
   return DG_OK;
 }
 
@@ -1401,80 +1663,69 @@ dg_status_t dg_attn_destroy(dg_attn_t* a) {
 dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const dg_heads_t* out,
                             float* lse, const dg_kv_batch_t* batch, int n_tokens,
                             dg_stream_t stream) {
-  if (!a) return DG_ERR_INVALID_ARG;
-  const dg_kv_config_t& c = a->kv->cfg;
-  if (layer < 0 || layer >= c.n_layers || n_tokens < 0) return DG_ERR_INVALID_ARG;
-  dg_status_t st = check_batch(batch, c);
-  if (st != DG_OK) return st;
-  if (n_tokens > kMaxKvTokens) return DG_ERR_UNSUPPORTED;
-  if (n_tokens == 0 || batch->n_seqs == 0) return DG_OK;
-  if ((st = check_heads(q)) != DG_OK || (st = check_heads(out)) != DG_OK) return st;
-  if (lse && !aligned(lse, 4)) return DG_ERR_ALIGNMENT;
-  if (q->p == out->p) return DG_ERR_INVALID_ARG;
-  const int group = a->cfg.n_q_heads / c.n_kv_heads;
-  AttnParams p;
-  p.step = kRows / group;
-  p.q_box = p.step < n_tokens ? p.step : n_tokens;
-  st = encode_queries(&p.qm, *q, a->cfg.n_q_heads, c.head_dim, n_tokens, group, p.q_box);
-  if (st != DG_OK) return st;
-  // Few rows (one tile a CTA) or many, by the average rows of a sequence.  16
-  // sequences behind 4000 cached tokens, 4 query heads a key/value head, us few
-  // / many: head size 64: 41 / 48 at 128 rows, 65 / 53 at 192, 112 / 94 at 512;
-  // 128: 65 / 63 at 128, 104 / 69 at 192, 180 / 123 at 512; 256: 93 / 95 at 32,
-  // 102 / 99 at 64, 199 / 113 at 256.
+  bool done, many;
+  dg_status_t st = check_call(a, layer, q, out, lse, batch, n_tokens, &done);
+  if (st != DG_OK || done) return st;
+  const int group = a->cfg.n_q_heads / a->kv->cfg.n_kv_heads;
   const int64_t rows = (int64_t)n_tokens * group / batch->n_seqs;
-  const bool many = rows > (c.head_dim == 256 ? 32 : 128);
-  const int ps = c.page_size;
-  const int kmax = 1 << key_shift_max(c.head_dim, many && pair_of(c.head_dim));
-  const int vmax = 1 << value_shift_max(c.head_dim);
-  const uint32_t kbox = ps < kmax ? ps : kmax, vbox = ps < vmax ? ps : vmax;
-  if (!encode_pages(&p.km, c, c.k, layer, kbox) || !encode_pages(&p.vm, c, c.v, layer, vbox))
-    return DG_ERR_CUDA;
-  p.table = batch->page_table;
-  p.table_stride = batch->table_stride;
-  p.lens = batch->lens;
-  p.cu = batch->cu;
-  p.n_seqs = batch->n_seqs;
-  p.cap = batch->max_pages * c.page_size;
-  p.n_tokens = n_tokens;
-  p.n_pages = c.n_pages;
-  p.page_shift = log2_of(c.page_size);
-  p.kv_heads = c.n_kv_heads;
-  p.group = group;
-  // a limit past every distance is none
-  p.left = a->cfg.left >= p.cap + n_tokens ? -1 : a->cfg.left;
-  p.right = a->cfg.right >= p.cap + n_tokens ? -1 : a->cfg.right;
-  p.scale2 = a->cfg.scale * 1.4426950408889634f;
-  p.out = static_cast<uint16_t*>(out->p);
-  p.o_tok = out->token_stride;
-  p.o_head = out->head_stride;
-  p.lse = lse;
-  p.part = reinterpret_cast<float4*>(a->ws + a->L.part);
-  p.ml = reinterpret_cast<float2*>(a->ws + a->L.ml);
-  p.rec = reinterpret_cast<JoinRec*>(a->ws + a->L.rec);
-  p.status = reinterpret_cast<DevStatus*>(a->ws + a->L.status);
-  // Many, head size 256: a pair, and teams of two pairs when there are that
-  // many tiles (us teams of two CTAs / four: 113 / 174 at 256 rows, 202 / 181 at
-  // 512).  Up to 128: every CTA by itself, unless a sequence's keys and values
-  // can be past the L2 (129 MB) and its tiles are many: then teams of four read
-  // them from memory once (heads of 128, 4 query heads on each of 8, us by
-  // itself / four: 4096 tokens behind 131072 6350 / 5712, behind 12288 572 / 615;
-  // 12 sequences of 20 to 600 283 / 357).
-  const int wide = c.head_dim == 256 ? kRows : 2 * kRows;
-  const int64_t seq_bytes = (int64_t)batch->max_pages * ps * c.n_kv_heads * c.head_dim * 4;
-  const bool past_l2 = seq_bytes > ((int64_t)256 << 20);
-  if (!many) p.team = 1;
-  else if (c.head_dim == 256) p.team = rows > 2 * wide ? 4 : 2;
-  else p.team = rows > 4 * wide && past_l2 ? 4 : 1;
-  // Ending one item and beginning the next, in key tiles: results to write, and
-  // a pipeline to fill again (8 canvases at 0, 2, 4, 6, 8: 120, 117, 114, 111,
-  // 110 us; the other two barely move).
-  p.over = !many ? 1 : (c.head_dim == 256 ? 6 : 2);
-  const int ctas = a->ctas / p.team * p.team;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = c.dtype == DG_T_FP16 ? run_dim<true>(c.head_dim, many, p, ctas, s)
-                                             : run_dim<false>(c.head_dim, many, p, ctas, s);
-  return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+  AttnParams p;
+  st = set_up(a, layer, q, out, lse, batch, n_tokens, rows, p, &many);
+  return st != DG_OK ? st : run_call(a, many, p, stream);
+}
+
+dg_status_t dg_attn_shared_workspace_size(const dg_attn_config_t* cfg, const dg_kv_t* kv,
+                                          int n_tokens, size_t* bytes) {
+  if (!bytes) return DG_ERR_INVALID_ARG;
+  const dg_status_t s = check_config(cfg, kv);
+  if (s != DG_OK) return s;
+  if (n_tokens < 0) return DG_ERR_INVALID_ARG;
+  if (n_tokens > kMaxKvTokens) return DG_ERR_UNSUPPORTED;
+  *bytes = pre_layout(*cfg, kv->cfg, n_tokens).total;
+  return DG_OK;
+}
+
+dg_status_t dg_attn_forward_shared(dg_attn_t* a, int layer, const dg_heads_t* q,
+                                   const dg_heads_t* out, float* lse, const dg_kv_batch_t* batch,
+                                   const dg_attn_shared_t* shared, int n_tokens,
+                                   dg_stream_t stream) {
+  bool done, many;
+  dg_status_t st = check_call(a, layer, q, out, lse, batch, n_tokens, &done);
+  if (st != DG_OK || done) return st;
+  if (!shared || shared->n_groups < 0) return DG_ERR_INVALID_ARG;
+  if (shared->n_groups > kMaxSeqs) return DG_ERR_UNSUPPORTED;
+  if (!shared->prefix || (shared->n_groups && !shared->groups)) return DG_ERR_INVALID_ARG;
+  if (!aligned(shared->prefix, 4) || !aligned(shared->groups, 4)) return DG_ERR_ALIGNMENT;
+  const dg_kv_config_t& c = a->kv->cfg;
+  const PreLayout L = pre_layout(a->cfg, c, n_tokens);
+  if (!shared->workspace || shared->workspace_bytes < L.total ||
+      !aligned(shared->workspace, 1024))
+    return DG_ERR_WORKSPACE;
+  const int group = a->cfg.n_q_heads / c.n_kv_heads;
+  const int64_t rows = (int64_t)n_tokens * group / batch->n_seqs;
+  if (shared->n_groups == 0 || a->cfg.left >= 0 || rows > kMaxSharedRows)
+    return dg_attn_forward(a, layer, q, out, lse, batch, n_tokens, stream);
+  uint8_t* ws = static_cast<uint8_t*>(shared->workspace);
+  auto with = [&](PreParams& p) {
+    p.pre = reinterpret_cast<float4*>(ws + L.o);
+    p.pre_ml = reinterpret_cast<float2*>(ws + L.ml);
+    p.prefix = shared->prefix;
+    p.groups = shared->groups;
+    p.n_real = batch->n_seqs;
+  };
+  PrefixParams first;
+  st = set_up(a, layer, q, out, lse, batch, n_tokens,
+              (int64_t)n_tokens * group / shared->n_groups, first, &many);
+  if (st != DG_OK) return st;
+  with(first);
+  first.n_seqs = shared->n_groups;
+  first.left = first.right = -1;
+  SuffixParams second;
+  bool unused;
+  st = set_up(a, layer, q, out, lse, batch, n_tokens, 1, second, &unused);
+  if (st != DG_OK) return st;
+  with(second);
+  st = run_call(a, many, first, stream);
+  return st != DG_OK ? st : run_call(a, false, second, stream);
 }
 
 dg_status_t dg_attn_last_device_status(dg_attn_t* a, dg_stream_t stream, unsigned int* where,

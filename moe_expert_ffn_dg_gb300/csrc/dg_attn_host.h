@@ -95,6 +95,7 @@ constexpr int kWeightKeys = 2 * kKeys;  // keys of a weights item
 struct JoinRec {
   int parts;  // 0: none
   int head, tok0, ntok;
+  int shared;  // a shared prefix's part is to be joined too
 };
 struct WeightRec {
   int parts;  // 0: none
