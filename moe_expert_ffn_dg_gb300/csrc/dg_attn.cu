@@ -395,28 +395,6 @@ __host__ __device__ constexpr int key_shift_max(int d, bool pair) {
 }
 __host__ __device__ constexpr int value_shift_max(int d) { return d == 128 ? 7 : 6; }
 
-// The same with A in tensor memory.
-template <bool PAIR>
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
-                                        uint32_t idesc, int accumulate) {
-  if constexpr (PAIR)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "mov.b64 b, {%2, %5};\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "mov.b64 b, {%2, %5};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
-        : "memory");
-}
-
 // Arrive, when this thread's MMAs so far are done, on `bar` of this CTA, or of
 // both CTAs of a pair.
 template <bool PAIR>

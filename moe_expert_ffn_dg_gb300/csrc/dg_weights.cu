@@ -9,16 +9,16 @@
 // query rows (the G heads of a group packed with their tokens, row = token * G +
 // head of the group) are the columns.
 //
-// A work item is 256 keys of a sequence (two tiles of 128, one a warpgroup)
-// against all of its rows that see them, head after head; its units are single
+// A work item is 256 keys of a sequence (two tiles of 128) against all of its rows that see them, head after head; its units are single
 // query tiles.  All units of a call lie in one line (sequences, blocks of keys,
 // heads, tiles) and every CTA takes a contiguous range, so that long and short
 // sequences balance alike.  An item that crosses a range boundary leaves fp32
 // partial sums in the workspace, joined in a fixed order by k_weights_join: the
 // result does not depend on which CTA comes first.
 //
-// Warps 0-3 and 4-7: exponentials and sums; 8: copies of keys; 9: MMA issuer and
-// TMEM owner; 10: copies of queries; 11: log-sums.
+// Warps: eight (few rows) or sixteen for exponentials and sums, then one each for
+// copies of keys, for the MMAs (it owns the tensor memory), for copies of
+// queries and for log-sums.
 #include <math.h>
 #include <string.h>
 
@@ -33,8 +33,6 @@ using namespace dg::host;
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kLseSlots = 4;
 
 // Sites of the device status word.
 enum : unsigned int {
@@ -76,6 +74,11 @@ struct Cfg {
   static constexpr size_t kSmem = (size_t)kKeyStages * kKeyBytes + (size_t)kRowStages * kRowBytes;
   static constexpr int kBufs = QN == 16 ? 4 : 2;  // score buffers of a key tile
   static constexpr uint32_t kTmem = 2 * kBufs * QN;
+  // Warpgroups that share a key tile's columns.  Two, 64 columns each: with one
+  // the latency of the loads and exponentials shows.
+  static constexpr int kColGroups = QN == 16 ? 1 : 2;
+  static constexpr int kSumWarps = 8 * kColGroups;
+  static constexpr int kThreads = 32 * (kSumWarps + 4);
 };
 
 struct Seq {
@@ -296,14 +299,18 @@ __device__ __forceinline__ void write_weight(const WeightParams& p, int b, int n
 }
 
 template <int D, int QN, bool FP16>
-__global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__ WeightParams p) {
+__global__ void __launch_bounds__(Cfg<D, QN>::kThreads, 1) k_weights(const __grid_constant__ WeightParams p) {
   using C = Cfg<D, QN>;
   constexpr int NK = C::kKeyStages, NR = C::kRowStages, NB = C::kBufs, PARTS = C::kParts;
+  constexpr int LS = NB + 1;  // query tiles whose log-sums are held
+  constexpr int CG = C::kColGroups, W0 = C::kSumWarps;  // W0: first of the other warps
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t keys = smem_u32(smem), rows = keys + NK * C::kKeyBytes;
   __shared__ uint64_t k_full[NK], k_empty[NK], q_full[NR], q_empty[NR];
-  __shared__ uint64_t s_full[NB], s_empty[NB], l_full[kLseSlots], l_empty[kLseSlots], drain;
-  __shared__ __align__(16) float lse[kLseSlots][QN];  // -lse log2 e
+  __shared__ uint64_t s_full[NB], s_empty[NB], drain;
+  __shared__ uint64_t x_full[2], x_empty[2];    // sums of a key tile's second column group
+  __shared__ float xch[CG == 2 ? kWeightKeys : 1];
+  __shared__ __align__(16) float lse[LS][QN];  // -lse log2 e of a query tile
   __shared__ uint32_t tmem_holder;
   __shared__ int abort_word;
   __shared__ Start start;
@@ -325,22 +332,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       mbar_init(&q_empty[i], 1);
     }
     for (int i = 0; i < NB; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 8);
+      mbar_init(&s_full[i], 2);  // the products, and the log-sums
+      mbar_init(&s_empty[i], W0);
     }
-    for (int i = 0; i < kLseSlots; ++i) {
-      mbar_init(&l_full[i], 1);
-      mbar_init(&l_empty[i], 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&x_full[i], 4);
+      mbar_init(&x_empty[i], 4);
     }
     mbar_init(&drain, 1);
     abort_word = 0;
     fence_mbar_init();
   }
-  if (tid == 8 * 32) {
+  if (tid == W0 * 32) {
     tma_prefetch_map(&p.qm);
     tma_prefetch_map(&p.km);
   }
-  if (warp == 9) {
+  if (warp == W0 + 1) {
     tmem_alloc(&tmem_holder, C::kTmem);
     tmem_relinquish();
   }
@@ -355,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
   // key tiles of a segment's block
   auto tiles_of = [](const Seg& s) { return s.kv - s.kb * kWeightKeys > kKeys ? 2 : 1; };
 
-  if (warp == 8) {
+  if (warp == W0) {
     // ---------------------------------------------------------------- keys
     const bool leader = elect_one();
     const int piece_shift = min(p.page_shift, 7), piece = 1 << piece_shift;
@@ -421,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
         done = wait_drain(&k_full[i % NK], (uint32_t)(i / NK) & 1u);
       if (!done && ok) report(p.status, kDevTimeout, kSiteWeightDrain, 8u, 0u);
     }
-  } else if (warp == 10) {
+  } else if (warp == W0 + 2) {
     // ------------------------------------------------------------- queries
     const bool leader = elect_one();
     Cursor<NR> c;
@@ -454,40 +461,62 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
         done = wait_drain(&q_full[i % NR], (uint32_t)(i / NR) & 1u);
       if (!done && ok) report(p.status, kDevTimeout, kSiteWeightDrain, 10u, 0u);
     }
-  } else if (warp == 11) {
+  } else if (warp == W0 + 3) {
     // ------------------------------------------------------------ log-sums
-    Cursor<kLseSlots> c;
-    bool ok = true;
+    // Fetched a tile ahead, written when the tile's score buffer is free: all warps
+    // have then taken the scores of tile T - NB, and done with those before it; a
+    // place is used again after NB + 1 tiles.
+    constexpr int NL = (QN + 31) / 32;
     const int heads = p.kv_heads * p.group;
-    while (ok && w.next(p, g))
-      for (int t = 0; t < g.tiles; ++t) {
-        const int i0 = (g.t0 + t) * p.step;
-        const int live = min(p.step, g.n - i0) * p.group;
-        float v[(QN + 31) / 32];
+    int tok[NL], off[NL];
 #pragma unroll
-        for (int k = 0; k < (QN + 31) / 32; ++k) {
-          const int r = lane + 32 * k;
-          const int tok = (unsigned)r / (unsigned)p.group, gh = r - tok * p.group;
-          v[k] = 0.f;  // rows that are not there: any finite number
-          if (r < live)
-            v[k] = -1.4426950408889634f *
-                   __ldg(p.lse + (int64_t)(g.n0 + i0 + tok) * heads + g.head * p.group + gh);
-        }
-        const bool here = mbar_wait(&l_empty[c.st], c.ph ^ 1u, abort_flag);
-        ok = __all_sync(0xffffffffu, here);
-        if (!ok) break;
-#pragma unroll
-        for (int k = 0; k < (QN + 31) / 32; ++k)
-          if (lane + 32 * k < QN) lse[c.st][lane + 32 * k] = v[k];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&l_full[c.st]);
-        c.next();
+    for (int i = 0; i < NL; ++i) {
+      const int c = lane + 32 * i;
+      tok[i] = (unsigned)c / (unsigned)p.group;
+      off[i] = tok[i] * heads + c % p.group;
+      if (c >= QN || tok[i] >= p.step) tok[i] = 1 << 30;  // no row
+    }
+    float ahead[NL];
+    int t = 0;
+    bool ok = true;
+    auto fetch = [&] {  // the next tile's, if there is one
+      ++t;
+      while (t >= g.tiles) {
+        if (!w.next(p, g)) return false;
+        t = 0;
       }
+      const int i0 = (g.t0 + t) * p.step;
+      const float* src = p.lse + (int64_t)(g.n0 + i0) * heads + g.head * p.group;
+#pragma unroll
+      for (int i = 0; i < NL; ++i)
+        ahead[i] = tok[i] < g.n - i0 ? __ldg(src + off[i]) : 0.f;  // no row: any finite number
+      return true;
+    };
+    g.tiles = 0;
+    bool more = fetch();
+    Cursor<NB> sc;
+    Cursor<LS> lc;
+    while (more) {
+      float now[NL];
+#pragma unroll
+      for (int i = 0; i < NL; ++i) now[i] = ahead[i];
+      more = fetch();
+      const bool here = mbar_wait(&s_empty[sc.st], sc.ph ^ 1u, abort_flag);
+      ok = __all_sync(0xffffffffu, here);
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < NL; ++i)
+        if (QN % 32 == 0 || lane < QN) lse[lc.st][lane + 32 * i] = -1.4426950408889634f * now[i];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_full[sc.st]);
+      sc.next();
+      lc.next();
+    }
     if (!ok) {
       if (lane == 0) report(p.status, kDevTimeout, kSiteWeightLoad, 0u, 11u);
       *abort_flag = 1;
     }
-  } else if (warp == 9) {
+  } else if (warp == W0 + 1) {
     // ---------------------------------------------------------- MMA issuer
     if (elect_one()) {
       Cursor<NK> kc;
@@ -549,14 +578,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
     }
   } else {
     // ---------------------------------------------------- weights and sums
-    const int kt = warp >> 2, quarter = warp & 3;
-    const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16) + kt * NB * QN;
+    constexpr int NC = QN / CG;  // columns of a thread
+    const int kt = warp / (4 * CG), cg = (warp >> 2) % CG, quarter = warp & 3;
+    const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16) + kt * NB * QN + cg * NC;
     const uint64_t sc2 = f2(p.scale2, p.scale2);
     const int mine = kt * kKeys + quarter * 32 + lane;  // key of the block
     Cursor<NB> sc;
-    Cursor<kLseSlots> lc;
+    Cursor<LS> lc;
     bool ok = true;
-    int at = 0;
+    int at = 0, items = 0;
     Sum sum;
     WeightRec rec{0, 0, 0};
     bool begun = false;  // the item's first unit is this CTA's
@@ -568,72 +598,84 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
         item_end = g.end;
       }
       const int key = g.kb * kWeightKeys + mine;
-      // tokens [see0, see1) of the sequence see this key
       const int pos = g.kv - g.n;
-      int see0 = p.right < 0 ? 0 : max(0, key - p.right - pos);
-      int see1 = p.left < 0 ? g.n : min(g.n, key + p.left - pos + 1);
-      if (key >= g.kv) see1 = 0;
+      // Tiles [full0, full1) of the segment whose tokens all see all keys of this
+      // warp need no mask.
+      const int w1 = key - lane + 31;  // its last key
+      const int f0 = (p.right < 0 ? 0 : max(0, w1 - p.right - pos)) - g.t0 * p.step;
+      const int f1 = w1 >= g.kv || p.step * p.group != QN
+                         ? 0
+                         : (p.left < 0 ? g.n : min(g.n, w1 - 31 + p.left - pos + 1)) - g.t0 * p.step;
+      const int full0 = f0 <= 0 ? 0 : (unsigned)(f0 + p.step - 1) / (unsigned)p.step;
+      const int full1 = f1 <= 0 ? 0 : (unsigned)f1 / (unsigned)p.step;
+      const bool none = key - lane >= g.kv;  // no keys of this warp
       for (int t = 0; t < g.tiles; ++t) {
-        const int i0 = (g.t0 + t) * p.step;
-        const int live = min(p.step, g.n - i0) * p.group;
-        // columns [rl, rh) see the key
-        const int rl = max(0, see0 - i0) * p.group;
-        const int rh = max(rl, min(live, (see1 - i0) * p.group));
-        bool here = mbar_wait(&s_full[sc.st], sc.ph, abort_flag);
-        here = here && mbar_wait(&l_full[lc.st], lc.ph, abort_flag);
+        const bool here = mbar_wait(&s_full[sc.st], sc.ph, abort_flag);
         ok = __all_sync(0xffffffffu, here);
         if (!ok) break;
         tc_fence_after();
-        const float* ls = lse[lc.st];
-        uint64_t acc[2] = {0, 0};
-        constexpr int W = QN == 16 ? 16 : 32;
-        auto block = [&](const float* s, int c) {  // columns [c, c + W)
-          const bool all = __all_sync(0xffffffffu, rl <= c && rh >= c + W);
-#pragma unroll
-          for (int e = 0; e < W; e += 4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(ls + c + e);
-            const float2 x = unf2(fma2(f2(s[e], s[e + 1]), sc2, f2(l4.x, l4.y)));
-            const float2 y = unf2(fma2(f2(s[e + 2], s[e + 3]), sc2, f2(l4.z, l4.w)));
-            float v[4] = {exp2_fast(x.x), exp2_fast(x.y), exp2_fast(y.x), exp2_fast(y.y)};
-            if (!all) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if ((unsigned)(c + e + i - rl) >= (unsigned)(rh - rl)) v[i] = 0.f;
-            }
-            acc[0] = add2(acc[0], f2(v[0], v[1]));
-            acc[1] = add2(acc[1], f2(v[2], v[3]));
-          }
-        };
-        if (__any_sync(0xffffffffu, rl < rh)) {
-          if constexpr (QN == 16) {
-            float s[16];
-            tmem_ld16(ts + sc.st * QN, s);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[sc.st]);
-            block(s, 0);
-          } else {
-            const int halves = (live + 63) >> 6;
-            for (int hf = 0; hf < halves; ++hf) {
-              float s[64];
-              tmem_load64(ts + sc.st * QN + hf * 64, s);
-              if (hf == halves - 1) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s_empty[sc.st]);
-              }
-              block(s, hf * 64);
-              block(s + 32, hf * 64 + 32);
-            }
-          }
-        } else {
+        constexpr int W = NC < 32 ? NC : 32;  // columns at a time: 64 would spill
+        const float* ls = lse[lc.st] + cg * NC;
+        uint64_t acc[4] = {0, 0, 0, 0};
+        auto taken = [&] {  // the scores have been read
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_empty[sc.st]);
+        };
+        auto load = [&](int c, float (&s)[W]) {
+          if constexpr (W == 16) tmem_ld16(ts + sc.st * QN, s);
+          else tmem_load32(ts + sc.st * QN + c, s);
+          if (c + W == NC) taken();
+        };
+        auto weigh = [&](float (&s)[W], int c) {
+#pragma unroll
+          for (int e = 0; e < W; e += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(ls + c + e);
+            const float2 x = unf2(fma2(f2(s[e], s[e + 1]), sc2, f2(l.x, l.y)));
+            const float2 y = unf2(fma2(f2(s[e + 2], s[e + 3]), sc2, f2(l.z, l.w)));
+            s[e] = exp2_fast(x.x);
+            s[e + 1] = exp2_fast(x.y);
+            s[e + 2] = exp2_fast(y.x);
+            s[e + 3] = exp2_fast(y.y);
+          }
+        };
+        auto gather = [&](const float (&s)[W]) {
+#pragma unroll
+          for (int e = 0; e < W; e += 2)
+            acc[e / 2 & 3] = add2(acc[e / 2 & 3], f2(s[e], s[e + 1]));
+        };
+        // two loops: the mask must not cost where every row sees every key
+        if (none) {
+          taken();
+        } else if (t >= full0 && t < full1) {
+#pragma unroll
+          for (int c = 0; c < NC; c += W) {
+            float s[W];
+            load(c, s);
+            weigh(s, c);
+            gather(s);
+          }
+        } else {
+          // tokens [see0, see1) of the sequence see this key, of this thread's
+          // columns those from rl to rh
+          const int i0 = (g.t0 + t) * p.step;
+          const int see0 = p.right < 0 ? 0 : key - p.right - pos;
+          const int see1 = key >= g.kv ? 0 : (p.left < 0 ? g.n : key + p.left - pos + 1);
+          const int rl = max(0, see0 - i0) * p.group - cg * NC;
+          const int rh = min(min(p.step, g.n - i0) * p.group, (see1 - i0) * p.group) - cg * NC;
+#pragma unroll
+          for (int c = 0; c < NC; c += W) {
+            float s[W];
+            load(c, s);
+            if (!__any_sync(0xffffffffu, rl < rh && rh > c && rl < c + W)) continue;
+            weigh(s, c);
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+              if (c + e < rl || c + e >= rh) s[e] = 0.f;
+            gather(s);
+          }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&l_empty[lc.st]);
-        const float2 x = unf2(add2(acc[0], acc[1]));
+        const float2 x = unf2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])));
         sum.add(x.x + x.y);
         sc.next();
         lc.next();
@@ -641,6 +683,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       }
       if (!ok) break;
       if (!g.ends) continue;
+      if (CG == 2) {  // the second group's sums go to the first
+        const uint32_t ph = (uint32_t)items++ & 1u;
+        const bool here = cg == 1 ? mbar_wait(&x_empty[kt], ph ^ 1u, abort_flag)
+                                  : mbar_wait(&x_full[kt], ph, abort_flag);
+        ok = __all_sync(0xffffffffu, here);
+        if (!ok) break;
+        if (cg == 1) xch[CG == 2 ? mine : 0] = sum.value();
+        else sum.add(xch[CG == 2 ? mine : 0]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(cg == 1 ? &x_full[kt] : &x_empty[kt]);
+        if (cg == 1) continue;
+      }
       if (begun && g.last) {
         write_weight(p, g.b, g.n, g.kv, key, sum.value());
       } else {
@@ -661,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == W0 + 1) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmem);
@@ -710,7 +764,8 @@ cudaError_t prepare_dim() {
 template <int D, int QN>
 cudaError_t run(const WeightParams& p, bool fp16, int ctas, cudaStream_t s) {
   const cudaError_t e = launch_pdl(fp16 ? k_weights<D, QN, true> : k_weights<D, QN, false>,
-                                   dim3(ctas), dim3(kThreads), Cfg<D, QN>::kSmem, s, p);
+                                   dim3(ctas), dim3(Cfg<D, QN>::kThreads),
+                                   Cfg<D, QN>::kSmem, s, p);
   return e != cudaSuccess ? e : launch_pdl(k_weights_join, dim3(ctas), dim3(kWeightKeys), 0, s, p);
 }
 template <int QN>
