@@ -1,6 +1,8 @@
 // Bookkeeping of forked and thinned sequences (include/dg_attn.h): the pages
 // that the sequences of a group have in common, and the choice of the tokens
 // that stay when a cache is thinned.
+#include <algorithm>
+
 #include "../../include/dg_attn.h"
 #include "dg_attn_host.h"
 #include "dg_common.cuh"
@@ -36,6 +38,12 @@ __device__ __forceinline__ int peer_int(const int* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
+}
+
+__device__ __forceinline__ void peer_add(int* p, uint32_t rank, int v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
 // Sums over the block; `warps` holds one entry a warp.  Ends with a barrier.
@@ -83,7 +91,7 @@ struct SharedParams {
 // columns of all members before the next ones, and none past the nearest
 // difference found.
 __global__ void __launch_bounds__(kThinThreads) k_kv_shared(const __grid_constant__ SharedParams p) {
-  __shared__ int warps[32], least, bad;
+  __shared__ int least, bad;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   if (tid == 0) {
@@ -187,9 +195,10 @@ __device__ __forceinline__ int digit_bits(int d) { return d == 2 ? 10 : 11; }
 // of the row, keeps it in shared memory, and adds up the others' histograms
 // through distributed shared memory.
 template <bool CACHED>
-__global__ void __launch_bounds__(kThinThreads) k_kv_select(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_constant__ SelectParams p) {
   extern __shared__ float kept[];
-  __shared__ int hist[kBins], warps[32], found[3], counts[2];
+  __shared__ int hist[kBins], warps[32], found[2], counts[2];
+  __shared__ int sums[kDigits][kBins];  // of the cluster, in its first CTA
   const dg_kv_select_t& q = p.s;
   const int tid = threadIdx.x;
   const int ctas = (int)cluster_ctas(), rank = (int)cluster_rank();
@@ -249,6 +258,10 @@ __global__ void __launch_bounds__(kThinThreads) k_kv_select(const __grid_constan
     for (int i = tid; i < n; i += kThinThreads) kept[i] = __ldg(src + i);
   }
   auto weight = [&](int i) { return CACHED ? kept[i] : __ldg(src + i); };
+  if (ctas > 1) {
+    for (int i = tid; i < kDigits * kBins; i += kThinThreads) sums[0][i] = 0;
+    cluster_sync();
+  }
   uint32_t top = 0;        // the digits found so far
   int above = 0, equal = 0;  // of this slice: larger than the m-th largest, equal to it
   for (int d = 0; d < kDigits; ++d) {
@@ -260,17 +273,18 @@ __global__ void __launch_bounds__(kThinThreads) k_kv_select(const __grid_constan
       const uint32_t u = order_of(weight(i));
       if (d == 0 || u >> (shift + bits) == top) atomicAdd(&hist[u >> shift & ((1u << bits) - 1)], 1);
     }
-    if (ctas > 1) cluster_sync();
-    else __syncthreads();
-    // bins from the largest down, two a thread
+    __syncthreads();
+    // bins from the largest down, two a thread; all CTAs' in the first one's sums
     const int b0 = kBins - 1 - 2 * tid, b1 = b0 - 1;
     const int own0 = hist[b0], own1 = hist[b1];
     int all0 = own0, all1 = own1;
-    for (int r = 0; r < ctas; ++r)
-      if (r != rank) {
-        all0 += peer_int(&hist[b0], r);
-        all1 += peer_int(&hist[b1], r);
-      }
+    if (ctas > 1) {
+      if (own0) peer_add(&sums[d][b0], 0, own0);
+      if (own1) peer_add(&sums[d][b1], 0, own1);
+      cluster_sync();
+      all0 = peer_int(&sums[d][b0], 0);
+      all1 = peer_int(&sums[d][b1], 0);
+    }
     int total;
     const int over = block_before(all0 + all1, warps, &total);
     if (over < m && over + all0 + all1 >= m) {
@@ -286,9 +300,7 @@ __global__ void __launch_bounds__(kThinThreads) k_kv_select(const __grid_constan
     above += block_sum(higher, warps);
     equal = hist[bin];
     top = top << bits | (uint32_t)bin;
-    // no CTA clears its histogram while another one reads it
-    if (ctas > 1) cluster_sync();
-    else __syncthreads();
+    __syncthreads();
   }
   // tokens kept of the slices before this one
   int gt = 0, eq = 0;
@@ -336,13 +348,13 @@ __global__ void __launch_bounds__(kThinThreads) k_kv_select(const __grid_constan
   if (ctas > 1) cluster_sync();
 }
 
-// Weights that a CTA holds in shared memory at most: two CTAs an SM.
-constexpr int kSliceMost = 24 * 1024;
+// Weights that a CTA holds in shared memory at most.
+constexpr int kSliceMost = 48 * 1024;
 
+// CTAs of a sequence: as many as the SMs have room for at once, none with fewer
+// than 2048 weights.
 int select_ctas(int n_seqs, int width, int sms) {
-  int c = 1;
-  while (c < 8 && width > c * 4096 && n_seqs * c < 2 * sms) c *= 2;
-  return c;
+  return std::max(1, std::min({8, sms / n_seqs, (width + 2047) / 2048}));
 }
 
 }  // namespace
@@ -421,7 +433,7 @@ dg_status_t dg_kv_select(dg_kv_t* kv, const dg_kv_select_t* q, dg_stream_t strea
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   cudaError_t e = cudaSuccess;
-  if (cfg.dynamicSmemBytes > 32 * 1024)  // beside 9 KB of static shared memory
+  if (cfg.dynamicSmemBytes > 8 * 1024)  // beside 33 KB of static shared memory
     e = cudaFuncSetAttribute(k_kv_select<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)sizeof(float) * kSliceMost);
   if (e == cudaSuccess)
