@@ -173,10 +173,16 @@ struct SelectParams {
 
 // An unsigned order of the weights: NaN above everything, -0 as 0.
 __device__ __forceinline__ uint32_t order_of(float w) {
-  if (w != w) return 0xffffffffu;
+  if (w != w) return 0xffffffffu;  // kOrderNan
   const uint32_t u = __float_as_uint(w + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+
+// The weight of an order, but for NaN and the two zeros.
+__device__ __forceinline__ float weight_of(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+constexpr uint32_t kOrderNan = 0xffffffffu, kOrderZero = 0x80000000u;
 
 // Digits of the order, from the top: 11, 11 and 10 bits.
 constexpr int kDigits = 3;
@@ -196,7 +202,7 @@ __device__ __forceinline__ int digit_bits(int d) { return d == 2 ? 10 : 11; }
 // through distributed shared memory.
 template <bool CACHED>
 __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_constant__ SelectParams p) {
-  extern __shared__ float kept[];
+  extern __shared__ uint32_t kept[];  // orders of the slice
   __shared__ int hist[kBins], warps[32], found[2], counts[2];
   __shared__ int sums[kDigits][kBins];  // of the cluster, in its first CTA
   const dg_kv_select_t& q = p.s;
@@ -253,11 +259,7 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_cons
   const int mid = L - q.first - q.last, each = (mid + ctas - 1) / ctas;
   const int lo = min(rank * each, mid), n = min(each, mid - lo);
   const float* src = row + q.first + lo;
-  if (CACHED) {
-#pragma unroll 8
-    for (int i = tid; i < n; i += kThinThreads) kept[i] = __ldg(src + i);
-  }
-  auto weight = [&](int i) { return CACHED ? kept[i] : __ldg(src + i); };
+  auto order = [&](int i) { return CACHED ? kept[i] : order_of(__ldg(src + i)); };
   if (ctas > 1) {
     for (int i = tid; i < kDigits * kBins; i += kThinThreads) sums[0][i] = 0;
     cluster_sync();
@@ -268,10 +270,19 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_cons
     const int shift = digit_shift(d), bits = digit_bits(d);
     for (int i = tid; i < kBins; i += kThinThreads) hist[i] = 0;
     __syncthreads();
-#pragma unroll 4
-    for (int i = tid; i < n; i += kThinThreads) {
-      const uint32_t u = order_of(weight(i));
-      if (d == 0 || u >> (shift + bits) == top) atomicAdd(&hist[u >> shift & ((1u << bits) - 1)], 1);
+    if (d == 0) {
+#pragma unroll 8
+      for (int i = tid; i < n; i += kThinThreads) {
+        const uint32_t u = order_of(__ldg(src + i));
+        if (CACHED) kept[i] = u;
+        atomicAdd(&hist[u >> shift], 1);
+      }
+    } else {
+#pragma unroll 8
+      for (int i = tid; i < n; i += kThinThreads) {
+        const uint32_t u = order(i);
+        if (u >> (shift + bits) == top) atomicAdd(&hist[u >> shift & ((1u << bits) - 1)], 1);
+      }
     }
     __syncthreads();
     // bins from the largest down, two a thread; all CTAs' in the first one's sums
@@ -315,34 +326,38 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_cons
       eq += peer_int(&counts[1], r);
     }
   }
-  constexpr int kEach = 4;
-  for (int t0 = 0; t0 < n; t0 += kEach * kThinThreads) {
-    const int i0 = t0 + kEach * tid;
-    float w[kEach];
-    int sum = 0;  // larger ones; equal ones in the high half
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      w[k] = i0 + k < n ? weight(i0 + k) : 0.f;
-      const uint32_t u = order_of(w[k]);
-      sum += i0 + k < n ? (u > top ? 1 : u == top ? 1 << 16 : 0) : 0;
+  // A warp takes a run of rows of 32 places; first what it will keep, then where.
+  const int lane = tid & 31, run = ((n + kThinThreads - 1) / kThinThreads) * 32;
+  const int i0 = min((tid >> 5) * run, n), i1 = min(i0 + run, n);
+  int g_own = 0, e_own = 0;
+#pragma unroll 8
+  for (int i = i0 + lane; i < i1; i += 32) {
+    const uint32_t u = order(i);
+    g_own += u > top;
+    e_own += u == top;
+  }
+  int total;
+  gt += block_before(g_own, warps, &total);
+  eq += block_before(e_own, warps, &total);
+  // (the lanes' counts lie between a warp's first lane and its own)
+  gt = __shfl_sync(kAllLanes, gt, 0);
+  eq = __shfl_sync(kAllLanes, eq, 0);
+  const unsigned below = (1u << lane) - 1;
+#pragma unroll 4
+  for (int i = i0; i < i1; i += 32) {
+    const bool in = i + lane < i1;
+    const uint32_t u = in ? order(i + lane) : 0u;
+    const unsigned larger = __ballot_sync(kAllLanes, in && u > top);
+    const unsigned same = __ballot_sync(kAllLanes, in && u == top);
+    const int e = eq + __popc(same & below);
+    if ((larger >> lane & 1u) || ((same >> lane & 1u) && e < m)) {
+      const int to = q.first + gt + __popc(larger & below) + min(e, m);
+      keep[to] = q.first + lo + i + lane;
+      // (fetched again only where the order does not say: the store would wait for it)
+      out[to] = u == kOrderNan || u == kOrderZero ? __ldg(src + i + lane) : weight_of(u);
     }
-    int total;
-    const int off = block_before(sum, warps, &total);
-    int g = gt + (off & 0xffff), e = eq + (off >> 16);
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      if (i0 + k >= n) break;
-      const uint32_t u = order_of(w[k]);
-      if (u > top || (u == top && e < m)) {
-        const int to = q.first + g + min(e, m);
-        keep[to] = q.first + lo + i0 + k;
-        out[to] = w[k];
-      }
-      g += u > top;
-      e += u == top;
-    }
-    gt += total & 0xffff;
-    eq += total >> 16;
+    gt += __popc(larger);
+    eq += __popc(same);
   }
   // another CTA may still read this one's counts
   if (ctas > 1) cluster_sync();
