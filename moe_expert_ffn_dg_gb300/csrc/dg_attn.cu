@@ -247,13 +247,15 @@ __device__ __forceinline__ void check_seq(const AttnParams& p, int b) {
 }
 
 // Attention that reads a prefix once for all sequences that share it, in two
-// launches.  In the first a "sequence" is a group: its rows are the new tokens of
-// all of its members, its keys the prefix, all of which every row sees.  Its
-// results stay as they are, fp32 and with their (m, l), in `pre`.  In the second
-// every sequence attends to what lies behind its prefix and takes the first
-// one's result in as one more part.  Rows of one key/value head lie together in
-// `pre`, in the order in which tiles hold them, four columns of all rows at a
-// time, so that a warp's accesses are contiguous.
+// launches.  In the first every sequence attends to what lies behind its prefix;
+// where there is one, its results stay as they are, fp32 and with their (m, l), in
+// `pre`.  In the second a "sequence" is a group: its rows are the new tokens of all
+// of its members, its keys the prefix, all of which every row sees; the first
+// one's results are taken in as one more part.  (The other way round each of the
+// many short items of the sequences would end in that, and take 13 us more in 40
+// for 64 samples of one prompt.)  Rows of one key/value head lie together in `pre`,
+// in the order in which tiles hold them, four columns of all rows at a time, so
+// that a warp's accesses are contiguous.
 struct PreParams : AttnParams {
   float4* pre;    // [D / 4][kv_heads * n_tokens * group]
   float2* pre_ml;
@@ -289,7 +291,7 @@ __device__ __forceinline__ Seq load_seq(const PrefixParams& p, int g) {
   s.n = s.kv > 0 ? max(min(e, p.n_tokens) - s.n0, 0) : 0;
   return s;
 }
-__device__ __forceinline__ void check_seq(const PrefixParams&, int) {}  // in the second launch
+__device__ __forceinline__ void check_seq(const PrefixParams&, int) {}  // the first launch did
 
 __device__ __forceinline__ Seq load_seq(const SuffixParams& p, int b) {
   Seq s = load_seq(static_cast<const AttnParams&>(p), b);
@@ -1152,7 +1154,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         float own = 1.f, pre_f = 0.f;
         if constexpr (PREFIX || SUFFIX) {
           pre_at = p.pre_row(g.head, g.tok0 + i * p.step + tok, gh);
-          if (SUFFIX && whole && row_live && g.klo > 0) {
+          if (PREFIX && whole && row_live) {
             const float2 q = p.pre_ml[pre_at];
             pre = !(q.y == 0.f);  // one that saw nothing holds nothing
             if (pre) {
@@ -1181,7 +1183,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             for (int e = 0; e < 32; ++e) o[e] = 0.f;
           }
           if (!row_live) continue;
-          if constexpr (SUFFIX) {
+          if constexpr (PREFIX) {
             if (pre) {
               const float4* src = p.pre + (size_t)((o0 + c) / 4) * p.pre_rows() + pre_at;
 #pragma unroll
@@ -1194,8 +1196,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
               }
             }
           }
-          if (PREFIX && whole) {
-            if constexpr (PREFIX) {
+          if (SUFFIX && whole && g.klo > 0) {
+            if constexpr (SUFFIX) {
               float4* dst = p.pre + (size_t)((o0 + c) / 4) * p.pre_rows() + pre_at;
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
@@ -1227,9 +1229,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         if (row_live && (NQ == 2 || wg == 0)) {
           if (!whole)
             p.ml[prow] = make_float2(m, l);
-          else if constexpr (PREFIX)
-            p.pre_ml[pre_at] = make_float2(m, l);
-          else if (p.lse)
+          else if (SUFFIX && g.klo > 0) {
+            if constexpr (SUFFIX) p.pre_ml[pre_at] = make_float2(m, l);
+          } else if (p.lse)
             p.lse[(size_t)trow * (p.kv_heads * p.group) + head] =
                 l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
         }
@@ -1299,6 +1301,15 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ P p) 
     const int tok = vr / p.group, gh = vr - tok * p.group;
     const int i = tok / p.step;
     const int row = i * kRows + (tok - i * p.step) * p.group + gh;
+    const int trow = rec.tok0 + tok, head = rec.head * p.group + gh;
+    float2 pre_ml;  // the first launch's part
+    float4 pre_lo, pre_hi;
+    if constexpr (PREFIX) {
+      const size_t at = p.pre_row(rec.head, trow, gh);
+      pre_ml = p.pre_ml[at];
+      pre_lo = p.pre[2 * c * p.pre_rows() + at];
+      pre_hi = p.pre[(2 * c + 1) * p.pre_rows() + at];
+    }
     float m = -INFINITY, l = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int k0 = 0; k0 < rec.parts; k0 += BATCH) {
       float4 v[BATCH][2];
@@ -1341,29 +1352,25 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ P p) 
           acc[7] += f * v[k][1].w;
         }
     }
-    const int trow = rec.tok0 + tok, head = rec.head * p.group + gh;
-    if constexpr (PREFIX) {
-      const size_t at = p.pre_row(rec.head, trow, gh);
-      p.pre[2 * c * p.pre_rows() + at] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      p.pre[(2 * c + 1) * p.pre_rows() + at] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-      if (c == 0) p.pre_ml[at] = make_float2(m, l);
-      continue;
-    }
     if constexpr (SUFFIX) {
       if (rec.shared) {
         const size_t at = p.pre_row(rec.head, trow, gh);
-        const float2 q = p.pre_ml[at];
-        const float4 x = p.pre[2 * c * p.pre_rows() + at];
-        const float4 y = p.pre[(2 * c + 1) * p.pre_rows() + at];
-        if (!(q.y == 0.f)) {
-          const float top = fmaxf(m, q.x), f = exp2f(q.x - top);
-          const float own = l == 0.f ? 0.f : exp2f(m - top);  // (acc is 0 with l)
-          const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-          l = own * l + f * q.y;
+        p.pre[2 * c * p.pre_rows() + at] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        p.pre[(2 * c + 1) * p.pre_rows() + at] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (c == 0) p.pre_ml[at] = make_float2(m, l);
+        continue;
+      }
+    }
+    if constexpr (PREFIX) {
+      if (!(pre_ml.y == 0.f)) {
+        const float top = fmaxf(m, pre_ml.x), f = exp2f(pre_ml.x - top);
+        const float own = l == 0.f ? 0.f : exp2f(m - top);  // (acc is 0 with l)
+        const float z[8] = {pre_lo.x, pre_lo.y, pre_lo.z, pre_lo.w,
+                            pre_hi.x, pre_hi.y, pre_hi.z, pre_hi.w};
+        l = own * l + f * pre_ml.y;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] = own * acc[e] + f * z[e];
-          m = top;
-        }
+        for (int e = 0; e < 8; ++e) acc[e] = own * acc[e] + f * z[e];
+        m = top;
       }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1419,8 +1426,12 @@ struct Variant {
     else
       e = cudaLaunchKernelEx(&cfg, m ? many_of<P> : few_of<P>, p);
     if (e != cudaSuccess) return e;
-    // few rows are split into many parts, many rows into two or three
-    if constexpr (!kSuffix) {
+    // few rows are split into many parts, many rows into two or three, but a
+    // prefix's into many again
+    if constexpr (std::is_same<P, PrefixParams>::value) {
+      if (m)
+        return launch_pdl(k_attn_join<D, kManyNq, 8, FP16, P>, dim3(ctas, 16), dim3(256), 0, s, p);
+    } else if constexpr (!kSuffix) {
       if (m && kManyNq == 2)
         return launch_pdl(k_attn_join<D, kManyNq, 2, FP16, P>, dim3(ctas, 8), dim3(256), 0, s, p);
       if (m) return launch_pdl(k_attn_join<D, 1, 2, FP16, P>, dim3(ctas, 8), dim3(256), 0, s, p);
@@ -1690,20 +1701,20 @@ dg_status_t dg_attn_forward_shared(dg_attn_t* a, int layer, const dg_heads_t* q,
     p.groups = shared->groups;
     p.n_real = batch->n_seqs;
   };
-  PrefixParams first;
-  st = set_up(a, layer, q, out, lse, batch, n_tokens,
-              (int64_t)n_tokens * group / shared->n_groups, first, &many);
-  if (st != DG_OK) return st;
-  with(first);
-  first.n_seqs = shared->n_groups;
-  first.left = first.right = -1;
-  SuffixParams second;
+  SuffixParams own;
   bool unused;
-  st = set_up(a, layer, q, out, lse, batch, n_tokens, 1, second, &unused);
+  st = set_up(a, layer, q, out, lse, batch, n_tokens, 1, own, &unused);
   if (st != DG_OK) return st;
-  with(second);
-  st = run_call(a, many, first, stream);
-  return st != DG_OK ? st : run_call(a, false, second, stream);
+  with(own);
+  PrefixParams prefix;
+  st = set_up(a, layer, q, out, lse, batch, n_tokens,
+              (int64_t)n_tokens * group / shared->n_groups, prefix, &many);
+  if (st != DG_OK) return st;
+  with(prefix);
+  prefix.n_seqs = shared->n_groups;
+  prefix.left = prefix.right = -1;
+  st = run_call(a, false, own, stream);
+  return st != DG_OK ? st : run_call(a, many, prefix, stream);
 }
 
 dg_status_t dg_attn_last_device_status(dg_attn_t* a, dg_stream_t stream, unsigned int* where,

@@ -95,7 +95,7 @@ constexpr int kWeightKeys = 2 * kKeys;  // keys of a weights item
 struct JoinRec {
   int parts;  // 0: none
   int head, tok0, ntok;
-  int shared;  // a shared prefix's part is to be joined too
+  int shared;  // its sequence shares a prefix, whose part is still to come
 };
 struct WeightRec {
   int parts;  // 0: none
