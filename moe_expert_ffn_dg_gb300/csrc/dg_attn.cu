@@ -397,6 +397,28 @@ __host__ __device__ constexpr int key_shift_max(int d, bool pair) {
 }
 __host__ __device__ constexpr int value_shift_max(int d) { return d == 128 ? 7 : 6; }
 
+// umma_ss with A in tensor memory.
+template <bool PAIR>
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                        uint32_t idesc, int accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+        : "memory");
+}
+
 // Arrive, when this thread's MMAs so far are done, on `bar` of this CTA, or of
 // both CTAs of a pair.
 template <bool PAIR>
@@ -573,8 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
   volatile int* abort_flag = &abort_word;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_trigger();
+  if constexpr (!SUFFIX) pdl_trigger();
   if (ring & 1023u) {  // the swizzle needs it; the declaration asks for it
+    if constexpr (PREFIX) pdl_wait();
     if (tid == 0) report(p.status, kDevBounds, kSiteAttnLoad, ring, 0u);
     return;
   }
@@ -620,7 +643,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
       tmem_relinquish();
     }
   }
-  pdl_wait();
+  // The launch over the prefixes runs beside the one before it (the sequences' own
+  // parts) and its join, and waits for them where it takes their results in.  What
+  // came before those is done: the first lets others begin only once it is.
+  if constexpr (!PREFIX) pdl_wait();
+  if constexpr (SUFFIX) pdl_trigger();
   tc_fence_before();
   find_start<NQ>(p, reinterpret_cast<long long*>(smem), &start);
   tc_fence_after();
@@ -1154,6 +1181,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
         float own = 1.f, pre_f = 0.f;
         if constexpr (PREFIX || SUFFIX) {
           pre_at = p.pre_row(g.head, g.tok0 + i * p.step + tok, gh);
+          if (PREFIX && whole) pdl_wait();
           if (PREFIX && whole && row_live) {
             const float2 q = p.pre_ml[pre_at];
             pre = !(q.y == 0.f);  // one that saw nothing holds nothing
@@ -1259,6 +1287,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
     if (tid == 0) p.rec[blockIdx.x] = ok ? rec : JoinRec{0, 0, 0, 0, 0};
   }
 
+  if constexpr (PREFIX) pdl_wait();  // completion stays transitive
   tc_fence_before();
   __syncthreads();
   if (PAIR) {  // the first CTA has waited for the pair's products
@@ -1429,14 +1458,16 @@ struct Variant {
     // few rows are split into many parts, many rows into two or three, but a
     // prefix's into many again
     if constexpr (std::is_same<P, PrefixParams>::value) {
-      if (m)
+      if (m && kManyNq == 2)
         return launch_pdl(k_attn_join<D, kManyNq, 8, FP16, P>, dim3(ctas, 16), dim3(256), 0, s, p);
+      return launch_pdl(k_attn_join<D, 1, 8, FP16, P>, dim3(ctas, 16), dim3(256), 0, s, p);
     } else if constexpr (!kSuffix) {
       if (m && kManyNq == 2)
         return launch_pdl(k_attn_join<D, kManyNq, 2, FP16, P>, dim3(ctas, 8), dim3(256), 0, s, p);
       if (m) return launch_pdl(k_attn_join<D, 1, 2, FP16, P>, dim3(ctas, 8), dim3(256), 0, s, p);
     }
-    return launch_pdl(k_attn_join<D, 1, 8, FP16, P>, dim3(ctas), dim3(256), 0, s, p);
+    if constexpr (!std::is_same<P, PrefixParams>::value)
+      return launch_pdl(k_attn_join<D, 1, 8, FP16, P>, dim3(ctas), dim3(256), 0, s, p);
   }
   template <class K>
   static cudaError_t limit(K kernel, size_t smem) {
@@ -1474,16 +1505,27 @@ dg_status_t run_call(const dg_attn* a, bool many, const P& p, dg_stream_t stream
   return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 
-// Results of the shared prefixes: fp32 rows, and their (m, l).
+// Workspace of a call with shared prefixes: results of the sequences' own parts
+// (fp32 rows, and their (m, l)), and a place for that launch's partial results, which
+// runs beside the one over the prefixes.
 struct PreLayout {
-  size_t o, ml, total;
+  size_t o, ml, rec, part_ml, part, total;
 };
 PreLayout pre_layout(const dg_attn_config_t& a, const dg_kv_config_t& c, int n_tokens) {
   const size_t rows = (size_t)n_tokens * a.n_q_heads;
   PreLayout L;
-  L.o = 0;
-  L.ml = round_up(rows * c.head_dim * sizeof(float), 256);
-  L.total = L.ml + rows * sizeof(float2);
+  size_t at = 0;
+  L.o = at;
+  at = round_up(at + rows * c.head_dim * sizeof(float), 256);
+  L.ml = at;
+  at = round_up(at + rows * sizeof(float2), 256);
+  L.rec = at;
+  at = round_up(at + sizeof(JoinRec) * kMaxCtas, 256);
+  L.part_ml = at;
+  at = round_up(at + 2 * kMaxCtas * kRows * sizeof(float2), 256);
+  L.part = at;
+  at += 2 * kMaxCtas * kRows * c.head_dim * sizeof(float);
+  L.total = at;
   return L;
 }
 
@@ -1691,7 +1733,15 @@ dg_status_t dg_attn_forward_shared(dg_attn_t* a, int layer, const dg_heads_t* q,
     return DG_ERR_WORKSPACE;
   const int group = a->cfg.n_q_heads / c.n_kv_heads;
   const int64_t rows = (int64_t)n_tokens * group / batch->n_seqs;
-  if (shared->n_groups == 0 || a->cfg.left >= 0 || rows > kMaxSharedRows)
+  // One by one: with many rows a sequence the keys are read once for all of them
+  // anyway; and where all that the sequences can hold is little, a second launch
+  // costs more than reading a prefix again, mostly from the L2 (2 to 32 sequences,
+  // one token each, us one by one / together: at 140 to 170 MB 24 / 29, 24 / 34, 44 /
+  // 47; at 270 to 300 MB 65 / 47, 34 / 31, 30 / 32; at 550 to 600 MB 60 / 55, 48 / 35).
+  const int64_t held = (int64_t)batch->n_seqs * batch->max_pages * c.page_size * c.n_kv_heads *
+                       c.head_dim * 4;
+  if (shared->n_groups == 0 || a->cfg.left >= 0 || rows > kMaxSharedRows ||
+      held <= ((int64_t)256 << 20))
     return dg_attn_forward(a, layer, q, out, lse, batch, n_tokens, stream);
   uint8_t* ws = static_cast<uint8_t*>(shared->workspace);
   auto with = [&](PreParams& p) {
@@ -1706,9 +1756,17 @@ dg_status_t dg_attn_forward_shared(dg_attn_t* a, int layer, const dg_heads_t* q,
   st = set_up(a, layer, q, out, lse, batch, n_tokens, 1, own, &unused);
   if (st != DG_OK) return st;
   with(own);
+  own.part = reinterpret_cast<float4*>(ws + L.part);
+  own.ml = reinterpret_cast<float2*>(ws + L.part_ml);
+  own.rec = reinterpret_cast<JoinRec*>(ws + L.rec);
+  // A prefix's items are split into many parts, and parts of few rows cost less to
+  // write and join (behind 16384 tokens, us few / many: head size 64 39.6 / 40.4 at
+  // 256 rows, 58.6 / 56.3 at 512; 128: 45.7 / 51.8, 69.7 / 75.4, at 2048 rows behind
+  // 65536 643 / 392; 256: 58.8 / 66.8 at 128, 78.2 / 73.6 at 192).
   PrefixParams prefix;
+  const int64_t prefix_rows = (int64_t)n_tokens * group / shared->n_groups;
   st = set_up(a, layer, q, out, lse, batch, n_tokens,
-              (int64_t)n_tokens * group / shared->n_groups, prefix, &many);
+              prefix_rows > (c.head_dim == 256 ? 160 : 512) ? prefix_rows : 1, prefix, &many);
   if (st != DG_OK) return st;
   with(prefix);
   prefix.n_seqs = shared->n_groups;

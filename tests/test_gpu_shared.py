@@ -56,11 +56,21 @@ def make(groups, hq, hkv, d, ps, dtype, seed=0):
     return q, k, v, table, lens, cu, bounds
 
 
-def handles(data, left=-1, right=0, **kw):
+def widened(table, k):
+    """A page table with room for more than 256 MB of keys and values: below that
+    sequences are taken one by one."""
+    n, (_, ps, hkv, d) = table.shape[0], k.shape
+    room = (256 << 20) // (n * ps * hkv * d * 4) + 1
+    wide = torch.full((n, max(room, table.shape[1])), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    return wide
+
+
+def handles(data, left=-1, right=0, wide=True, **kw):
     import moe_expert_ffn_dg_gb300 as pkg
     q, k, v, table, lens, cu, bounds = data
     cache = pkg.KvCache(k[None].cuda(), v[None].cuda())
-    batch = pkg.KvBatch(table.cuda(), i32(lens), i32(cu))
+    batch = pkg.KvBatch((widened(table, k) if wide else table).cuda(), i32(lens), i32(cu))
     attn = pkg.PagedAttention(cache, q.shape[1], left=left, right=right,
                               shared_tokens=max(q.shape[0], 1), **kw)
     return attn, q.cuda(), batch, i32(bounds)
@@ -167,7 +177,7 @@ def test_what_is_not_seen_may_hold_anything():
     attn = pkg.PagedAttention(cache, 4, shared_tokens=8)
     wide = torch.full((8, 4, 64), math.nan, dtype=BF, device="cuda")
     wide[2:5] = q.cuda()
-    batch = pkg.KvBatch(table.cuda(), i32(lens), i32([c + 2 for c in cu]))
+    batch = pkg.KvBatch(widened(table, k).cuda(), i32(lens), i32([c + 2 for c in cu]))
     out, lse = torch.full_like(wide, 7.0), torch.full((8, 4), 7.0, device="cuda")
     attn.forward(wide, batch, out=out, lse=lse, shared=cache.shared(batch, i32(bounds)))
     assert attn.device_status()[0] == 0
@@ -210,6 +220,17 @@ def test_same_result_every_time_and_close_to_the_plain_call():
         assert torch.equal(attn.forward(q, batch, shared=shared), first)
     plain = attn.forward(q, batch)
     assert (plain.float() - first.float()).abs().max() <= 2 ** -6
+
+
+def test_little_is_taken_one_by_one():
+    """The same launches as without a plan, so the same bits; not so with room for
+    more."""
+    data = make([(2000, [(i + 1, 1) for i in range(20)])], 8, 2, 128, 64, BF, 11)
+    attn, q, batch, groups = handles(data, wide=False)
+    out = attn.forward(q, batch, shared=attn.cache.shared(batch, groups))
+    assert torch.equal(out, attn.forward(q, batch))
+    attn, q, batch, groups = handles(data)
+    assert not torch.equal(attn.forward(q, batch, shared=attn.cache.shared(batch, groups)), out)
 
 
 def test_captured_with_its_plan_and_replayed_on_new_lengths():
@@ -271,7 +292,7 @@ def test_bad_prefixes_and_pages_are_reported():
     compare(data, out, lse)
     table = data[3].clone()
     table[:, 2] = 1 << 20
-    bad = pkg.KvBatch(table.cuda(), batch.lens, batch.cu)
+    bad = pkg.KvBatch(widened(table, data[1]).cuda(), batch.lens, batch.cu)
     attn.forward(q, bad, shared=attn.cache.shared(bad, groups))
     assert attn.device_status()[0] == B.DG_ERR_DEVICE_CHECK
 
