@@ -162,10 +162,16 @@ class KvShared:
     same pages in all of a sequence's group.  It holds for the batch's tensors as
     they were then."""
 
-    __slots__ = ("batch", "groups", "prefix")
+    __slots__ = ("batch", "groups", "prefix", "c")
 
-    def __init__(self, batch, groups, prefix):
+    def __init__(self, batch: KvBatch, groups: torch.Tensor, prefix: torch.Tensor):
+        if groups.dim() != 1 or groups.shape[0] < 1:
+            raise ValueError("groups: [n_groups + 1]")
         self.batch, self.groups, self.prefix = batch, groups, prefix
+        n = groups.shape[0]
+        self.c = B.dg_attn_shared_t(_ints(groups, batch.device, (n,), "groups"),
+                                    _ints(prefix, batch.device, (batch.c.n_seqs,), "prefix"),
+                                    n - 1, None, 0)
 
 
 class KvKeep:
@@ -277,16 +283,20 @@ class KvCache(_Handle, _Memory):
             if stream is not None:  # allocated on the current one
                 for t in (out.keep, out.cu, out.lens, out.weights):
                     t.record_stream(stream)
-        elif out.weights.dim() != 2 or out.weights.shape[1] < most:
-            raise ValueError(f"out.weights: [n_seqs, {most}] or wider")
-        w_out, out_stride = _weights(out.weights, dev, n, "out.weights")
-        cu = _ints(out.cu, dev, (n + 1,), "out.cu")
+            outputs = (out.keep.data_ptr(), out.cu.data_ptr(), out.lens.data_ptr(),
+                       out.weights.data_ptr(), most)
+        else:
+            if out.weights.dim() != 2 or out.weights.shape[1] < most:
+                raise ValueError(f"out.weights: [n_seqs, {most}] or wider")
+            outputs = (_ints(out.keep, dev, (n * most,), "out.keep"),
+                       _ints(out.cu, dev, (n + 1,), "out.cu"),
+                       _ints(out.lens, dev, (n,), "out.lens"),
+                       *_weights(out.weights, dev, n, "out.weights"))
         if n == 0:
             out.cu.zero_()
         B.dg_kv_select(self.handle, B.dg_kv_select_t(
-            w, stride, _ints(lens, dev, (n,), "lens"), n, width, budget, first, last,
-            _ints(out.keep, dev, (n * most,), "out.keep"), cu,
-            _ints(out.lens, dev, (n,), "out.lens"), w_out, out_stride), self._use(stream))
+            w, stride, _ints(lens, dev, (n,), "lens"), n, width, budget, first, last, *outputs),
+            self._use(stream))
         return out
 
     def shared(self, batch: KvBatch, groups: torch.Tensor, out: KvShared = None,
@@ -295,18 +305,14 @@ class KvCache(_Handle, _Memory):
         [n_groups + 1], ascending) have in common, for every group: the tokens
         from the first on that lie in the same pages and that all of them had
         before this call's new ones.  For :meth:`PagedAttention.forward`."""
-        n = batch.lens.shape[0]
         if out is None:
-            out = KvShared(batch, groups, batch.lens.new_empty(n))
+            out = KvShared(batch, groups, batch.lens.new_empty(batch.c.n_seqs))
             if stream is not None:  # allocated on the current one
                 out.prefix.record_stream(stream)
-        else:
-            out.batch, out.groups = batch, groups
-        if groups.shape[0] < 1:
-            raise ValueError("groups: [n_groups + 1]")
-        B.dg_kv_shared(self.handle, self._batch(batch),
-                       _ints(groups, self.device, (groups.shape[0],), "groups"),
-                       groups.shape[0] - 1, _ints(out.prefix, self.device, (n,), "out.prefix"),
+        elif out.batch is not batch or out.groups is not groups:
+            raise ValueError("out: of this batch and these groups")
+        c = out.c
+        B.dg_kv_shared(self.handle, self._batch(batch), c.groups, c.n_groups, c.prefix,
                        self._use(stream))
         return out
 
@@ -434,11 +440,10 @@ class PagedAttention(_Handle, _Memory):
             if q.shape[0] > self.shared_tokens:
                 raise ValueError(f"{q.shape[0]} tokens with shared prefixes, room for "
                                  f"{self.shared_tokens} (shared_tokens)")
-            n = shared.groups.shape[0]
+            s = shared.c
             B.dg_attn_forward_shared(*args, B.dg_attn_shared_t(
-                _ints(shared.groups, c.device, (n,), "groups"),
-                _ints(shared.prefix, c.device, (batch.lens.shape[0],), "prefix"), n - 1,
-                self._pre, self._pre_bytes), q.shape[0], self._use(stream))
+                s.groups, s.prefix, s.n_groups, self._pre, self._pre_bytes), q.shape[0],
+                self._use(stream))
         return (out, lse) if lse is not None else out
 
     def weights(self, q: torch.Tensor, lse: torch.Tensor, batch: KvBatch, weights: torch.Tensor,

@@ -311,10 +311,10 @@ def test_refusals():
         small.forward(q, batch, shared=shared)
     with pytest.raises(ValueError):
         pkg.PagedAttention(attn.cache, 4).forward(q, batch, shared=shared)
-    with pytest.raises(ValueError):
-        attn.forward(q, batch, shared=pkg.KvShared(batch, groups, shared.prefix[:2]))
-    with pytest.raises(ValueError):
-        attn.forward(q, batch, shared=pkg.KvShared(batch, groups.long(), shared.prefix))
+    for a in ((groups, shared.prefix[:2]), (groups.long(), shared.prefix),
+              (groups.cpu(), shared.prefix), (groups[:0], shared.prefix)):
+        with pytest.raises(ValueError):
+            pkg.KvShared(batch, *a)
     lib = B.load_library()
     x = B.dg_heads_t(q.data_ptr(), 256, 64)
     o = torch.empty_like(q)

@@ -302,8 +302,10 @@ def test_shared_refusals_and_capture():
             cache.shared(batch, groups)
     groups = i32([0, 9])
     got = cache.shared(batch, groups)
-    with pytest.raises(ValueError):
-        cache.shared(batch, groups, out=pkg.KvShared(batch, groups, got.prefix[:4]))
+    for kw in (dict(groups=groups.clone(), batch=batch),
+               dict(groups=groups, batch=pkg.KvBatch(batch.page_table, batch.lens, batch.cu))):
+        with pytest.raises(ValueError):
+            cache.shared(out=got, **kw)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         cache.shared(batch, groups, out=got)
