@@ -187,6 +187,7 @@ constexpr uint32_t kOrderNan = 0xffffffffu, kOrderZero = 0x80000000u;
 // Digits of the order, from the top: 11, 11 and 10 bits.
 constexpr int kDigits = 3;
 constexpr int kBins = 2048;
+constexpr int kListed = 64;  // orders of a run that are listed at most
 __device__ __forceinline__ int digit_shift(int d) { return d == 0 ? 21 : d == 1 ? 10 : 0; }
 __device__ __forceinline__ int digit_bits(int d) { return d == 2 ? 10 : 11; }
 
@@ -202,9 +203,11 @@ __device__ __forceinline__ int digit_bits(int d) { return d == 2 ? 10 : 11; }
 // through distributed shared memory.
 template <bool CACHED>
 __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_constant__ SelectParams p) {
-  extern __shared__ uint32_t kept[];  // orders of the slice
-  __shared__ int hist[kBins], warps[32], found[2], counts[2];
+  extern __shared__ __align__(16) uint32_t kept[];  // orders of the slice
+  __shared__ int hist[kBins], warps[32], found[3], counts[2];
   __shared__ int sums[kDigits][kBins];  // of the cluster, in its first CTA
+  // of each run, the orders with the first digit of the m-th largest
+  __shared__ uint32_t lists[CACHED ? 32 : 1][CACHED ? kListed : 1];
   const dg_kv_select_t& q = p.s;
   const int tid = threadIdx.x;
   const int ctas = (int)cluster_ctas(), rank = (int)cluster_rank();
@@ -264,8 +267,14 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_cons
     for (int i = tid; i < kDigits * kBins; i += kThinThreads) sums[0][i] = 0;
     cluster_sync();
   }
-  uint32_t top = 0;        // the digits found so far
-  int above = 0, equal = 0;  // of this slice: larger than the m-th largest, equal to it
+  // A warp takes a run of rows of 128 places.
+  const int lane = tid & 31, warp = tid >> 5, run = (n + 32 * 128 - 1) / (32 * 128) * 128;
+  const int i0 = min(warp * run, n), i1 = min(i0 + run, n);
+  int g_own = 0, e_own = 0;  // of its run: kept for sure, equal to the m-th largest
+  bool few = false;          // those with the first digit are listed
+  int listed = 0;
+  uint32_t* mine = lists[CACHED ? warp : 0];
+  uint32_t top = 0;          // the digits found so far
   for (int d = 0; d < kDigits; ++d) {
     const int shift = digit_shift(d), bits = digit_bits(d);
     for (int i = tid; i < kBins; i += kThinThreads) hist[i] = 0;
@@ -276,6 +285,11 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_cons
         const uint32_t u = order_of(__ldg(src + i));
         if (CACHED) kept[i] = u;
         atomicAdd(&hist[u >> shift], 1);
+      }
+    } else if (few) {
+      for (int i = lane; i < listed; i += 32) {
+        const uint32_t u = mine[i];
+        if (u >> (shift + bits) == top) atomicAdd(&hist[u >> shift & ((1u << bits) - 1)], 1);
       }
     } else {
 #pragma unroll 8
@@ -302,20 +316,49 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_cons
       const bool second = over + all0 < m;
       found[0] = second ? b1 : b0;
       found[1] = m - over - (second ? all0 : 0);
+      found[2] = second ? all1 : all0;
     }
     __syncthreads();
-    const int bin = found[0];
     m = found[1];
-    // what of this slice lies in the bins above, and in the bin itself
-    const int higher = (b0 > bin ? own0 : 0) + (b1 > bin ? own1 : 0);
-    above += block_sum(higher, warps);
-    equal = hist[bin];
-    top = top << bits | (uint32_t)bin;
+    top = top << bits | (uint32_t)found[0];
     __syncthreads();
+    if (CACHED && d == 0) {  // list those with this digit, if they are few in every run
+#pragma unroll 8
+      for (int i = i0; i < i1; i += 32) {
+        const uint32_t digit = i + lane < i1 ? kept[i + lane] >> shift : 0u;
+        const bool in = i + lane < i1;
+        g_own += in && digit > top;
+        const unsigned same = __ballot_sync(kAllLanes, in && digit == top);
+        if (same) {
+          const int at = listed + __popc(same & ((1u << lane) - 1));
+          if ((same >> lane & 1u) && at < kListed) mine[at] = kept[i + lane];
+          listed += __popc(same);
+        }
+      }
+      few = !__syncthreads_or(listed > kListed);
+      if (!few) g_own = 0;
+    }
   }
-  // tokens kept of the slices before this one
-  int gt = 0, eq = 0;
-  if (ctas > 1) {
+  // What each run keeps, and what of it equals the m-th largest.
+  if (few) {
+    for (int i = lane; i < listed; i += 32) {
+      g_own += mine[i] > top;
+      e_own += mine[i] == top;
+    }
+  } else {
+#pragma unroll 8
+    for (int i = i0 + lane; i < i1; i += 32) {
+      const uint32_t u = order(i);
+      g_own += u > top;
+      e_own += u == top;
+    }
+  }
+  int above, equal;  // of the slice
+  int gt = block_before(g_own, warps, &above), eq = block_before(e_own, warps, &equal);
+  // (the lanes' counts lie between a warp's first lane and its own)
+  gt = __shfl_sync(kAllLanes, gt, 0);
+  eq = __shfl_sync(kAllLanes, eq, 0);
+  if (ctas > 1) {  // and of the slices before
     if (tid == 0) {
       counts[0] = above;
       counts[1] = equal;
@@ -326,45 +369,98 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_cons
       eq += peer_int(&counts[1], r);
     }
   }
-  // A warp takes a run of rows of 32 places; first what it will keep, then where.
-  const int lane = tid & 31, run = ((n + kThinThreads - 1) / kThinThreads) * 32;
-  const int i0 = min((tid >> 5) * run, n), i1 = min(i0 + run, n);
-  int g_own = 0, e_own = 0;
-#pragma unroll 8
-  for (int i = i0 + lane; i < i1; i += 32) {
-    const uint32_t u = order(i);
-    g_own += u > top;
-    e_own += u == top;
-  }
-  int total;
-  gt += block_before(g_own, warps, &total);
-  eq += block_before(e_own, warps, &total);
-  // (the lanes' counts lie between a warp's first lane and its own)
-  gt = __shfl_sync(kAllLanes, gt, 0);
-  eq = __shfl_sync(kAllLanes, eq, 0);
-  const unsigned below = (1u << lane) - 1;
-#pragma unroll 4
-  for (int i = i0; i < i1; i += 32) {
-    const bool in = i + lane < i1;
-    const uint32_t u = in ? order(i + lane) : 0u;
-    const unsigned larger = __ballot_sync(kAllLanes, in && u > top);
-    const unsigned same = __ballot_sync(kAllLanes, in && u == top);
-    const int e = eq + __popc(same & below);
-    if ((larger >> lane & 1u) || ((same >> lane & 1u) && e < m)) {
-      const int to = q.first + gt + __popc(larger & below) + min(e, m);
-      keep[to] = q.first + lo + i + lane;
-      // (fetched again only where the order does not say: the store would wait for it)
-      out[to] = u == kOrderNan || u == kOrderZero ? __ldg(src + i + lane) : weight_of(u);
+  // Ranks by a scan over the lanes, four places each.  Where all that equals the
+  // m-th largest is kept, which is where no other weight equals it, one comparison
+  // says what stays.
+  if (CACHED && found[2] == m) {
+    gt += eq;
+#pragma unroll 2
+    for (int i = i0; i < i1; i += 128) {
+      const int at = i + 4 * lane, in = i1 - at;  // (there is room behind the last)
+      const uint4 x = *reinterpret_cast<const uint4*>(kept + at);
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+      bool stays[4];
+      int incl = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        stays[k] = u[k] >= top && k < in;
+        incl += stays[k];
+      }
+      int to = -incl;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kAllLanes, incl, o);
+        if (lane >= o) incl += y;
+      }
+      to += q.first + gt + incl;
+      gt += __shfl_sync(kAllLanes, incl, 31);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (stays[k]) {
+          keep[to] = q.first + lo + at + k;
+          out[to] = weight_of(u[k]);
+          // (where the order does not say, it is fetched again)
+          if (u[k] == kOrderNan || u[k] == kOrderZero) out[to] = __ldg(src + at + k);
+          ++to;
+        }
     }
-    gt += __popc(larger);
-    eq += __popc(same);
+    if (ctas > 1) cluster_sync();  // another CTA may still read this one's counts
+    return;
+  }
+#pragma unroll 2
+  for (int i = i0; i < i1; i += 128) {
+    uint32_t u[4];
+    const int at = i + 4 * lane, in = min(4, i1 - at);  // places of this lane
+    if (CACHED) {
+      const uint4 x = *reinterpret_cast<const uint4*>(kept + at);  // (there is room behind the last)
+      u[0] = x.x, u[1] = x.y, u[2] = x.z, u[3] = x.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) u[k] = k < in ? order(at + k) : 0u;
+    }
+    int incl = 0;  // larger ones; equal ones in the high half
+#pragma unroll
+    for (int k = 0; k < 4; ++k) incl += k < in ? (u[k] > top ? 1 : u[k] == top ? 1 << 16 : 0) : 0;
+    const int own = incl;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kAllLanes, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const int all = __shfl_sync(kAllLanes, incl, 31);
+    int g = gt + (incl - own & 0xffff), e = eq + (incl - own >> 16);
+    bool open = false;  // where the order does not say what the weight was
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool larger = k < in && u[k] > top, same = k < in && u[k] == top;
+      if (larger || (same && e < m)) {
+        const int to = q.first + g + min(e, m);
+        keep[to] = q.first + lo + at + k;
+        out[to] = weight_of(u[k]);
+        open |= u[k] == kOrderNan || u[k] == kOrderZero;
+      }
+      g += larger;
+      e += same;
+    }
+    if (__any_sync(kAllLanes, open)) {  // fetched again
+      g = gt + (incl - own & 0xffff), e = eq + (incl - own >> 16);
+#pragma unroll 1
+      for (int k = 0; k < in; ++k) {
+        const bool larger = order(at + k) > top, same = order(at + k) == top;
+        if (larger || (same && e < m)) out[q.first + g + min(e, m)] = __ldg(src + at + k);
+        g += larger;
+        e += same;
+      }
+    }
+    gt += all & 0xffff;
+    eq += all >> 16;
   }
   // another CTA may still read this one's counts
   if (ctas > 1) cluster_sync();
 }
 
-// Weights that a CTA holds in shared memory at most.
-constexpr int kSliceMost = 48 * 1024;
+// Weights that a CTA holds in shared memory at most (beside 41 KB).
+constexpr int kSliceMost = 45 * 1024;
 
 // CTAs of a sequence: as many as the SMs have room for at once, none with fewer
 // than 2048 weights.
@@ -437,7 +533,7 @@ dg_status_t dg_kv_select(dg_kv_t* kv, const dg_kv_select_t* q, dg_stream_t strea
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(q->n_seqs * ctas);
   cfg.blockDim = dim3(kThinThreads);
-  cfg.dynamicSmemBytes = sizeof(float) * p.slice;
+  cfg.dynamicSmemBytes = sizeof(uint32_t) * (p.slice ? round_up(p.slice, 128) : 0);
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -448,7 +544,7 @@ dg_status_t dg_kv_select(dg_kv_t* kv, const dg_kv_select_t* q, dg_stream_t strea
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   cudaError_t e = cudaSuccess;
-  if (cfg.dynamicSmemBytes > 8 * 1024)  // beside 33 KB of static shared memory
+  if (cfg.dynamicSmemBytes > 6 * 1024)  // beside 41 KB of static shared memory
     e = cudaFuncSetAttribute(k_kv_select<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)sizeof(float) * kSliceMost);
   if (e == cudaSuccess)
