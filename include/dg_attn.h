@@ -295,8 +295,9 @@ dg_status_t dg_attn_forward(dg_attn_t* a, int layer, const dg_heads_t* q, const 
 /* The same for sequences of which groups share a prefix (dg_kv_shared):
  * groups and prefix as it has them, for this batch.  The prefix of a group is
  * read once for all of its sequences; results are dg_attn_forward's but for
- * the order of fp32 sums.  Calls with a left limit, or with many rows a
- * sequence, where nothing is gained, take the sequences one by one.  workspace:
+ * the order of fp32 sums.  Calls in which nothing is gained by it take the
+ * sequences one by one: with a left limit, with many rows a sequence, or where the
+ * rows of the page table have room for little altogether (256 MB).  workspace:
  * 1024-byte aligned, for n_tokens tokens at least; calls that share it must not
  * overlap. */
 typedef struct {

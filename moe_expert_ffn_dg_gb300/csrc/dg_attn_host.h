@@ -18,6 +18,7 @@ struct dg_rope {
 struct dg_kv {
   dg_kv_config_t cfg;
   void* status;
+  int sms;  // of the device that it was made on
 };
 
 namespace dg {
@@ -127,8 +128,10 @@ inline Layout layout_of(int head_dim) {
   return L;
 }
 
-// Kernels whose limits a new handle raises on its device (dg_weights.cu).
+// Kernels whose limits a new handle raises on its device (dg_weights.cu,
+// dg_thin.cu).
 cudaError_t prepare_weights(int head_dim);
+cudaError_t prepare_select();
 
 // Clear the status word of a new handle: through the default stream, done when
 // this returns, whatever stream the handle's first call runs on.

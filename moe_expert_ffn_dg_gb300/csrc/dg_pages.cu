@@ -487,12 +487,18 @@ dg_status_t dg_kv_create(const dg_kv_config_t* cfg, void* status, dg_kv_t** out)
   if (!status) return DG_ERR_WORKSPACE;
   if (!aligned(status, 16)) return DG_ERR_WORKSPACE;
   if (!clear_status(status, 256)) return DG_ERR_CUDA;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      prepare_select() != cudaSuccess)
+    return DG_ERR_CUDA;
   dg_kv* kv = new (std::nothrow) dg_kv();
   if (!kv) return DG_ERR_CUDA;
   kv->cfg = c;
   // a size-1 dimension's stride is never used, but a descriptor wants one
   if (c.n_kv_heads == 1) kv->cfg.k.head_stride = kv->cfg.v.head_stride = c.head_dim;
   kv->status = status;
+  kv->sms = sms;
   *out = kv;
   return DG_OK;
 }

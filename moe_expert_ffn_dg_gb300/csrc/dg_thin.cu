@@ -86,7 +86,8 @@ struct SharedParams {
 // prefix = min(page_size * (leading columns in which all rows of the group are
 // equal), fewest tokens that a member had before this call).
 //
-// A block a group.  What is read is little (four bytes a page), so latency
+// A block a group: 2.5 us for 8 sequences, 4 us for 512 of 40 groups, most of it
+// the launch.  What is read is little (four bytes a page), so latency
 // bounds it: a warp takes 128 columns of a member against the first one, the
 // columns of all members before the next ones, and none past the nearest
 // difference found.
@@ -167,7 +168,6 @@ __global__ void __launch_bounds__(kThinThreads) k_kv_shared(const __grid_constan
 
 struct SelectParams {
   dg_kv_select_t s;
-  int slice;  // weights of a CTA that are kept in shared memory, 0: none
   DevStatus* status;
 };
 
@@ -199,8 +199,17 @@ __device__ __forceinline__ int digit_bits(int d) { return d == 2 ? 10 : 11; }
 // of the places, each kept token's rank from a running count.
 //
 // A cluster a sequence (one CTA where rows are short): each CTA takes a slice
-// of the row, keeps it in shared memory, and adds up the others' histograms
-// through distributed shared memory.
+// of the row and keeps its orders in shared memory; the first one's shared memory
+// adds the histograms up.  The weights are read once.
+//
+// Instructions bound it, of the CTAs of the longest row, and the cluster's barriers
+// (two a digit and two more, about 1.5 us a digit): 48 rows of 8000 to 131072 cut to
+// 16384 in 25-27 us, of which 3 go by before the first load, 4 with loading and the
+// first digit, 8 with the other two and 9 with writing; 6.5 us for 8 rows of up to
+// 1500.  Measured and not kept, us for the first: other CTAs' histograms read bin by
+// bin (103, clusters of 8); four copies of a histogram against colliding additions
+// (37, from 27: the hardware adds equal addresses at once); ranks from votes, one
+// place a lane (29).
 template <bool CACHED>
 __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_constant__ SelectParams p) {
   extern __shared__ __align__(16) uint32_t kept[];  // orders of the slice
@@ -470,6 +479,15 @@ int select_ctas(int n_seqs, int width, int sms) {
 
 }  // namespace
 
+namespace dg {
+namespace host {
+cudaError_t prepare_select() {
+  return cudaFuncSetAttribute(k_kv_select<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)sizeof(uint32_t) * kSliceMost);
+}
+}  // namespace host
+}  // namespace dg
+
 extern "C" {
 
 dg_status_t dg_kv_shared(dg_kv_t* kv, const dg_kv_batch_t* batch, const int32_t* groups,
@@ -521,19 +539,14 @@ dg_status_t dg_kv_select(dg_kv_t* kv, const dg_kv_select_t* q, dg_stream_t strea
     if (!aligned(x, 4)) return DG_ERR_ALIGNMENT;
   if (p.s.budget > 0 && q->weights == q->weights_out) return DG_ERR_INVALID_ARG;
   if (q->lens == q->lens_out || q->lens == q->cu) return DG_ERR_INVALID_ARG;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return DG_ERR_CUDA;
-  const int ctas = select_ctas(q->n_seqs, q->width, sms);
+  const int ctas = select_ctas(q->n_seqs, q->width, kv->sms);
   const int slice = (q->width + ctas - 1) / ctas;
   const bool cached = slice <= kSliceMost;
-  p.slice = cached ? slice : 0;
   p.status = static_cast<DevStatus*>(kv->status);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(q->n_seqs * ctas);
   cfg.blockDim = dim3(kThinThreads);
-  cfg.dynamicSmemBytes = sizeof(uint32_t) * (p.slice ? round_up(p.slice, 128) : 0);
+  cfg.dynamicSmemBytes = cached ? sizeof(uint32_t) * round_up(slice, 128) : 0;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -543,12 +556,8 @@ dg_status_t dg_kv_select(dg_kv_t* kv, const dg_kv_select_t* q, dg_stream_t strea
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaSuccess;
-  if (cfg.dynamicSmemBytes > 6 * 1024)  // beside 41 KB of static shared memory
-    e = cudaFuncSetAttribute(k_kv_select<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)sizeof(float) * kSliceMost);
-  if (e == cudaSuccess)
-    e = cudaLaunchKernelEx(&cfg, cached ? k_kv_select<true> : k_kv_select<false>, p);
+  const cudaError_t e =
+      cudaLaunchKernelEx(&cfg, cached ? k_kv_select<true> : k_kv_select<false>, p);
   return e == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 

@@ -16,6 +16,17 @@
 // partial sums in the workspace, joined in a fixed order by k_weights_join: the
 // result does not depend on which CTA comes first.
 //
+// What bounds it, on one GB300: memory for single tokens (64 of them over 471k cached
+// ones, 32 query heads on 8 of 128: 171 us, 6.2 TB/s); shared memory for many rows,
+// of which an MMA of 128 x 128 with both operands there takes all 128 bytes a cycle
+// while query tiles are copied in and log-sums read (4096 tokens behind 12288, same
+// heads: 359 us, 1.34 PFLOP/s; 8 canvases of 256 over 36k, 16 heads on 8 of 256:
+// 69 us).  Measured and not kept, us for the first: the key tiles in tensor memory,
+// whose score tiles then are one fewer and wait for one another (391 to 418); eight
+// warps that add 128 columns each (374); an MMA issuer a key tile (354, but 73 for
+// the canvases); 512 keys an item (455); log-sums fetched by every warp for itself
+// (480); all 64 columns of a warp loaded at once, which spills (566).
+//
 // Warps: eight (few rows) or sixteen for exponentials and sums, then one each for
 // copies of keys, for the MMAs (it owns the tensor memory), for copies of
 // queries and for log-sums.
