@@ -9,12 +9,13 @@
 // query rows (the G heads of a group packed with their tokens, row = token * G +
 // head of the group) are the columns.
 //
-// A work item is 256 keys of a sequence (two tiles of 128) against all of its rows that see them, head after head; its units are single
-// query tiles.  All units of a call lie in one line (sequences, blocks of keys,
-// heads, tiles) and every CTA takes a contiguous range, so that long and short
-// sequences balance alike.  An item that crosses a range boundary leaves fp32
-// partial sums in the workspace, joined in a fixed order by k_weights_join: the
-// result does not depend on which CTA comes first.
+// A work item is 256 keys of a sequence (two tiles of 128) against all of its rows
+// that see them, head after head; its units are single query tiles.  All units of a
+// call lie in one line (sequences, blocks of keys, heads, tiles) and every CTA takes
+// a contiguous range, so that long and short sequences balance alike.  An item that
+// crosses a range boundary leaves fp32 partial sums in the workspace, joined in a
+// fixed order by k_weights_join: the result does not depend on which CTA comes
+// first.
 //
 // What bounds it, on one GB300: memory for single tokens (64 of them over 471k cached
 // ones, 32 query heads on 8 of 128: 171 us, 6.2 TB/s); shared memory for many rows,
@@ -43,7 +44,6 @@ using namespace dg;
 using namespace dg::host;
 
 namespace {
-
 
 // Sites of the device status word.
 enum : unsigned int {
