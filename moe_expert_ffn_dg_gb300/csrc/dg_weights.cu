@@ -672,8 +672,9 @@ __global__ void __launch_bounds__(Cfg<D, QN>::kThreads, 1) k_weights(const __gri
           const int i0 = (g.t0 + t) * p.step;
           const int see0 = p.right < 0 ? 0 : key - p.right - pos;
           const int see1 = key >= g.kv ? 0 : (p.left < 0 ? g.n : key + p.left - pos + 1);
-          const int rl = max(0, see0 - i0) * p.group - cg * NC;
-          const int rh = min(min(p.step, g.n - i0) * p.group, (see1 - i0) * p.group) - cg * NC;
+          // (tokens counted inside the tile first: the products stay small)
+          const int rl = min(max(0, see0 - i0), p.step) * p.group - cg * NC;
+          const int rh = max(0, min(min(p.step, g.n - i0), see1 - i0)) * p.group - cg * NC;
 #pragma unroll
           for (int c = 0; c < NC; c += W) {
             float s[W];

@@ -183,6 +183,16 @@ def test_long_sums_and_offsets():
     run(make([700], [700], 8, 1, 64, 64, BF, 11), -1, -1)
 
 
+@pytest.mark.parametrize("left,right", [(1 << 27, 0), (0, 1 << 27), (1 << 27, 1 << 27)])
+def test_limits_past_every_token(left, right):
+    """Limits that a table of 2^27 places leaves standing, with 32 heads on one:
+    rows times heads pass 32 bits before the tile bounds them."""
+    q, k, v, table, lens, cu = make([3, 1], [300, 40], 64, 2, 64, 256, BF, 17)
+    wide = torch.full((2, (1 << 19) + 8), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    run((q, k, v, wide, lens, cu), left, right)
+
+
 def test_same_result_every_time():
     a = [run(make([70, 1], [3000, 900], 6, 2, 128, 64, BF, 12))[-1].clone() for _ in range(2)]
     assert torch.equal(a[0].nan_to_num(5), a[1].nan_to_num(5))
