@@ -277,6 +277,8 @@ class KvCache(_Handle, _Memory):
         most = min(budget, width)
         if budget < 0 or first < 0 or last < 0 or first + last > budget:
             raise ValueError("budget: at least first + last, none of them negative")
+        if budget >= width:  # all stay; the C call takes 32 bits
+            budget, first, last = width, 0, 0
         if out is None:
             new = lens.new_empty
             out = KvKeep(new(n * most), new(n + 1), new(n), weights.new_empty((n, most)))
@@ -293,7 +295,8 @@ class KvCache(_Handle, _Memory):
                        _ints(out.lens, dev, (n,), "out.lens"),
                        *_weights(out.weights, dev, n, "out.weights"))
         if n == 0:
-            out.cu.zero_()
+            with torch.cuda.stream(stream):  # None: the current one
+                out.cu.zero_()
         B.dg_kv_select(self.handle, B.dg_kv_select_t(
             w, stride, _ints(lens, dev, (n,), "lens"), n, width, budget, first, last, *outputs),
             self._use(stream))

@@ -12,9 +12,11 @@ using namespace dg::host;
 
 namespace {
 
-enum : unsigned int { kSiteSharedLen = 56, kSiteSharedGroups = 57, kSiteSelectLen = 58 };
+enum : unsigned int { kSiteSharedLen = 56, kSiteSharedGroups = 57, kSiteSelectLen = 58,
+                      kSiteSelectWait = 59 };
 
 constexpr int kThinThreads = 1024;
+constexpr int kSelectThreads = 1024;
 constexpr unsigned kAllLanes = 0xffffffffu;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -40,10 +42,17 @@ __device__ __forceinline__ int peer_int(const int* p, uint32_t rank) {
   return v;
 }
 
-__device__ __forceinline__ void peer_add(int* p, uint32_t rank, int v) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+// Add `bytes` of ints to another CTA's, counted on a barrier of that CTA.
+__device__ __forceinline__ void peer_add(const int* to, const int* from, int bytes,
+                                         const uint64_t* bar, uint32_t rank) {
+  uint32_t a, b;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(to)), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(smem_u32(bar)), "r"(rank));
+  asm volatile(
+      "cp.reduce.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes.add.u32"
+      " [%0], [%1], %2, [%3];" ::"r"(a),
+      "r"(smem_u32(from)), "r"(bytes), "r"(b)
+      : "memory");
 }
 
 // Sums over the block; `warps` holds one entry a warp.  Ends with a barrier.
@@ -51,25 +60,34 @@ __device__ __forceinline__ int block_sum(int v, int* warps) {
   v = __reduce_add_sync(kAllLanes, v);
   if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = __reduce_add_sync(kAllLanes, warps[threadIdx.x & 31]);
+  v = __reduce_add_sync(
+      kAllLanes, (threadIdx.x & 31) < blockDim.x >> 5 ? warps[threadIdx.x & 31] : 0);
   __syncthreads();
   return v;
+}
+// Sum over the lanes before this one, and over all.
+__device__ __forceinline__ int lanes_before(int v, int* total) {
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kAllLanes, incl, o);
+    if ((threadIdx.x & 31) >= o) incl += x;
+  }
+  *total = __shfl_sync(kAllLanes, incl, 31);
+  return incl - v;
 }
 // Sum over the threads before this one, and over all.  Ends with a barrier.
 __device__ __forceinline__ int block_before(int v, int* warps, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = v;
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(kAllLanes, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) warps[warp] = incl;
+  int all;
+  const int lanes = lanes_before(v, &all);
+  if (lane == 0) warps[warp] = all;
   __syncthreads();
-  const int w = warps[lane];
+  const int w = lane < blockDim.x >> 5 ? warps[lane] : 0;
   const int before = __reduce_add_sync(kAllLanes, lane < warp ? w : 0);
   *total = __reduce_add_sync(kAllLanes, w);
   __syncthreads();
-  return before + incl - v;
+  return before + lanes;
 }
 
 // ------------------------------------------------------------------ shared
@@ -186,7 +204,8 @@ constexpr uint32_t kOrderNan = 0xffffffffu, kOrderZero = 0x80000000u;
 
 // Digits of the order, from the top: 11, 11 and 10 bits.
 constexpr int kDigits = 3;
-constexpr int kBins = 2048;
+constexpr int kAllBins = 2048 + 2048 + 1024;
+constexpr int kPlaces = 256;  // places of a warp on their way out
 constexpr int kListed = 64;  // orders of a run that are listed at most
 __device__ __forceinline__ int digit_shift(int d) { return d == 0 ? 21 : d == 1 ? 10 : 0; }
 __device__ __forceinline__ int digit_bits(int d) { return d == 2 ? 10 : 11; }
@@ -199,24 +218,30 @@ __device__ __forceinline__ int digit_bits(int d) { return d == 2 ? 10 : 11; }
 // of the places, each kept token's rank from a running count.
 //
 // A cluster a sequence (one CTA where rows are short): each CTA takes a slice
-// of the row and keeps its orders in shared memory; the first one's shared memory
-// adds the histograms up.  The weights are read once.
+// of the row and keeps its orders in shared memory; each adds its histogram to
+// every CTA's, in the fabric between them.  The weights are read once.
 //
-// Instructions bound it, of the CTAs of the longest row, and the cluster's barriers
-// (two a digit and two more, about 1.5 us a digit): 48 rows of 8000 to 131072 cut to
-// 16384 in 25-27 us, of which 3 go by before the first load, 4 with loading and the
-// first digit, 8 with the other two and 9 with writing; 6.5 us for 8 rows of up to
-// 1500.  Measured and not kept, us for the first: other CTAs' histograms read bin by
-// bin (103, clusters of 8); four copies of a histogram against colliding additions
-// (37, from 27: the hardware adds equal addresses at once); ranks from votes, one
-// place a lane (29).
+// Instructions bound it, of the CTAs of the longest row (comparisons and votes go at
+// half the rate or less): 48 rows of 8000 to 131072 cut to 16384 in 21 us, of which
+// 5 go by with loading and the first digit, 4 with listing what has it, 5 with adding
+// up and looking through the three histograms, 2 with counting and 4 with writing;
+// 6.6 us for 8 rows of up to 1500.  Measured and not kept, us for the first: other CTAs' histograms read bin
+// by bin (103, clusters of 8) or added up bin by bin in the first CTA's (26; 92 with
+// clusters of 8); two CTAs an SM of half the size (22 three to a row, 45 eight); four
+// copies of a histogram against colliding additions (37, from 27: the hardware adds
+// equal addresses at once); stores straight from the lanes (24); ranks of four rows of
+// places by one scan instead of votes (22.5).
 template <bool CACHED>
-__global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_constant__ SelectParams p) {
-  extern __shared__ __align__(16) uint32_t kept[];  // orders of the slice
-  __shared__ int hist[kBins], warps[32], found[3], counts[2];
-  __shared__ int sums[kDigits][kBins];  // of the cluster, in its first CTA
+__global__ void __launch_bounds__(kSelectThreads, 1)
+    k_kv_select(const __grid_constant__ SelectParams p) {
+  // histograms of the slice, a digit each (they are sent from here), and its orders
+  extern __shared__ __align__(16) int hists[];
+  uint32_t* kept = reinterpret_cast<uint32_t*>(hists + kAllBins);
+  __shared__ __align__(16) int sums[kAllBins];  // histograms of the cluster
+  __shared__ uint64_t arrived[kDigits];
+  __shared__ int warps[32], found[3], counts[2], abort_word;
   // of each run, the orders with the first digit of the m-th largest
-  __shared__ uint32_t lists[CACHED ? 32 : 1][CACHED ? kListed : 1];
+  __shared__ uint32_t lists[CACHED ? kSelectThreads / 32 : 1][CACHED ? kListed : 1];
   const dg_kv_select_t& q = p.s;
   const int tid = threadIdx.x;
   const int ctas = (int)cluster_ctas(), rank = (int)cluster_rank();
@@ -225,7 +250,7 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_cons
   pdl_wait();
   // kept tokens of the sequences before this one, and of all
   int before = 0, all = 0;
-  for (int s = tid; s < q.n_seqs; s += kThinThreads) {
+  for (int s = tid; s < q.n_seqs; s += kSelectThreads) {
     const int c = min(min(max(__ldg(q.lens + s), 0), q.width), q.budget);
     all += c;
     if (s < seq) before += c;
@@ -242,13 +267,13 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_cons
     if (seq == q.n_seqs - 1) q.cu[q.n_seqs] = all;
   }
   const int64_t room = (int64_t)q.n_seqs * q.budget;
-  for (int64_t i = all + (int64_t)blockIdx.x * kThinThreads + tid; i < room;
-       i += (int64_t)gridDim.x * kThinThreads)
+  for (int64_t i = all + (int64_t)blockIdx.x * kSelectThreads + tid; i < room;
+       i += (int64_t)gridDim.x * kSelectThreads)
     q.keep[i] = -1;
   const float* row = q.weights + seq * q.weights_stride;
   int32_t* keep = q.keep + before;
   float* out = q.weights_out + seq * q.out_stride;
-  const int wide = ctas * kThinThreads, at = rank * kThinThreads + tid;
+  const int wide = ctas * kSelectThreads, at = rank * kSelectThreads + tid;
   for (int i = count + at; i < q.budget; i += wide) out[i] = 0.f;
   if (L <= q.budget) {  // the same for every CTA of the cluster
     for (int i = at; i < L; i += wide) {
@@ -272,13 +297,25 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_cons
   const int lo = min(rank * each, mid), n = min(each, mid - lo);
   const float* src = row + q.first + lo;
   auto order = [&](int i) { return CACHED ? kept[i] : order_of(__ldg(src + i)); };
+  for (int i = tid; i < kAllBins; i += kSelectThreads) hists[i] = sums[i] = 0;
   if (ctas > 1) {
-    for (int i = tid; i < kDigits * kBins; i += kThinThreads) sums[0][i] = 0;
+    if (tid == 0) {
+      abort_word = 0;
+      for (int d = 0; d < kDigits; ++d) mbar_init(&arrived[d], 1);
+      fence_mbar_init();
+      for (int d = 0; d < kDigits; ++d)
+        mbar_arrive_expect_tx(&arrived[d], ctas * (int)sizeof(int) << digit_bits(d));
+    }
+    fence_proxy_async_smem();
     cluster_sync();
   }
+  __syncthreads();
   // A warp takes a run of rows of 128 places.
-  const int lane = tid & 31, warp = tid >> 5, run = (n + 32 * 128 - 1) / (32 * 128) * 128;
-  const int i0 = min(warp * run, n), i1 = min(i0 + run, n);
+  constexpr int kAtOnce = kSelectThreads * 4;
+  const int lane = tid & 31, warp = tid >> 5, run = (n + kAtOnce - 1) / kAtOnce * 128;
+  // (zeros behind the last: no weight's order)
+  const int full = CACHED ? (n + 127) / 128 * 128 : n;
+  const int i0 = min(warp * run, full), i1 = min(i0 + run, full);
   int g_own = 0, e_own = 0;  // of its run: kept for sure, equal to the m-th largest
   bool few = false;          // those with the first digit are listed
   int listed = 0;
@@ -286,11 +323,11 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_cons
   uint32_t top = 0;          // the digits found so far
   for (int d = 0; d < kDigits; ++d) {
     const int shift = digit_shift(d), bits = digit_bits(d);
-    for (int i = tid; i < kBins; i += kThinThreads) hist[i] = 0;
-    __syncthreads();
+    int* hist = hists + (d << 11);
     if (d == 0) {
+      if (CACHED && tid < full - n) kept[n + tid] = 0;
 #pragma unroll 8
-      for (int i = tid; i < n; i += kThinThreads) {
+      for (int i = tid; i < n; i += kSelectThreads) {
         const uint32_t u = order_of(__ldg(src + i));
         if (CACHED) kept[i] = u;
         atomicAdd(&hist[u >> shift], 1);
@@ -302,46 +339,71 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_cons
       }
     } else {
 #pragma unroll 8
-      for (int i = tid; i < n; i += kThinThreads) {
+      for (int i = tid; i < n; i += kSelectThreads) {
         const uint32_t u = order(i);
         if (u >> (shift + bits) == top) atomicAdd(&hist[u >> shift & ((1u << bits) - 1)], 1);
       }
     }
-    __syncthreads();
-    // bins from the largest down, two a thread; all CTAs' in the first one's sums
-    const int b0 = kBins - 1 - 2 * tid, b1 = b0 - 1;
-    const int own0 = hist[b0], own1 = hist[b1];
-    int all0 = own0, all1 = own1;
-    if (ctas > 1) {
-      if (own0) peer_add(&sums[d][b0], 0, own0);
-      if (own1) peer_add(&sums[d][b1], 0, own1);
-      cluster_sync();
-      all0 = peer_int(&sums[d][b0], 0);
-      all1 = peer_int(&sums[d][b1], 0);
+    if (ctas > 1) {  // every CTA's to every CTA
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (tid < ctas)
+        peer_add(sums + (d << 11), hist, (int)sizeof(int) << bits, &arrived[d],
+                 (rank + tid) % ctas);
+      const bool ok = mbar_wait(&arrived[d], 0, &abort_word);
+      if (__syncthreads_or(!ok)) {  // (the copies on their way still land here)
+        if (tid == 0) report(p.status, kDevTimeout, kSiteSelectWait, (unsigned)seq, (unsigned)d);
+        abort_word = 0;
+        for (int e = d; e < kDigits; ++e) mbar_wait(&arrived[e], 0, &abort_word);
+        cluster_sync();
+        cluster_sync();
+        return;
+      }
+      hist = sums + (d << 11);
+    } else {
+      __syncthreads();
     }
+    // bins from the largest down, four a thread
+    const int b0 = (1 << bits) - 1 - 4 * tid;
+    const int4 four =
+        b0 >= 0 ? *reinterpret_cast<const int4*>(hist + b0 - 3) : make_int4(0, 0, 0, 0);
+    const int bin[4] = {four.w, four.z, four.y, four.x};
+    const int here = bin[0] + bin[1] + bin[2] + bin[3];
     int total;
-    const int over = block_before(all0 + all1, warps, &total);
-    if (over < m && over + all0 + all1 >= m) {
-      const bool second = over + all0 < m;
-      found[0] = second ? b1 : b0;
-      found[1] = m - over - (second ? all0 : 0);
-      found[2] = second ? all1 : all0;
+    int over = block_before(here, warps, &total);
+    if (over < m && over + here >= m) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (over < m && over + bin[i] >= m) {
+          found[0] = b0 - i;
+          found[1] = m - over;
+          found[2] = bin[i];
+        }
+        over += bin[i];
+      }
     }
     __syncthreads();
     m = found[1];
     top = top << bits | (uint32_t)found[0];
     __syncthreads();
     if (CACHED && d == 0) {  // list those with this digit, if they are few in every run
-#pragma unroll 8
-      for (int i = i0; i < i1; i += 32) {
-        const uint32_t digit = i + lane < i1 ? kept[i + lane] >> shift : 0u;
-        const bool in = i + lane < i1;
-        g_own += in && digit > top;
-        const unsigned same = __ballot_sync(kAllLanes, in && digit == top);
-        if (same) {
-          const int at = listed + __popc(same & ((1u << lane) - 1));
-          if ((same >> lane & 1u) && at < kListed) mine[at] = kept[i + lane];
-          listed += __popc(same);
+      const uint32_t least = top << shift, most = least | ((1u << shift) - 1);
+      const unsigned before = (1u << lane) - 1;
+      for (int i = i0 + lane; i < i1; i += 128) {
+        uint32_t u[4], row[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          u[k] = kept[i + 32 * k];
+          g_own += u[k] > most;
+          row[k] = __ballot_sync(kAllLanes, u[k] >= least && u[k] <= most);
+        }
+        if (row[0] | row[1] | row[2] | row[3]) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int at = listed + __popc(row[k] & before);
+            if ((row[k] >> lane & 1u) && at < kListed) mine[at] = u[k];
+            listed += __popc(row[k]);
+          }
         }
       }
       few = !__syncthreads_or(listed > kListed);
@@ -378,44 +440,43 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_cons
       eq += peer_int(&counts[1], r);
     }
   }
-  // Ranks by a scan over the lanes, four places each.  Where all that equals the
-  // m-th largest is kept, which is where no other weight equals it, one comparison
-  // says what stays.
+  // Where all that equals the m-th largest is kept, which is where no other weight
+  // equals it, one comparison says what stays, and votes give the ranks.  Places go
+  // through shared memory (the histograms', which nobody reads any more), so that
+  // stores of neighbouring lanes fall together.
   if (CACHED && found[2] == m) {
-    gt += eq;
-#pragma unroll 2
-    for (int i = i0; i < i1; i += 128) {
-      const int at = i + 4 * lane, in = i1 - at;  // (there is room behind the last)
-      const uint4 x = *reinterpret_cast<const uint4*>(kept + at);
-      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-      bool stays[4];
-      int incl = 0;
+    uint16_t* places = reinterpret_cast<uint16_t*>(hists) + warp * kPlaces;
+    const unsigned lanes = (1u << lane) - 1;
+    keep += q.first + gt + eq;
+    out += q.first + gt + eq;
+    int some = 0;
+    for (int i = i0 + lane; i - lane < i1; i += 128) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        stays[k] = u[k] >= top && k < in;
-        incl += stays[k];
+        const bool stays = kept[i + 32 * k] >= top;
+        const unsigned row = __ballot_sync(kAllLanes, stays);
+        if (stays) places[some + __popc(row & lanes)] = (uint16_t)(i + 32 * k);
+        some += __popc(row);
       }
-      int to = -incl;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(kAllLanes, incl, o);
-        if (lane >= o) incl += y;
-      }
-      to += q.first + gt + incl;
-      gt += __shfl_sync(kAllLanes, incl, 31);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (stays[k]) {
-          keep[to] = q.first + lo + at + k;
-          out[to] = weight_of(u[k]);
+      if (some > kPlaces - 128 || i - lane + 128 >= i1) {
+        __syncwarp();
+        for (int t = lane; t < some; t += 32) {
+          const int place = places[t];
+          const uint32_t u = kept[place];
+          keep[t] = q.first + lo + place;
           // (where the order does not say, it is fetched again)
-          if (u[k] == kOrderNan || u[k] == kOrderZero) out[to] = __ldg(src + at + k);
-          ++to;
+          out[t] = u == kOrderNan || u == kOrderZero ? __ldg(src + place) : weight_of(u);
         }
+        __syncwarp();
+        keep += some;
+        out += some;
+        some = 0;
+      }
     }
     if (ctas > 1) cluster_sync();  // another CTA may still read this one's counts
     return;
   }
+  // Ranks by a scan over the lanes, four places each.
 #pragma unroll 2
   for (int i = i0; i < i1; i += 128) {
     uint32_t u[4];
@@ -427,17 +488,11 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_cons
 #pragma unroll
       for (int k = 0; k < 4; ++k) u[k] = k < in ? order(at + k) : 0u;
     }
-    int incl = 0;  // larger ones; equal ones in the high half
+    int all, own = 0;  // larger ones; equal ones in the high half
 #pragma unroll
-    for (int k = 0; k < 4; ++k) incl += k < in ? (u[k] > top ? 1 : u[k] == top ? 1 << 16 : 0) : 0;
-    const int own = incl;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(kAllLanes, incl, o);
-      if (lane >= o) incl += x;
-    }
-    const int all = __shfl_sync(kAllLanes, incl, 31);
-    int g = gt + (incl - own & 0xffff), e = eq + (incl - own >> 16);
+    for (int k = 0; k < 4; ++k) own += k < in ? (u[k] > top ? 1 : u[k] == top ? 1 << 16 : 0) : 0;
+    const int lanes = lanes_before(own, &all);
+    int g = gt + (lanes & 0xffff), e = eq + (lanes >> 16);
     bool open = false;  // where the order does not say what the weight was
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -452,7 +507,7 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_cons
       e += same;
     }
     if (__any_sync(kAllLanes, open)) {  // fetched again
-      g = gt + (incl - own & 0xffff), e = eq + (incl - own >> 16);
+      g = gt + (lanes & 0xffff), e = eq + (lanes >> 16);
 #pragma unroll 1
       for (int k = 0; k < in; ++k) {
         const bool larger = order(at + k) > top, same = order(at + k) == top;
@@ -468,13 +523,17 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_kv_select(const __grid_cons
   if (ctas > 1) cluster_sync();
 }
 
-// Weights that a CTA holds in shared memory at most (beside 41 KB).
-constexpr int kSliceMost = 45 * 1024;
+// Weights that a CTA holds in shared memory at most (beside 49 KB).
+constexpr int kSliceMost = 44 * 1024;
 
-// CTAs of a sequence: as many as the SMs have room for at once, none with fewer
-// than 2048 weights.
+// CTAs of a sequence: so many that each can hold its slice, more where SMs would
+// be left over, none with fewer than 20480 weights (us at the least of 2048 / 8192 /
+// 20480 / 32768: 8 rows of 4096 10.1 / 7.4 / 7.4 / 7.4, of 16384 16.8 / 12.7 / 10.8 /
+// 10.7, of 65536 19.0 / 19.2 / 16.1 / 18.3).  Rows that are not held are read again for
+// every digit: 160 rows of 65536 in 62 us by two CTAs each, two rounds of them, 101 by one.
 int select_ctas(int n_seqs, int width, int sms) {
-  return std::max(1, std::min({8, sms / n_seqs, (width + 2047) / 2048}));
+  const int cached = (width + kSliceMost - 1) / kSliceMost;
+  return std::max(1, std::min({8, std::max(sms / n_seqs, cached), (width + 20479) / 20480}));
 }
 
 }  // namespace
@@ -483,7 +542,7 @@ namespace dg {
 namespace host {
 cudaError_t prepare_select() {
   return cudaFuncSetAttribute(k_kv_select<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)sizeof(uint32_t) * kSliceMost);
+                              (int)sizeof(int) * (kAllBins + kSliceMost));
 }
 }  // namespace host
 }  // namespace dg
@@ -545,8 +604,8 @@ dg_status_t dg_kv_select(dg_kv_t* kv, const dg_kv_select_t* q, dg_stream_t strea
   p.status = static_cast<DevStatus*>(kv->status);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(q->n_seqs * ctas);
-  cfg.blockDim = dim3(kThinThreads);
-  cfg.dynamicSmemBytes = cached ? sizeof(uint32_t) * round_up(slice, 128) : 0;
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = sizeof(int) * (kAllBins + (cached ? round_up(slice, 128) : 0));
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -88,6 +88,18 @@ def test_select_rows_past_shared_memory():
     check_select(w, [300000, 123457], 60000, 10, 1000)
 
 
+@pytest.mark.parametrize("width", [20481, 45100, 61441, 90000, 110001, 131072, 170000, 400000])
+def test_select_rows_of_several_blocks(width):
+    """Two to eight blocks a row; in the last case none holds its slice."""
+    rng = np.random.default_rng(width)
+    w = np.exp(2 * rng.standard_normal((3, width)))
+    w[1] = rng.integers(0, 50, width)  # equal ones on both sides of every border
+    w[2, ::7] = math.nan
+    lens = [width, width - 5, width // 3]
+    check_select(w, lens, width // 9, 10, 100)
+    check_select(w, lens, width // 2)
+
+
 @pytest.mark.parametrize("kind", ["equal", "zeros", "few", "last digit", "nan", "inf", "negative"])
 @pytest.mark.parametrize("width", [900, 20000])
 def test_select_ties_and_special_values(kind, width):
@@ -165,6 +177,20 @@ def test_select_captured_and_on_a_side_stream():
         torch.cuda.synchronize()
         for name in got.__slots__:
             assert torch.equal(getattr(got, name), getattr(want, name)), name
+
+
+def test_select_budgets_past_32_bits_keep_all():
+    w = np.arange(20, dtype=np.float32).reshape(2, 10)
+    for budget, first, last in [(2**31, 0, 0), (2**32 + 3, 1, 1), (2**40, 2**33, 2**39),
+                                (2**63, 0, 2**32 + 1), (11, 6, 5)]:
+        check_select(w, [10, 4], budget, first, last)
+
+
+def test_select_of_no_sequences_on_a_side_stream():
+    cache, side = a_cache(), torch.cuda.Stream()
+    out = cache.select(torch.zeros(0, 8, device="cuda"), i32([]), 4, stream=side)
+    side.synchronize()
+    assert out.cu.tolist() == [0] and out.keep.numel() == out.lens.numel() == 0
 
 
 def test_select_refusals():
