@@ -225,12 +225,12 @@ __device__ __forceinline__ int digit_bits(int d) { return d == 2 ? 10 : 11; }
 // half the rate or less): 48 rows of 8000 to 131072 cut to 16384 in 21 us, of which
 // 5 go by with loading and the first digit, 4 with listing what has it, 5 with adding
 // up and looking through the three histograms, 2 with counting and 4 with writing;
-// 6.6 us for 8 rows of up to 1500.  Measured and not kept, us for the first: other CTAs' histograms read bin
-// by bin (103, clusters of 8) or added up bin by bin in the first CTA's (26; 92 with
-// clusters of 8); two CTAs an SM of half the size (22 three to a row, 45 eight); four
-// copies of a histogram against colliding additions (37, from 27: the hardware adds
-// equal addresses at once); stores straight from the lanes (24); ranks of four rows of
-// places by one scan instead of votes (22.5).
+// 6.6 us for 8 rows of up to 1500.  Measured and not kept, us for the first: other
+// CTAs' histograms read bin by bin (103, clusters of 8) or added up bin by bin in the
+// first CTA's (26; 92 with clusters of 8); two CTAs an SM of half the size (22 three
+// to a row, 45 eight); four copies of a histogram against colliding additions (37,
+// from 27: the hardware adds equal addresses at once); stores straight from the lanes
+// (24); ranks of four rows of places by one scan instead of votes (22.5).
 template <bool CACHED>
 __global__ void __launch_bounds__(kSelectThreads, 1)
     k_kv_select(const __grid_constant__ SelectParams p) {
