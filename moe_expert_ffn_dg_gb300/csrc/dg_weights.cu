@@ -22,15 +22,16 @@
 // of which an MMA of 128 x 128 with both operands there takes all 128 bytes a cycle
 // while query tiles are copied in and log-sums read (4096 tokens behind 12288, same
 // heads: 359 us, 1.34 PFLOP/s; 8 canvases of 256 over 36k, 16 heads on 8 of 256:
-// 69 us).  Measured and not kept, us for the first: the key tiles in tensor memory,
-// whose score tiles then are one fewer and wait for one another (391 to 418); eight
-// warps that add 128 columns each (374); an MMA issuer a key tile (354, but 73 for
-// the canvases); 512 keys an item (455); log-sums fetched by every warp for itself
-// (480); all 64 columns of a warp loaded at once, which spills (566).
+// 86 us, with the wait for a buffer that the two accumulators of that size cost).
+// Measured and not kept, us for the first: the key tiles in tensor memory, whose score
+// tiles then are one fewer and wait for one another (391 to 418); eight warps that add
+// 128 columns each (374); an MMA issuer a key tile (354, but 73 for the canvases, then
+// at 69); 512 keys an item (455); log-sums fetched by every warp for itself (480); all
+// 64 columns of a warp loaded at once, which spills (566).
 //
-// The log-sums are best the attention's own: both kernels' scores come from the same
-// truncating additions, and what those lose (up to 1.7e-6 of a weight at head size
-// 256) falls out of the difference (5e-8 to 1.5e-7 of the exact weight remain).
+// The log-sums are best the attention's own: both kernels' scores come from
+// truncating additions, and what those lose (up to 1e-6 of a weight) mostly falls out
+// of the difference.
 //
 // Warps: eight (few rows) or sixteen for exponentials and sums, then one each for
 // copies of keys, for the MMAs (it owns the tensor memory), for copies of
@@ -87,8 +88,17 @@ struct Cfg {
   static constexpr int kKeyStages = QN == 16 ? (D == 64 ? 12 : 6) : (D == 64 ? 6 : 4);
   static constexpr int kRowStages = QN == 16 ? 6 : (D == 64 ? 7 : 3);
   static constexpr size_t kSmem = (size_t)kKeyStages * kKeyBytes + (size_t)kRowStages * kRowBytes;
-  static constexpr int kBufs = QN == 16 ? 4 : 2;  // score buffers of a key tile
-  static constexpr uint32_t kTmem = 2 * kBufs * QN;
+  // Score buffers of a key tile, and accumulators of each: the tensor core's additions
+  // truncate, and of half the products each they lose less than half as much (head size
+  // 256, 510 tokens over 5700 with a log-sum computed elsewhere: 7.4e-7 of the weights
+  // for 1.5e-6; it leaves no room for a second buffer, 8 canvases 86 us for 70; one key
+  // tile after the other, for both by a part of the query tile at a time: 85).
+  static constexpr int kAccs = D == 256 ? 2 : 1;
+  static constexpr int kBufs = QN == 16 ? 4 : 2 / kAccs;
+  static constexpr uint32_t kTmem = 2 * kBufs * kAccs * QN;
+  // Barriers of a buffer: one for both key tiles, or, where a tile has no second
+  // buffer, one each, so that one tile's products run while the other's are read.
+  static constexpr int kBars = kBufs == 1 ? 2 : 1;
   // Warpgroups that share a key tile's columns.  Two, 64 columns each: with one
   // the latency of the loads and exponentials shows.
   static constexpr int kColGroups = QN == 16 ? 1 : 2;
@@ -292,6 +302,29 @@ struct Cursor {
   }
 };
 
+// The sum of 16 columns each of two accumulators.
+__device__ __forceinline__ void tmem_add16(uint32_t a, uint32_t b, float (&v)[16]) {
+  uint32_t x[16], y[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]),
+        "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]),
+        "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]),
+        "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]),
+        "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3]),
+        "=r"(y[4]), "=r"(y[5]), "=r"(y[6]), "=r"(y[7]),
+        "=r"(y[8]), "=r"(y[9]), "=r"(y[10]), "=r"(y[11]),
+        "=r"(y[12]), "=r"(y[13]), "=r"(y[14]), "=r"(y[15])
+      : "r"(a), "r"(b)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(x[i]) + __uint_as_float(y[i]);
+}
+
 // A sum that carries what its additions round away.
 struct Sum {
   float hi = 0.f, lo = 0.f;
@@ -317,12 +350,13 @@ template <int D, int QN, bool FP16>
 __global__ void __launch_bounds__(Cfg<D, QN>::kThreads, 1) k_weights(const __grid_constant__ WeightParams p) {
   using C = Cfg<D, QN>;
   constexpr int NK = C::kKeyStages, NR = C::kRowStages, NB = C::kBufs, PARTS = C::kParts;
+  constexpr int NA = C::kAccs, KB = C::kBars;
   constexpr int LS = NB + 1;  // query tiles whose log-sums are held
   constexpr int CG = C::kColGroups, W0 = C::kSumWarps;  // W0: first of the other warps
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t keys = smem_u32(smem), rows = keys + NK * C::kKeyBytes;
   __shared__ uint64_t k_full[NK], k_empty[NK], q_full[NR], q_empty[NR];
-  __shared__ uint64_t s_full[NB], s_empty[NB], drain;
+  __shared__ uint64_t s_full[NB * KB], s_empty[NB * KB], drain;
   __shared__ uint64_t x_full[2], x_empty[2];    // sums of a key tile's second column group
   __shared__ float xch[CG == 2 ? kWeightKeys : 1];
   __shared__ __align__(16) float lse[LS][QN];  // -lse log2 e of a query tile
@@ -346,9 +380,9 @@ __global__ void __launch_bounds__(Cfg<D, QN>::kThreads, 1) k_weights(const __gri
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
     }
-    for (int i = 0; i < NB; ++i) {
+    for (int i = 0; i < NB * KB; ++i) {
       mbar_init(&s_full[i], 2);  // the products, and the log-sums
-      mbar_init(&s_empty[i], W0);
+      mbar_init(&s_empty[i], W0 / KB);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&x_full[i], 4);
@@ -516,14 +550,15 @@ __global__ void __launch_bounds__(Cfg<D, QN>::kThreads, 1) k_weights(const __gri
 #pragma unroll
       for (int i = 0; i < NL; ++i) now[i] = ahead[i];
       more = fetch();
-      const bool here = mbar_wait(&s_empty[sc.st], sc.ph ^ 1u, abort_flag);
+      bool here = mbar_wait(&s_empty[sc.st * KB], sc.ph ^ 1u, abort_flag);
+      if (KB == 2) here = here && mbar_wait(&s_empty[sc.st * KB + KB - 1], sc.ph ^ 1u, abort_flag);
       ok = __all_sync(0xffffffffu, here);
       if (!ok) break;
 #pragma unroll
       for (int i = 0; i < NL; ++i)
         if (QN % 32 == 0 || lane < QN) lse[lc.st][lane + 32 * i] = -1.4426950408889634f * now[i];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s_full[sc.st]);
+      if (lane < KB) mbar_arrive(&s_full[sc.st * KB + lane]);
       sc.next();
       lc.next();
     }
@@ -552,21 +587,24 @@ __global__ void __launch_bounds__(Cfg<D, QN>::kThreads, 1) k_weights(const __gri
           const uint32_t idesc =
               idesc_16<FP16>(kKeys, 0, false) | ((uint32_t)((live + 15) & ~15) >> 3 << 17);
           const bool last = t == g.tiles - 1;
-          if (!need(&s_empty[sc.st], sc.ph ^ 1u)) break;
+          if (KB == 1 && !need(&s_empty[sc.st], sc.ph ^ 1u)) break;
           Cursor<NK> k = k0;
           for (int x = 0; x < PARTS && ok; ++x) {
             if (!need(&q_full[qc.st], qc.ph)) break;
             const uint32_t b = row_lo + qc.st * (C::kRowBytes / 16);
             for (int kt = 0; kt < nt; ++kt) {
               if (t == 0 && !need(&k_full[k.st], k.ph)) break;
+              if (KB == 2 && x == 0 && !need(&s_empty[sc.st * KB + kt], sc.ph ^ 1u)) break;
               tc_fence_after();
               const uint32_t a = key_lo + k.st * (C::kKeyBytes / 16);
-              const uint32_t d = tmem + (kt * NB + sc.st) * QN;
+              const uint32_t d = tmem + ((kt * NB + sc.st) * NA + x % NA) * QN;
 #pragma unroll
               for (int i = 0; i < C::kChunks * 4; ++i)
                 umma_ss<false>(d, a + ((i >> 2) * (kKeys * 128) + 32 * (i & 3)) / 16,
-                               b + ((i >> 2) * (QN * 128) + 32 * (i & 3)) / 16, idesc, x | i);
+                               b + ((i >> 2) * (QN * 128) + 32 * (i & 3)) / 16, idesc,
+                               NA == PARTS ? i : x | i);
               issued = true;
+              if (KB == 2 && x == PARTS - 1) umma_commit(&s_full[sc.st * KB + kt]);
               if (last) umma_commit(&k_empty[k.st]);
               k.next();
             }
@@ -575,7 +613,11 @@ __global__ void __launch_bounds__(Cfg<D, QN>::kThreads, 1) k_weights(const __gri
             qc.next();
           }
           if (!ok) break;
-          umma_commit(&s_full[sc.st]);
+          if (KB == 1) umma_commit(&s_full[sc.st]);
+          if (KB == 2 && nt == 1) {  // the second tile's warps go through it all the same
+            if (!need(&s_empty[sc.st * KB + 1], sc.ph ^ 1u)) break;
+            umma_commit(&s_full[sc.st * KB + 1]);
+          }
           sc.next();
           if (last) kc = k;
           ++at;
@@ -595,7 +637,7 @@ __global__ void __launch_bounds__(Cfg<D, QN>::kThreads, 1) k_weights(const __gri
     // ---------------------------------------------------- weights and sums
     constexpr int NC = QN / CG;  // columns of a thread
     const int kt = warp / (4 * CG), cg = (warp >> 2) % CG, quarter = warp & 3;
-    const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16) + kt * NB * QN + cg * NC;
+    const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16) + kt * NB * NA * QN + cg * NC;
     const uint64_t sc2 = f2(p.scale2, p.scale2);
     const int mine = kt * kKeys + quarter * 32 + lane;  // key of the block
     Cursor<NB> sc;
@@ -625,21 +667,25 @@ __global__ void __launch_bounds__(Cfg<D, QN>::kThreads, 1) k_weights(const __gri
       const int full1 = f1 <= 0 ? 0 : (unsigned)f1 / (unsigned)p.step;
       const bool none = key - lane >= g.kv;  // no keys of this warp
       for (int t = 0; t < g.tiles; ++t) {
-        const bool here = mbar_wait(&s_full[sc.st], sc.ph, abort_flag);
+        const int bar = sc.st * KB + (KB == 2 ? kt : 0);
+        const bool here = mbar_wait(&s_full[bar], sc.ph, abort_flag);
         ok = __all_sync(0xffffffffu, here);
         if (!ok) break;
         tc_fence_after();
-        constexpr int W = NC < 32 ? NC : 32;  // columns at a time: 64 would spill
+        // columns at a time: 64 would spill
+        constexpr int W = NC < 32 || NA == 2 ? 16 : 32;
         const float* ls = lse[lc.st] + cg * NC;
         uint64_t acc[4] = {0, 0, 0, 0};
         auto taken = [&] {  // the scores have been read
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[sc.st]);
+          if (lane == 0) mbar_arrive(&s_empty[bar]);
         };
         auto load = [&](int c, float (&s)[W]) {
-          if constexpr (W == 16) tmem_ld16(ts + sc.st * QN, s);
-          else tmem_load32(ts + sc.st * QN + c, s);
+          const uint32_t at = ts + sc.st * NA * QN + c;
+          if constexpr (NA == 2) tmem_add16(at, at + QN, s);
+          else if constexpr (W == 16) tmem_ld16(at, s);
+          else tmem_load32(at, s);
           if (c + W == NC) taken();
         };
         auto weigh = [&](float (&s)[W], int c) {
