@@ -162,7 +162,10 @@ __global__ void __launch_bounds__(kThinThreads) k_kv_shared(const __grid_constan
   const long long tasks = (long long)(b - a - 1) * ((pages + kCols - 1) / kCols);
   for (long long t = warp; t < tasks; t += kThinThreads / 32) {
     const int c0 = (int)(t / (b - a - 1)) * kCols, m = (int)(t % (b - a - 1)) + 1;
-    if (c0 >= *(volatile int*)&least) break;  // later tasks lie no further left
+    // Later tasks lie no further left.  One lane reads for all: the nearest difference
+    // may move meanwhile, and a warp has to leave as one.
+    const int end = __shfl_sync(kAllLanes, lane == 0 ? *(volatile int*)&least : 0, 0);
+    if (c0 >= end) break;
     const int32_t* row = first + m * p.table_stride;
     int x[kCols / 32], y[kCols / 32], at = pages;
 #pragma unroll
