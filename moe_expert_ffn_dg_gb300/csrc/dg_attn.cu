@@ -238,7 +238,8 @@ struct Start {
   int teams;
 };
 
-// Row of the page table of sequence b, and what is wrong with it.
+// Row of the page table of sequence b (of the batch: what a report names), and what
+// is wrong with it.
 __device__ __forceinline__ int table_row(const AttnParams&, int b) { return b; }
 __device__ __forceinline__ void check_seq(const AttnParams& p, int b) {
   const int a = __ldg(p.cu + b), e = __ldg(p.cu + b + 1), kv = __ldg(p.lens + b);
@@ -728,7 +729,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
           if (key < g.khi && ((pg + 1) << p.page_shift) > g.klo) {
             id = __ldg(p.table + (int64_t)table_row(p, g.b) * p.table_stride + pg);
             if ((unsigned)id >= (unsigned)p.n_pages) {
-              report(p.status, kDevBounds, kSiteAttnPage, (unsigned)g.b, (unsigned)id);
+              report(p.status, kDevBounds, kSiteAttnPage, (unsigned)table_row(p, g.b),
+                     (unsigned)id);
               id = p.n_pages;
             }
           }
