@@ -156,22 +156,22 @@ class KvBatch:
                                  _ints(cu, device, (n + 1,), "cu"), n, page_table.shape[1])
 
 
-class KvShared:
+class KvShared(_Memory):
     """What the sequences of a batch's groups have in common (of
     :meth:`KvCache.shared`): prefix int32 [n_seqs], the tokens that lie in the
     same pages in all of a sequence's group.  It holds for the batch's tensors as
-    they were then."""
-
-    __slots__ = ("batch", "groups", "prefix", "c")
+    they were then.  A plan may be dropped while calls with it are under way, on
+    any stream."""
 
     def __init__(self, batch: KvBatch, groups: torch.Tensor, prefix: torch.Tensor):
         if groups.dim() != 1 or groups.shape[0] < 1:
             raise ValueError("groups: [n_groups + 1]")
         self.batch, self.groups, self.prefix = batch, groups, prefix
-        n = groups.shape[0]
+        self.device, n = batch.device, groups.shape[0]
         self.c = B.dg_attn_shared_t(_ints(groups, batch.device, (n,), "groups"),
                                     _ints(prefix, batch.device, (batch.c.n_seqs,), "prefix"),
                                     n - 1, None, 0)
+        self._own(prefix, groups)
 
 
 class KvKeep:
@@ -308,15 +308,16 @@ class KvCache(_Handle, _Memory):
         [n_groups + 1], ascending) have in common, for every group: the tokens
         from the first on that lie in the same pages and that all of them had
         before this call's new ones.  For :meth:`PagedAttention.forward`."""
+        sequences = self._batch(batch)
         if out is None:
             out = KvShared(batch, groups, batch.lens.new_empty(batch.c.n_seqs))
-            if stream is not None:  # allocated on the current one
-                out.prefix.record_stream(stream)
+            out._seen.add(_stream(self.device))  # the one that it was allocated on
         elif out.batch is not batch or out.groups is not groups:
             raise ValueError("out: of this batch and these groups")
-        c = out.c
-        B.dg_kv_shared(self.handle, self._batch(batch), c.groups, c.n_groups, c.prefix,
-                       self._use(stream))
+        c, raw = out.c, self._use(stream)
+        if raw not in out._seen:
+            out._use(stream)
+        B.dg_kv_shared(self.handle, sequences, c.groups, c.n_groups, c.prefix, raw)
         return out
 
     def device_status(self, stream=None):
@@ -444,6 +445,7 @@ class PagedAttention(_Handle, _Memory):
                 raise ValueError(f"{q.shape[0]} tokens with shared prefixes, room for "
                                  f"{self.shared_tokens} (shared_tokens)")
             s = shared.c
+            shared._use(stream)
             B.dg_attn_forward_shared(*args, B.dg_attn_shared_t(
                 s.groups, s.prefix, s.n_groups, self._pre, self._pre_bytes), q.shape[0],
                 self._use(stream))

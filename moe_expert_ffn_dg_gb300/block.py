@@ -36,7 +36,7 @@ def _stream(device, stream=None) -> int:
 class _Memory:
     """Owner of device memory that its calls use, on whatever stream."""
 
-    def _own(self, memory: torch.Tensor):
+    def _own(self, *memory: torch.Tensor):
         self._held, self._seen = memory, set()
 
     def _use(self, stream) -> int:
@@ -45,8 +45,9 @@ class _Memory:
         again, once this object is dropped, only when the calls there are done."""
         raw = _stream(self.device, stream)
         if raw not in self._seen:
-            self._held.record_stream(torch.cuda.current_stream(self.device) if stream is None
-                                     else stream)
+            used = torch.cuda.current_stream(self.device) if stream is None else stream
+            for t in self._held:
+                t.record_stream(used)
             self._seen.add(raw)
         return raw
 
