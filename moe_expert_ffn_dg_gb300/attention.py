@@ -22,12 +22,24 @@ _SCALINGS = {"none": B.DG_ROPE_PLAIN, "linear": B.DG_ROPE_LINEAR, "base": B.DG_R
              "ramp": B.DG_ROPE_RAMP}
 
 
+def _results(make, device, stream=None):
+    """The tensors that make() allocates for a call on `stream`.  They are memory
+    of that stream: what the current one gave back, its earlier work may still
+    use.  The current one is recorded, for the caller goes on with them there."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        out = make()
+    current = torch.cuda.current_stream(device)
+    for t in out:
+        t.record_stream(current)
+    return out
+
+
 def _new(like: torch.Tensor, stream=None) -> torch.Tensor:
     """A contiguous tensor of the same shape for a call on `stream`."""
-    out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    if stream is not None:  # allocated on the current one
-        out.record_stream(stream)
-    return out
+    return _results(lambda: (torch.empty(like.shape, dtype=like.dtype, device=like.device),),
+                    like.device, stream)[0]
 
 
 def _heads(t: torch.Tensor, dtype, device, dim: int, what: str) -> B.dg_heads_t:
@@ -281,10 +293,8 @@ class KvCache(_Handle, _Memory):
             budget, first, last = width, 0, 0
         if out is None:
             new = lens.new_empty
-            out = KvKeep(new(n * most), new(n + 1), new(n), weights.new_empty((n, most)))
-            if stream is not None:  # allocated on the current one
-                for t in (out.keep, out.cu, out.lens, out.weights):
-                    t.record_stream(stream)
+            out = KvKeep(*_results(lambda: (new(n * most), new(n + 1), new(n),
+                                            weights.new_empty((n, most))), dev, stream))
             outputs = (out.keep.data_ptr(), out.cu.data_ptr(), out.lens.data_ptr(),
                        out.weights.data_ptr(), most)
         else:
@@ -310,8 +320,9 @@ class KvCache(_Handle, _Memory):
         before this call's new ones.  For :meth:`PagedAttention.forward`."""
         sequences = self._batch(batch)
         if out is None:
-            out = KvShared(batch, groups, batch.lens.new_empty(batch.c.n_seqs))
-            out._seen.add(_stream(self.device))  # the one that it was allocated on
+            out = KvShared(batch, groups, *_results(
+                lambda: (batch.lens.new_empty(batch.c.n_seqs),), self.device, stream))
+            out._seen.add(_stream(self.device))  # the allocator knows of it
         elif out.batch is not batch or out.groups is not groups:
             raise ValueError("out: of this batch and these groups")
         c, raw = out.c, self._use(stream)
@@ -367,11 +378,8 @@ class KvPager(_Memory):
                   _ints(grow, dev, (n_new,), "grow"))
         if out is None:
             new = lens.new_empty  # cheaper than views of one allocation
-            out = KvFork(new((n_new, row)), new(n_new), new(self.n_pages), new((n_new, 3)),
-                         new(1))
-            if stream is not None:  # allocated on the current one
-                for t in (out.table, out.lens, out.ref, out.copies, out.short):
-                    t.record_stream(stream)
+            out = KvFork(*_results(lambda: (new((n_new, row)), new(n_new), new(self.n_pages),
+                                            new((n_new, 3)), new(1)), dev, stream))
             outputs = (out.table.data_ptr(), out.lens.data_ptr(), out.ref.data_ptr(),
                        out.copies.data_ptr(), out.short.data_ptr())
         else:
