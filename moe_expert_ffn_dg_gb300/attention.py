@@ -14,26 +14,12 @@ import math
 import torch
 
 from . import binding as B
-from .block import _Memory, _settle, _stream
+from .block import _Memory, _results, _settle, _stream
 
 _DTYPES = {torch.bfloat16: B.DG_T_BF16, torch.float16: B.DG_T_FP16, torch.float32: B.DG_T_FP32}
 _LAYOUTS = {"half": B.DG_ROPE_HALF, "interleaved": B.DG_ROPE_INTERLEAVED}
 _SCALINGS = {"none": B.DG_ROPE_PLAIN, "linear": B.DG_ROPE_LINEAR, "base": B.DG_ROPE_BASE,
              "ramp": B.DG_ROPE_RAMP}
-
-
-def _results(make, device, stream=None):
-    """The tensors that make() allocates for a call on `stream`.  They are memory
-    of that stream: what the current one gave back, its earlier work may still
-    use.  The current one is recorded, for the caller goes on with them there."""
-    if stream is None:
-        return make()
-    with torch.cuda.stream(stream):
-        out = make()
-    current = torch.cuda.current_stream(device)
-    for t in out:
-        t.record_stream(current)
-    return out
 
 
 def _new(like: torch.Tensor, stream=None) -> torch.Tensor:

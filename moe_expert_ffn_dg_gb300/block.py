@@ -33,6 +33,26 @@ def _stream(device, stream=None) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _results(make, device, stream=None):
+    """The tensors (a sequence or a dict) that make() allocates for a call on
+    `stream`.  They are memory of that stream: what the current one gave back, its
+    earlier work may still use.  The current one is recorded, for the caller goes
+    on with them there."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        out = make()
+    current = torch.cuda.current_stream(device)
+    for t in out.values() if isinstance(out, dict) else out:
+        t.record_stream(current)
+    return out
+
+
+def _like(x: torch.Tensor, stream=None) -> torch.Tensor:
+    """A tensor like x for a call on `stream`."""
+    return _results(lambda: (torch.empty_like(x),), x.device, stream)[0]
+
+
 class _Memory:
     """Owner of device memory that its calls use, on whatever stream."""
 
@@ -176,12 +196,12 @@ class MoEBlock(_Memory):
         assert h.dtype == torch.bfloat16 and h.is_contiguous() and h.shape[1] == self.hidden
         T = h.shape[0]
         if out is None:
-            out = torch.empty_like(h)
+            out = _like(h, stream)
         dbg = None
         tensors = None
         if debug:
             dev, K, H, E = self.device, self.top_k, self.hidden, self.n_experts
-            tensors = {
+            tensors = _results(lambda: {
                 "idx": torch.empty(T, K, dtype=torch.int32, device=dev),
                 "w": torch.empty(T, K, dtype=torch.float32, device=dev),
                 "logits": torch.empty(T, E, dtype=torch.float32, device=dev),
@@ -192,7 +212,7 @@ class MoEBlock(_Memory):
                 "y_moe": torch.empty(T, H, dtype=torch.float32, device=dev),
                 "y_dense": torch.empty(T, H, dtype=torch.float32, device=dev),
                 "n_refined": torch.zeros(1, dtype=torch.int32, device=dev),
-            }
+            }, dev, stream)
             dbg = B.dg_moe_debug_t(*[tensors[k].data_ptr() for k in (
                 "idx", "w", "logits", "offsets", "perm", "xd", "xe_perm", "y_moe", "y_dense",
                 "n_refined")])
@@ -214,9 +234,9 @@ class MoEBlock(_Memory):
         assert x.shape == attn_out.shape
         T = x.shape[0]
         if out is None:
-            out = torch.empty_like(x)
+            out = _like(x, stream)
         if w_next_in is not None and next_in is None:
-            next_in = torch.empty_like(x)
+            next_in = _like(x, stream)
         nb = B.dg_moe_neighbours_t(attn_out.data_ptr(), w_post_attn.data_ptr(),
                                    w_next_in.data_ptr() if w_next_in is not None else None,
                                    next_in.data_ptr() if w_next_in is not None else None,
@@ -290,7 +310,7 @@ class ScMlp(_Memory):
             assert t.dtype == torch.bfloat16 and t.is_contiguous() and t.shape[1] == self.hidden
         assert embeds.shape == signal.shape
         if out is None:
-            out = torch.empty_like(embeds)
+            out = _like(embeds, stream)
         B.dg_sc_mlp_forward(self.handle, embeds.data_ptr(), signal.data_ptr(), out.data_ptr(),
                             embeds.shape[0], self._use(stream))
         return out
