@@ -1740,6 +1740,9 @@ dg_status_t dg_attn_forward_shared(dg_attn_t* a, int layer, const dg_heads_t* q,
   // costs more than reading a prefix again, mostly from the L2 (2 to 32 sequences,
   // one token each, us one by one / together: at 140 to 170 MB 24 / 29, 24 / 34, 44 /
   // 47; at 270 to 300 MB 65 / 47, 34 / 31, 30 / 32; at 550 to 600 MB 60 / 55, 48 / 35).
+  // It is the table's room that the host knows, not the lengths: short sequences in a
+  // wide table go together all the same (4 behind 2000 tokens, room for 131072 each: 23
+  // together, 13 one by one).
   const int64_t held = (int64_t)batch->n_seqs * batch->max_pages * c.page_size * c.n_kv_heads *
                        c.head_dim * 4;
   if (shared->n_groups == 0 || a->cfg.left >= 0 || rows > kMaxSharedRows ||
@@ -1764,7 +1767,8 @@ dg_status_t dg_attn_forward_shared(dg_attn_t* a, int layer, const dg_heads_t* q,
   // A prefix's items are split into many parts, and parts of few rows cost less to
   // write and join (behind 16384 tokens, us few / many: head size 64 39.6 / 40.4 at
   // 256 rows, 58.6 / 56.3 at 512; 128: 45.7 / 51.8, 69.7 / 75.4, at 2048 rows behind
-  // 65536 643 / 392; 256: 58.8 / 66.8 at 128, 78.2 / 73.6 at 192).
+  // 65536 643 / 392; 256: 58.8 / 66.8 at 128, 78.2 / 73.6 at 192).  By the average of
+  // the groups, those without a fork counted too.
   PrefixParams prefix;
   const int64_t prefix_rows = (int64_t)n_tokens * group / shared->n_groups;
   st = set_up(a, layer, q, out, lse, batch, n_tokens,

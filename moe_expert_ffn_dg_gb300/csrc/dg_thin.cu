@@ -104,11 +104,11 @@ struct SharedParams {
 // prefix = min(page_size * (leading columns in which all rows of the group are
 // equal), fewest tokens that a member had before this call).
 //
-// A block a group: 2.5 us for 8 sequences, 4 us for 512 of 40 groups, most of it
-// the launch.  What is read is little (four bytes a page), so latency
-// bounds it: a warp takes 128 columns of a member against the first one, the
-// columns of all members before the next ones, and none past the nearest
-// difference found.
+// A block a group: 2.4 us for 8 sequences, 3.6 us for 512 of 40 groups (in a replayed
+// graph, 2070 MHz; 11 to 17 for a call from Python), most of it the launch.  What is
+// read is little (four bytes a page), so latency bounds it: a warp takes 128 columns
+// of a member against the first one, the columns of all members before the next ones,
+// and none past the nearest difference found.
 __global__ void __launch_bounds__(kThinThreads) k_kv_shared(const __grid_constant__ SharedParams p) {
   __shared__ int least, bad;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -225,15 +225,17 @@ __device__ __forceinline__ int digit_bits(int d) { return d == 2 ? 10 : 11; }
 // every CTA's, in the fabric between them.  The weights are read once.
 //
 // Instructions bound it, of the CTAs of the longest row (comparisons and votes go at
-// half the rate or less): 48 rows of 8000 to 131072 cut to 16384 in 21 us, of which
-// 5 go by with loading and the first digit, 4 with listing what has it, 5 with adding
-// up and looking through the three histograms, 2 with counting and 4 with writing;
-// 6.6 us for 8 rows of up to 1500.  Measured and not kept, us for the first: other
-// CTAs' histograms read bin by bin (103, clusters of 8) or added up bin by bin in the
-// first CTA's (26; 92 with clusters of 8); two CTAs an SM of half the size (22 three
-// to a row, 45 eight); four copies of a histogram against colliding additions (37,
-// from 27: the hardware adds equal addresses at once); stores straight from the lanes
-// (24); ranks of four rows of places by one scan instead of votes (22.5).
+// half the rate or less): 48 rows of 8000 to 131072 cut to 16384 in 21 us (in a
+// replayed graph, 2070 MHz; 21 to 28 for a call from Python), of which 5 go by with
+// loading and the first digit, 4 with listing what has it, 5 with adding up and looking
+// through the three histograms, 2 with counting and 4 with writing; 8 rows of up to
+// 1500 in 6.5 us (a call 17 to 27, 8 where its outputs are given).  Measured and not
+// kept, us for the first: other CTAs' histograms read bin by bin (103, clusters of 8) or
+// added up bin by bin in the first CTA's (26; 92 with clusters of 8); two CTAs an SM of
+// half the size (22 three to a row, 45 eight); four copies of a histogram against
+// colliding additions (37, from 27: the hardware adds equal addresses at once); stores
+// straight from the lanes (24); ranks of four rows of places by one scan instead of
+// votes (22.5).
 template <bool CACHED>
 __global__ void __launch_bounds__(kSelectThreads, 1)
     k_kv_select(const __grid_constant__ SelectParams p) {

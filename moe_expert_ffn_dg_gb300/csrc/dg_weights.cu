@@ -17,21 +17,31 @@
 // fixed order by k_weights_join: the result does not depend on which CTA comes
 // first.
 //
-// What bounds it, on one GB300: memory for single tokens (64 of them over 471k cached
-// ones, 32 query heads on 8 of 128: 171 us, 6.2 TB/s); shared memory for many rows,
-// of which an MMA of 128 x 128 with both operands there takes all 128 bytes a cycle
-// while query tiles are copied in and log-sums read (4096 tokens behind 12288, same
-// heads: 359 us, 1.34 PFLOP/s; 8 canvases of 256 over 36k, 16 heads on 8 of 256:
-// 86 us, with the wait for a buffer that the two accumulators of that size cost).
-// Measured and not kept, us for the first: the key tiles in tensor memory, whose score
-// tiles then are one fewer and wait for one another (391 to 418); eight warps that add
-// 128 columns each (374); an MMA issuer a key tile (354, but 73 for the canvases, then
-// at 69); 512 keys an item (455); log-sums fetched by every warp for itself (480); all
-// 64 columns of a warp loaded at once, which spills (566).
+// What bounds it, on one GB300 (us of a call in a replayed graph, in brackets of calls
+// from Python whose inputs change): memory for single tokens (64 of them over 471k
+// cached ones, 32 query heads on 8 of 128: 172 us [173 to 179], 6.2 TB/s); shared
+// memory for many rows, of which an MMA of 128 x 128 with both operands there takes
+// all 128 bytes a cycle while query tiles are copied in and log-sums read (4096 tokens
+// behind 12288, same heads: 374 us at 1995 MHz [368 to 413, by the clock under the
+// power limit], 1.17 to 1.31 PFLOP/s; 8 canvases of 256 over 36k, 16 heads on 8 of
+// 256: 89 us [91 to 93], with the wait for a buffer that the two accumulators of that
+// size cost).  Heads of a group that do not divide a tile leave columns without a row,
+// so that all of its tiles are masked: the same 4096 with 3, 5 and 7 query heads on
+// each of 8 in 498, 824 and 1141 us, 0.73 PFLOP/s (2, 4 and 8: 193, 368 and 747).
+// Measured and not kept, us for the 4096 when they took 359: the key tiles in tensor
+// memory, whose score tiles then are one fewer and wait for one another (391 to 418);
+// eight warps that add 128 columns each (374); an MMA issuer a key tile (354, but 73
+// for the canvases, then at 69); 512 keys an item (455); log-sums fetched by every warp
+// for itself (480); all 64 columns of a warp loaded at once, which spills (566).
 //
-// The log-sums are best the attention's own: both kernels' scores come from
-// truncating additions, and what those lose (up to 1e-6 of a weight) mostly falls out
-// of the difference.
+// How exact it is: an addition of the tensor core truncates, and loses less than 2^-23
+// of the partial sum, so that a weight is off by a factor that grows with the scores:
+// at most 2^-23 scale times the sizes of all partial sums, and 2^-24 |lse| for the
+// scaled log-sum's rounding.  Root mean square for 512 rows of queries three times
+// normal over 1500 normal keys, bf16 and fp16: at head sizes 64 and 128 6e-7 to 1.2e-6
+// of the weights with log-sums from 64 bits, 3e-7 to 4e-7 with the attention's own,
+// whose scores lose the same; at 256, where the attention has one accumulator and this
+// kernel two, 1.0e-6 to 1.5e-6 with either.
 //
 // Warps: eight (few rows) or sixteen for exponentials and sums, then one each for
 // copies of keys, for the MMAs (it owns the tensor memory), for copies of
@@ -90,9 +100,10 @@ struct Cfg {
   static constexpr size_t kSmem = (size_t)kKeyStages * kKeyBytes + (size_t)kRowStages * kRowBytes;
   // Score buffers of a key tile, and accumulators of each: the tensor core's additions
   // truncate, and of half the products each they lose less than half as much (head size
-  // 256, 510 tokens over 5700 with a log-sum computed elsewhere: 7.4e-7 of the weights
-  // for 1.5e-6; it leaves no room for a second buffer, 8 canvases 86 us for 70; one key
-  // tile after the other, for both by a part of the query tile at a time: 85).
+  // 256, with log-sums from 64 bits: 1.0e-6 to 1.5e-6 of the weights for 2.1e-6 to
+  // 2.9e-6; with those of the attention, which has one accumulator, 1.1e-6 to 1.4e-6 for
+  // 5e-7 to 6e-7).  It leaves no room for a second buffer: 8 canvases 92 us for 77; one
+  // key tile after the other, for both by a part of the query tile at a time: as long.
   static constexpr int kAccs = D == 256 ? 2 : 1;
   static constexpr int kBufs = QN == 16 ? 4 : 2 / kAccs;
   static constexpr uint32_t kTmem = 2 * kBufs * kAccs * QN;
@@ -705,7 +716,8 @@ __global__ void __launch_bounds__(Cfg<D, QN>::kThreads, 1) k_weights(const __gri
           for (int e = 0; e < W; e += 2)
             acc[e / 2 & 3] = add2(acc[e / 2 & 3], f2(s[e], s[e + 1]));
         };
-        // two loops: the mask must not cost where every row sees every key
+        // two loops: the mask must not cost where every row sees every key (and every
+        // column is a row: step * group == QN above)
         if (none) {
           taken();
         } else if (t >= full0 && t < full1) {
@@ -872,6 +884,8 @@ extern "C" dg_status_t dg_attn_weights(dg_attn_t* a, int layer, const dg_heads_t
   }
   const int group = a->cfg.n_q_heads / c.n_kv_heads;
   WeightParams p;
+  // Few rows or many, by the average: a long chunk among single tokens is taken by the
+  // narrow tiles too (256 single tokens 108 us, 512 behind 4096 26, both in one call 202).
   const int64_t rows = (int64_t)n_tokens * group / batch->n_seqs;
   const bool few = group <= 16 && rows <= 16;
   p.step = (few ? 16 : kRows) / group;
