@@ -747,8 +747,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn(const __grid_constan
             const int st = (rp + h) % NS;
             if (!acquire(&empty[st], ((uint32_t)((rp + h) / NS) & 1u) ^ 1u)) break;
             const int key0 = key_t + (keys ? rank * (SH - 1) * KROWS : h * tokens);
-            auto live_from = [&](int key) {  // tokens of a stage from `key` on that are fetched
-              return max(0, min(tokens, (g.khi - key + piece - 1) & -piece));
+            // Tokens of a stage from `key` on that are fetched.  Of a pair both CTAs copy
+            // something of every stage (zeros, where no key is seen): one that could be
+            // filled, used and given back without the second CTA's producer might pass
+            // twice the phase that it waits for, which then looks like none.
+            auto live_from = [&](int key) {
+              return max(PAIR ? piece : 0, min(tokens, (g.khi - key + piece - 1) & -piece));
             };
             const int live = live_from(key0);
             // Pair: counted in the first CTA, both shares together; but values
